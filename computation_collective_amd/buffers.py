@@ -397,3 +397,112 @@ class A2aGemm(_Common):
 
     def run(self, stream=None, **kw):
         hocf.check(self.call(stream, **kw))
+
+
+def torch_dt(t: torch.Tensor) -> int:
+    """The library's type of a tensor (bf16 as torch.bfloat16 or as its bit patterns)."""
+    if t.dtype in (torch.bfloat16, torch.int16):
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise TypeError(f"{t.dtype}: the library takes fp32 and bf16")
+
+
+def _on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _dense(dtype, shape, **tensors):
+    """Raises unless every tensor given has this dtype and shape, dense and row-major."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+
+
+class _Moe(_Common):
+    """What the mixture-of-experts operators share: inputs are torch tensors, used
+    where they are (no copy); a call goes to the current stream of their device
+    unless it is given one."""
+
+    def _bind(self, device, ws_bytes=0):
+        self.device = device
+        self._alloc_sync(ws_bytes, device)
+        self._sync = self.next_sync()
+
+    def _args(self, stream):
+        """The call's sync block (one per handle, read during the call) and stream."""
+        self.epoch = (self.epoch % 0xFFFFFFF0) + 1
+        self._sync.epoch = self.epoch
+        return self._sync, torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def run(self, stream=None):
+        hocf.check(self.call(stream))
+
+
+def _rows_ld(logits, T, E):
+    """Row stride of the logits: [T][E], the experts of a row adjacent."""
+    if tuple(logits.shape) != (T, E):
+        raise ValueError(f"logits have shape {tuple(logits.shape)}, not {(T, E)}")
+    if E > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a row are not adjacent")
+    return max(logits.stride(0), E) if T > 1 else E
+
+
+class MoeRoute(_Moe):
+    """hocf_moe_route: logits [T][E] (rows may be apart) -> experts [T][topk], weights
+    [T][topk] and, with counts=True, the tokens of each expert [E]."""
+
+    def __init__(self, T, E, topk, logits, bias=None, score=hocf.HOCF_SCORE_SOFTMAX, n_group=1, topk_group=1,
+                 group_top=1, renorm=False, scale=1.0, counts=False):
+        ld = _rows_ld(logits, T, E)
+        _dense(torch.float32, (E,), bias=bias)
+        _on(logits.device, bias=bias)
+        self.logits, self.bias = logits, bias
+        self.experts = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+        self.weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+        self.counts = torch.empty(E, dtype=torch.int32, device=logits.device) if counts else None
+        self._a = (T, E, topk, torch_dt(logits), logits.data_ptr(), ld, hocf.ptr(bias), score, n_group, topk_group,
+                   group_top, int(renorm), scale, self.experts.data_ptr(), self.weights.data_ptr(),
+                   hocf.ptr(self.counts))
+        self._bind(logits.device, hocf.hocf_moe_route_workspace_bytes(E) if counts else 0)
+
+    def poison(self):
+        self.experts.fill_(-77)
+        nan_fill(self.weights)
+        if self.counts is not None:
+            self.counts.fill_(-77)
+
+    def call(self, stream=None) -> int:
+        s, stream = self._args(stream)
+        return hocf.hocf_moe_route(*self._a, s, stream)
+
+
+class MoeRouteBwd(_Moe):
+    """hocf_moe_route_bwd: logits [T][E], the chosen experts [T][topk] and the gradients
+    of their weights -> dlogits [T][E]."""
+
+    def __init__(self, T, E, topk, logits, experts, dweights, score=hocf.HOCF_SCORE_SOFTMAX, renorm=False, scale=1.0):
+        ld = _rows_ld(logits, T, E)
+        _dense(torch.int32, (T, topk), experts=experts)
+        _dense(torch.float32, (T, topk), dweights=dweights)
+        _on(logits.device, experts=experts, dweights=dweights)
+        self.logits, self.experts, self.dweights = logits, experts, dweights
+        self.dlogits = torch.empty((T, E), dtype=tdtype(torch_dt(logits)), device=logits.device)
+        self._a = (T, E, topk, torch_dt(logits), logits.data_ptr(), ld, experts.data_ptr(), dweights.data_ptr(), score,
+                   int(renorm), scale, self.dlogits.data_ptr())
+        self._bind(logits.device)
+
+    def poison(self):
+        nan_fill(self.dlogits)
+
+    def call(self, stream=None) -> int:
+        s, stream = self._args(stream)
+        return hocf.hocf_moe_route_bwd(*self._a, s, stream)

@@ -39,6 +39,7 @@ EXPORTED = [
     "hocf_gemm_a2a", "hocf_gemm_a2a_workspace_bytes",
     "hocf_a2a_gemm", "hocf_a2a_gemm_unfused", "hocf_a2a_gemm_workspace_bytes",
     "hocf_dma_put",
+    "hocf_moe_route", "hocf_moe_route_workspace_bytes", "hocf_moe_route_bwd",
     "hocf_status_string", "hocf_last_error", "hocf_abi_version",
 ]
 
@@ -116,6 +117,14 @@ def lib():
         PV = ctypes.POINTER(vp)
         L.hocf_dma_put.argtypes = [i, PV, PV, ctypes.POINTER(i64), PV, vp, i, vp]
         L.hocf_dma_put.restype = i
+        f32 = ctypes.c_float
+        L.hocf_moe_route.argtypes = [i64, i, i, i, vp, i64, vp, i, i, i, i, i, f32, vp, vp, vp, S, vp]
+        L.hocf_moe_route_workspace_bytes.argtypes = [i]
+        L.hocf_moe_route_bwd.argtypes = [i64, i, i, i, vp, i64, vp, vp, i, i, f32, vp, S, vp]
+        for f in ("hocf_moe_route", "hocf_moe_route_bwd"):
+            getattr(L, f).restype = i
+        for f in ("hocf_moe_route_workspace_bytes",):
+            getattr(L, f).restype = sz
         L.hocf_status_string.argtypes = [i]
         L.hocf_status_string.restype = ctypes.c_char_p
         L.hocf_last_error.argtypes = []
@@ -295,6 +304,27 @@ def hocf_a2a_gemm(P, E, e0, B, topk, N, K, in_dt, out_dt, X, experts, W, cap, re
     return fn(P, E, e0, B, topk, N, K, in_dt, out_dt, ptr(X), ptr(experts), ptr(W), cap, ptr(recv), ptr(Y),
               ptr(expert_offsets), ptr(dest), ptr(slot), ptr(send_counts), tile_m, tile_n, ctypes.byref(sync_),
               _stream(stream))
+
+
+HOCF_SCORE_SOFTMAX, HOCF_SCORE_SIGMOID = 0, 1
+
+
+def hocf_moe_route_workspace_bytes(E) -> int:
+    return lib().hocf_moe_route_workspace_bytes(E)
+
+
+def hocf_moe_route(T, E, topk, dt, logits, ld, bias, score, n_group, topk_group, group_top, renorm, scale, experts,
+                   weights, counts, sync_, stream=None) -> int:
+    """Router logits -> experts and weights of every token; every array a device buffer."""
+    return lib().hocf_moe_route(T, E, topk, dt, ptr(logits), ld, ptr(bias), score, n_group, topk_group, group_top,
+                                renorm, scale, ptr(experts), ptr(weights), ptr(counts), ctypes.byref(sync_),
+                                _stream(stream))
+
+
+def hocf_moe_route_bwd(T, E, topk, dt, logits, ld, experts, dweights, score, renorm, scale, dlogits, sync_,
+                       stream=None) -> int:
+    return lib().hocf_moe_route_bwd(T, E, topk, dt, ptr(logits), ld, ptr(experts), ptr(dweights), score, renorm,
+                                    scale, ptr(dlogits), ctypes.byref(sync_), _stream(stream))
 
 
 def _host_i64(a):

@@ -32,6 +32,13 @@
  *                    ("HOCCL: Offloading Collective Communication from GPU
  *                    Cores to Accelerate Distributed Training", abstract)
  *
+ * and, around the MoE pair, what a mixture-of-experts layer does before the
+ * dispatch, after the combine and in a decode step:
+ *
+ *   hocf_moe_route, hocf_moe_route_bwd
+ *                    router logits -> experts and weights of every token, and
+ *                    the gradient of the logits
+ *
  * The method (SC24 abstract; mKernel, section on persistent kernels and
  * tile/chunk overlap): the workgroups of one kernel each finish an output
  * tile and immediately publish it to its destination's receive window with
@@ -518,6 +525,59 @@ typedef enum hocf_engine HOCF_ENUM_INT { HOCF_ENGINE_DMA = 0, HOCF_ENGINE_CU = 1
 hocf_status hocf_dma_put(int n, const void* const* src, void* const* dst, const int64_t* bytes,
                          uint32_t* const* signal, const uint32_t* signal_value, hocf_engine engine,
                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * Routing to experts.
+ *
+ * For each of T tokens with router logits x (E of them):
+ *   s_e = softmax(x)_e, or sigmoid(x_e)            (score)
+ *   v_e = s_e + bias_e                             (the bias takes part in the choice only)
+ *   with n_group > 1: the experts form n_group runs of E / n_group; a group's
+ *         value is the sum of its group_top largest v (of all it has, if
+ *         fewer); the topk_group groups of largest value stay, the other
+ *         groups' experts are out
+ *   the topk experts of largest v among those left, in falling order of v
+ *   w_j = scale * s_{e_j}, divided by the sum of the chosen s when renorm
+ * Equal values rank by the lower index, among groups and among experts.  A
+ * logit of -inf or NaN switches its expert off for that token; a token with
+ * fewer than topk experts left gets expert -1 and weight 0 in the last
+ * places.  Logits of +inf share a softmax among themselves.  A bias must be
+ * finite (an expert whose v is NaN or -inf is never chosen).
+ *
+ *   logits   [T][ld] dt, the first E of each row (E <= ld <= 2^24)
+ *   bias     NULL or [E] fp32
+ *   experts  [T][topk] int32      weights [T][topk] fp32
+ *   counts   NULL or [E] int32: tokens that chose each expert
+ *
+ * The choice is the one that arithmetic in 64 bits makes.
+ * Supported: dt F32 or BF16; 1 <= E <= 512; 1 <= topk <= min(16, E); n_group
+ * <= 64 dividing E; group_top 1 or 2.  0 <= T < 2^31.
+ * ---------------------------------------------------------------------- */
+typedef enum hocf_score HOCF_ENUM_INT { HOCF_SCORE_SOFTMAX = 0, HOCF_SCORE_SIGMOID = 1 } hocf_score;
+hocf_status hocf_moe_route(int64_t T, int E, int topk, hocf_dtype dt, const void* logits, int64_t ld,
+                           const float* bias, hocf_score score, int n_group, int topk_group, int group_top,
+                           int renorm, float scale, int32_t* experts, float* weights, int32_t* counts,
+                           const hocf_sync* sync, void* stream);
+size_t hocf_moe_route_workspace_bytes(int E);
+
+/* ------------------------------------------------------------------------
+ * Routing to experts, backward: the gradient of the logits.
+ *
+ * With the experts that hocf_moe_route chose (constants) and the gradients of
+ * their weights: dlogits_e = sum_j dweights_j * dw_j / dx_e, over the whole
+ * row for a softmax without renorm, at the chosen experts only (zero
+ * elsewhere) for a sigmoid or with renorm.  A place of -1 has no gradient; a
+ * switched-off logit gets 0.  A place that names no expert of the row
+ * (neither -1 nor in [0, E)) is skipped and HOCF_ERR_BAD_INDEX goes to the
+ * status word.
+ *
+ *   logits [T][ld] dt    experts [T][topk] int32    dweights [T][topk] fp32
+ *   dlogits [T][E] dt
+ * Supported: as for hocf_moe_route.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_moe_route_bwd(int64_t T, int E, int topk, hocf_dtype dt, const void* logits, int64_t ld,
+                               const int32_t* experts, const float* dweights, hocf_score score, int renorm,
+                               float scale, void* dlogits, const hocf_sync* sync, void* stream);
 
 /* ---------------------------------------------------------------------- */
 const char* hocf_status_string(hocf_status s); /* static string, never NULL */

@@ -1,0 +1,225 @@
+"""The mixture-of-experts operators on the GPU against plain 64-bit
+implementations (moe_ref.py), at the sizes and masks where they can go wrong.
+
+Choices, slots and counts are equal.  Computed values: half a step of the
+output's type relative to the value, plus a stated number of binary32 half
+steps (2^-24) relative to the sum of the magnitudes that the value is a sum
+of.  Outputs are poisoned first, so an element that is not written shows."""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_ref as ref
+from computation_collective_amd import buffers as bf
+from computation_collective_amd import hocf
+
+pytestmark = pytest.mark.gpu
+SOFTMAX, SIGMOID = hocf.HOCF_SCORE_SOFTMAX, hocf.HOCF_SCORE_SIGMOID
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+
+
+def say(msg):
+    print(f"\n[case] {msg}", flush=True)
+
+
+def run(h):
+    h.poison()
+    h.run()
+    torch.cuda.synchronize()
+    assert h.status_value() == 0
+    return h
+
+
+def host(t):
+    """A result in 64 bits (bf16 bit patterns decoded)."""
+    t = t.view(torch.bfloat16) if t.dtype == torch.int16 else t
+    return t.detach().cpu().double().numpy()
+
+
+def near(got, want, size, dtype, steps):
+    """|got - want| within half a step of `dtype` of want and `steps` binary32 half steps of `size`."""
+    got = host(got)
+    assert not np.isnan(got).any(), "unwritten (NaN) elements"
+    room = HALF[dtype] * np.abs(want) + ref.rel_steps(steps) * size + 2.0 ** -126
+    off = np.abs(got - want) - room
+    at = np.unravel_index(np.argmax(off), off.shape)
+    assert off[at] <= 0, (at, got[at], want[at], room[at])
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ------------------------------------------------------------------------------ routing
+
+def logits(T, E, dtype, seed, ld=None, masked=0.0, spread=1.0):
+    g = gen(seed)
+    x = torch.full((T, ld or E), float("nan"))
+    x[:, :E] = torch.randn(T, E, generator=g) * spread
+    if masked:
+        x[:, :E][torch.rand(T, E, generator=g) < masked] = float("-inf")
+    return x.to(dtype).cuda()[:, :E]
+
+
+def check_route(x, topk, bias=None, counts=True, **kw):
+    T, E = x.shape
+    h = bf.MoeRoute(T, E, topk, x, bias=None if bias is None else bias.cuda(), counts=counts, **kw)
+    e, w, c = ref.route(x.double().cpu().numpy(), topk, None if bias is None else bias.numpy(), **kw)
+    for again in range(2):
+        run(h)
+        assert np.array_equal(h.experts.cpu().numpy(), e), "experts"
+        # distances of logits up to 12 from the row's largest, and 24 roundings of exp, sum and quotient
+        near(h.weights, w, np.abs(w), torch.float32, 40)
+        if counts:
+            assert np.array_equal(h.counts.cpu().numpy(), c), "counts"
+            assert not h.ws.any(), "workspace must be left zeroed"
+    return h
+
+
+@pytest.mark.parametrize("T,E,topk,dtype,ld", [
+    (1, 1, 1, torch.float32, 1), (1, 8, 8, torch.float32, 8), (5, 7, 3, torch.bfloat16, 7),
+    (33, 60, 4, torch.bfloat16, 64), (17, 61, 6, torch.float32, 64), (64, 64, 8, torch.float32, 64),
+    (65, 128, 1, torch.bfloat16, 131), (130, 256, 8, torch.float32, 256), (67, 257, 5, torch.bfloat16, 260),
+    (35, 512, 16, torch.float32, 515), (1000, 32, 2, torch.float32, 32)])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_route_sizes(T, E, topk, dtype, ld, score):
+    say(f"route T={T} E={E} topk={topk} {dtype} ld={ld} score={score}")
+    for renorm in (False, True):
+        check_route(logits(T, E, dtype, T + E, ld), topk, score=score, renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("E,n_group,topk_group,group_top,topk", [
+    (8, 8, 3, 1, 3), (8, 4, 2, 2, 4), (60, 4, 1, 2, 6), (63, 7, 3, 2, 8), (256, 8, 4, 2, 8), (256, 8, 8, 1, 8),
+    (240, 3, 2, 2, 8), (256, 64, 5, 2, 8), (512, 16, 4, 2, 16), (500, 4, 2, 1, 7), (48, 16, 3, 2, 9)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_groups(E, n_group, topk_group, group_top, topk, dtype):
+    say(f"route groups E={E} of {n_group} take {topk_group} top {group_top} {dtype}")
+    g = gen(E + n_group)
+    bias = 0.01 * torch.randint(-20, 21, (E,), generator=g).float()
+    for score, b, masked in ((SIGMOID, bias, 0.0), (SOFTMAX, None, 0.2), (SIGMOID, None, 0.5)):
+        check_route(logits(70, E, dtype, 5 * E, E + 1, masked), topk, bias=b, score=score, n_group=n_group,
+                    topk_group=topk_group, group_top=group_top, renorm=True)
+
+
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_route_masks_and_odd_values(score):
+    inf, nan, low = float("inf"), float("nan"), torch.finfo(torch.float32).min
+    rows = [[-inf] * 6, [nan] * 6, [nan, 0.0, -inf, -0.0, 0.0, -inf], [low] * 6, [low, -inf, low, 1.0, -inf, 1.0],
+            [-inf, -inf, -inf, -inf, -inf, 3.0], [0.0] * 6, [80.0, 80.0, -80.0, 80.0, 1.0, 0.0],
+            [-90.0, -91.0, -92.0, -93.0, -94.0, -95.0]]
+    x = torch.tensor(rows).cuda()
+    say(f"route odd values score={score}")
+    # distances beyond 12 (and sums below 2^-126): the weights of the far ones are compared absolutely
+    for renorm in (False, True):
+        h = run(bf.MoeRoute(9, 6, 4, x, score=score, renorm=renorm, counts=True))
+        e, w, c = ref.route(x.double().cpu().numpy(), 4, score=score, renorm=renorm)
+        assert np.array_equal(h.experts.cpu().numpy(), e) and np.array_equal(h.counts.cpu().numpy(), c)
+        got = host(h.weights)
+        assert np.isfinite(got).all()
+        assert (np.abs(got - w) <= ref.rel_steps(256) * np.abs(w) + 2.0 ** -126).all(), (got, w)
+
+
+def test_route_infinite_logits_share():
+    inf = float("inf")
+    x = torch.tensor([[1.0, inf, 2.0, inf], [inf, -inf, 0.0, float("nan")]]).cuda()
+    h = run(bf.MoeRoute(2, 4, 2, x))
+    assert h.experts.tolist() == [[1, 3], [0, 2]] and h.weights.tolist() == [[0.5, 0.5], [1.0, 0.0]]
+
+
+def test_route_near_ties():
+    """Scores one binary32 step apart, and biases that put sums a 2^-30 apart or equal: the order of 64 bits."""
+    say("route near ties")
+    base = torch.tensor([0.7, -1.3, 2.1, 0.01])
+    x = base.repeat(50, 16)
+    step = torch.arange(64).repeat(50, 1) % 5 - 2
+    x = torch.nextafter(x, x + step)            # neighbours: a step up, down, or the same
+    x = x.cuda()
+    for score in (SOFTMAX, SIGMOID):
+        check_route(x, 8, score=score)
+        check_route(x, 8, score=score, n_group=8, topk_group=3, group_top=2)
+    g = gen(0)
+    bias = torch.randint(-3, 4, (64,), generator=g).float() * 2.0 ** -24 + 0.1
+    check_route(x, 8, bias=bias, score=SIGMOID)
+    check_route(x, 8, bias=bias, score=SIGMOID, n_group=16, topk_group=3, group_top=2)
+
+
+def test_route_far_logits_by_value():
+    """Softmax scores that underflow or saturate even in 64 bits tie: the lower index."""
+    x = torch.tensor([[0.0, -800.0, -790.0, -900.0, -5.0], [60.0, 50.0, 55.0, 45.0, 70.0]]).cuda()
+    h = run(bf.MoeRoute(2, 5, 4, x))
+    e, _, _ = ref.route(x.double().cpu().numpy(), 4)
+    assert np.array_equal(h.experts.cpu().numpy(), e)
+    h = run(bf.MoeRoute(2, 5, 4, x, score=SIGMOID))
+    e, _, _ = ref.route(x.double().cpu().numpy(), 4, score=SIGMOID)
+    assert np.array_equal(h.experts.cpu().numpy(), e)
+
+
+def test_route_empty_and_counts():
+    x = torch.empty((0, 8), device="cuda")
+    h = run(bf.MoeRoute(0, 8, 2, x, counts=True))
+    assert not h.counts.any() and not h.ws.any()
+    bf.MoeRoute(0, 8, 2, x).run()
+    check_route(logits(20000, 40, torch.float32, 1), 5)          # many workgroups add to one table
+
+
+@pytest.mark.parametrize("T,E,topk,dtype,ld", [
+    (1, 1, 1, torch.float32, 1), (3, 9, 4, torch.bfloat16, 9), (33, 60, 4, torch.float32, 64),
+    (40, 64, 8, torch.bfloat16, 64), (65, 128, 8, torch.bfloat16, 128), (31, 256, 8, torch.float32, 259),
+    (20, 511, 16, torch.bfloat16, 511), (9, 512, 3, torch.float32, 512)])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_bwd(T, E, topk, dtype, ld, score, renorm):
+    say(f"route_bwd T={T} E={E} topk={topk} {dtype} score={score} renorm={renorm}")
+    x = logits(T, E, dtype, T + E, ld, masked=0.1)
+    xs = x.double().cpu().numpy()
+    e, _, _ = ref.route(xs, topk, score=score)
+    dw = torch.randn(T, topk, generator=gen(7))
+    if T > 2:
+        e[1] = -1                                # a token without experts
+        e[2, :topk // 2] = -1
+    h = run(bf.MoeRouteBwd(T, E, topk, x, torch.from_numpy(e).cuda(), dw.cuda(), score=score, renorm=renorm, scale=2.5))
+    d, size = ref.route_bwd(xs, e, dw.numpy(), score, renorm, 2.5)
+    # as the weights (40), the sum over topk places, and the products and differences after them
+    near(h.dlogits, d, size, dtype, 80)
+
+
+def test_route_bwd_against_differences():
+    T, E, topk = 6, 24, 4
+    x = logits(T, E, torch.float32, 9)
+    xs = x.double().cpu().numpy()
+    dw = torch.randn(T, topk, generator=gen(8))
+    for score in (SOFTMAX, SIGMOID):
+        for renorm in (False, True):
+            r = run(bf.MoeRoute(T, E, topk, x, score=score, renorm=renorm))
+            e = r.experts.cpu().numpy()
+            h = run(bf.MoeRouteBwd(T, E, topk, x, r.experts, dw.cuda(), score=score, renorm=renorm))
+            got, step = host(h.dlogits), 1e-5
+            for k in range(E):
+                up, dn = xs.copy(), xs.copy()
+                up[:, k] += step
+                dn[:, k] -= step
+                num = ((ref.weights_of(up, e, score, renorm, 1.0) - ref.weights_of(dn, e, score, renorm, 1.0)) *
+                       dw.numpy()).sum(1) / (2 * step)
+                # differences: step^2 (third derivatives below 1) and 2^-53 / step; the kernel: 80 half steps of |dw| < 4
+                assert np.abs(got[:, k] - num).max() <= 4 * (1e-10 + 2.0 ** -53 / step + ref.rel_steps(80) * 4)
+
+
+def test_route_bwd_bad_place():
+    x = logits(2, 8, torch.float32, 1)
+    e = torch.tensor([[1, 8], [-5, 3]], dtype=torch.int32).cuda()
+    h = bf.MoeRouteBwd(2, 8, 2, x, e, torch.ones(2, 2).cuda(), score=SIGMOID)
+    h.poison()
+    h.run()
+    torch.cuda.synchronize()
+    assert h.status_value() == hocf.HOCF_ERR_BAD_INDEX
+    keep = np.array([[1, -1], [-1, 3]])
+    d, size = ref.route_bwd(x.double().cpu().numpy(), keep, np.ones((2, 2)), SIGMOID, False, 1.0)
+    near(h.dlogits, d, size, torch.float32, 80)
