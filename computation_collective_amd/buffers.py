@@ -506,3 +506,81 @@ class MoeRouteBwd(_Moe):
     def call(self, stream=None) -> int:
         s, stream = self._args(stream)
         return hocf.hocf_moe_route_bwd(*self._a, s, stream)
+
+
+class MoeSlots(_Moe):
+    """hocf_moe_slots: experts [T][topk] -> index [T][topk], pair [bins * cap], counts [bins]."""
+
+    def __init__(self, T, topk, bins, per_bin, cap, experts):
+        _dense(torch.int32, (T, topk), experts=experts)
+        dev = experts.device
+        self.experts = experts
+        self.index = torch.empty((T, topk), dtype=torch.int32, device=dev)
+        self.pair = torch.empty(bins * cap, dtype=torch.int32, device=dev)
+        self.counts = torch.empty(bins, dtype=torch.int64, device=dev)
+        self._a = (T, topk, bins, per_bin, cap, experts.data_ptr(), self.index.data_ptr(), self.pair.data_ptr(),
+                   self.counts.data_ptr())
+        self._bind(dev, hocf.hocf_moe_slots_workspace_bytes(T, topk, bins))
+
+    def poison(self):
+        for t in (self.index, self.pair, self.counts):
+            t.fill_(-77)
+
+    def call(self, stream=None) -> int:
+        s, stream = self._args(stream)
+        return hocf.hocf_moe_slots(*self._a, s, stream)
+
+
+class MoeCombine(_Moe):
+    """hocf_moe_combine: rows [R][N], weights [T][topk], index [T][topk] (None: pair order),
+    add [T][N] (None: nothing) -> out [T][N]."""
+
+    def __init__(self, T, topk, N, rows, weights, index=None, add=None, out_dt=BF16):
+        R = rows.shape[0]
+        _dense(None, (R, N), rows=rows)
+        _dense(torch.float32, (T, topk), weights=weights)
+        _dense(torch.int32, (T, topk), index=index)
+        _dense(None, (T, N), add=add)
+        _on(rows.device, weights=weights, index=index, add=add)
+        if add is not None and torch_dt(add) != out_dt:
+            raise TypeError(f"add is {add.dtype}, not of the output's type")
+        self.rows, self.weights, self.index, self.add = rows, weights, index, add
+        self.out = torch.empty((T, N), dtype=tdtype(out_dt), device=rows.device)
+        self._a = (T, topk, N, R, torch_dt(rows), out_dt, rows.data_ptr(), weights.data_ptr(), hocf.ptr(index),
+                   hocf.ptr(add), self.out.data_ptr())
+        self._bind(rows.device)
+
+    def poison(self):
+        nan_fill(self.out)
+
+    def call(self, stream=None) -> int:
+        s, stream = self._args(stream)
+        return hocf.hocf_moe_combine(*self._a, s, stream)
+
+
+class MoeCombineBwd(_Moe):
+    """hocf_moe_combine_bwd: rows [R][N], weights [T][topk], dout [T][N], index [T][topk] and
+    its inverse pair [R] (both None: pair order) -> drows [R][N], dweights [T][topk]."""
+
+    def __init__(self, T, topk, N, rows, weights, dout, index=None, pair=None):
+        R = rows.shape[0]
+        _dense(None, (R, N), rows=rows)
+        _dense(torch.float32, (T, topk), weights=weights)
+        _dense(None, (T, N), dout=dout)
+        _dense(torch.int32, (T, topk), index=index)
+        _dense(torch.int32, (R,), pair=pair)
+        _on(rows.device, weights=weights, dout=dout, index=index, pair=pair)
+        self.rows, self.weights, self.dout, self.index, self.pair = rows, weights, dout, index, pair
+        self.drows = torch.empty((R, N), dtype=tdtype(torch_dt(rows)), device=rows.device)
+        self.dweights = torch.empty((T, topk), dtype=torch.float32, device=rows.device)
+        self._a = (T, topk, N, R, torch_dt(rows), torch_dt(dout), rows.data_ptr(), weights.data_ptr(),
+                   dout.data_ptr(), hocf.ptr(index), hocf.ptr(pair), self.drows.data_ptr(), self.dweights.data_ptr())
+        self._bind(rows.device)
+
+    def poison(self):
+        nan_fill(self.drows)
+        nan_fill(self.dweights)
+
+    def call(self, stream=None) -> int:
+        s, stream = self._args(stream)
+        return hocf.hocf_moe_combine_bwd(*self._a, s, stream)

@@ -35,6 +35,48 @@ struct RouteBwdArgs {
   SyncArgs sync;
 };
 
+constexpr int kSlotsMaxBins = 64;   // one lane counts one bin
+constexpr int kSlotsThreads = 1024;
+constexpr int kSlotsMaxChunks = 512;
+
+struct SlotsArgs {
+  const int32_t* experts;  // [pairs]
+  int32_t* index;          // [pairs]
+  int32_t* pair;           // [bins * cap]
+  int64_t* counts;         // [bins]
+  uint32_t* hist;          // workspace: [chunks][64] pairs of each bin (chunked form only)
+  uint32_t pairs, chunk;   // chunk: pairs of one workgroup, a multiple of kSlotsThreads
+  uint32_t cap, experts_end;  // experts_end = bins * per_bin
+  int bins, per_bin, chunks;
+};
+
+struct CombineArgs {
+  const void* rows;      // [R][N] dt
+  const float* weights;  // [T][topk]
+  const int32_t* index;  // [T][topk] or NULL
+  const int32_t* pair;   // [R] or NULL (backward)
+  const void* add;       // [T][N] out_dt or NULL (forward)
+  const void* dout;      // [T][N] out_dt (backward)
+  void* out;             // [T][N] out_dt (forward)
+  void* drows;           // [R][N] dt (backward)
+  float* dweights;       // [T][topk] (backward)
+  int64_t T, R;
+  int topk, N, dt, out_dt;
+  SyncArgs sync;
+};
+
+// Pairs of one chunk, and how many chunks, for a number of pairs.
+inline void slots_chunks(int64_t pairs, uint32_t* chunk, int* chunks) {
+  int64_t c = 4096;
+  if (pairs > c * kSlotsMaxChunks)
+    c = (pairs + (int64_t)kSlotsMaxChunks * kSlotsThreads - 1) / ((int64_t)kSlotsMaxChunks * kSlotsThreads) * kSlotsThreads;
+  *chunk = (uint32_t)c;
+  *chunks = (int)((pairs + c - 1) / c);
+}
+
+int launch_moe_slots(const SlotsArgs& a, hipStream_t s);
+int launch_moe_combine(const CombineArgs& a, hipStream_t s);
+int launch_moe_combine_bwd(const CombineArgs& a, hipStream_t s);
 int launch_moe_route(const RouteArgs& a, hipStream_t s);
 int launch_moe_route_bwd(const RouteBwdArgs& a, hipStream_t s);
 

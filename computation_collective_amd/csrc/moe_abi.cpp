@@ -105,4 +105,129 @@ hocf_status hocf_moe_route_bwd(int64_t T, int E, int topk, hocf_dtype dt, const 
   return launched(launch_moe_route_bwd(a, static_cast<hipStream_t>(stream)), op);
 }
 
+/* ------------------------------------------------------------ window rows */
+
+size_t hocf_moe_slots_workspace_bytes(int64_t T, int topk, int bins) {
+  if (T <= 0 || topk <= 0 || bins <= 0 || T > kMaxTokens || T * topk > kMaxTokens) return 0;
+  uint32_t chunk;
+  int chunks;
+  slots_chunks(T * topk, &chunk, &chunks);
+  return (size_t)chunks * kSlotsMaxBins * 4;
+}
+
+hocf_status hocf_moe_slots(int64_t T, int topk, int bins, int per_bin, int64_t cap, const int32_t* experts,
+                           int32_t* index, int32_t* pair, int64_t* counts, const hocf_sync* sync, void* stream) {
+  const char* op = "moe_slots";
+  if (T < 0 || T > kMaxTokens || topk < 1 || T * topk > kMaxTokens)
+    return fail(HOCF_ERR_INVALID_ARG, "%s: T=%lld tokens of topk=%d outside [0, 2^31) pairs", op, (long long)T, topk);
+  if (bins < 1 || per_bin < 1 || (int64_t)bins * per_bin > kMaxTokens)
+    return fail(HOCF_ERR_INVALID_ARG, "%s: bins=%d of per_bin=%d experts", op, bins, per_bin);
+  if (cap < 0 || cap > kMaxTokens || bins * cap > kMaxTokens)
+    return fail(HOCF_ERR_INVALID_ARG, "%s: bins * cap rows outside [0, 2^31)", op);
+  if (bins > kSlotsMaxBins) return fail(HOCF_ERR_UNSUPPORTED, "%s: bins=%d > %d", op, bins, kSlotsMaxBins);
+  const size_t need = hocf_moe_slots_workspace_bytes(T, topk, bins);
+  hocf_status st = check_sync(sync, need);
+  if (st != HOCF_OK) return st;
+  const int64_t pairs = T * topk;
+  if (!counts || (pairs && (!experts || !index)) || (cap && !pair))
+    return fail(HOCF_ERR_INVALID_ARG, "%s: NULL tensor", op);
+  if (!aligned16(experts) || !aligned16(index) || !aligned16(pair) || !aligned16(counts))
+    return fail(HOCF_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", op);
+  {
+    Ranges rg;
+    rg.in("experts", 0, experts, pairs * 4);
+    rg.out("index", 0, index, pairs * 4);
+    rg.out("pair", 0, pair, bins * cap * 4);
+    rg.out("counts", 0, counts, (int64_t)bins * 8);
+    add_sync(rg, sync, need);
+    if ((st = rg.check(op)) != HOCF_OK) return st;
+  }
+  SlotsArgs a{};
+  a.experts = experts; a.index = index; a.pair = pair; a.counts = counts;
+  a.hist = static_cast<uint32_t*>(sync->workspace);
+  a.pairs = (uint32_t)pairs; a.cap = (uint32_t)cap;
+  a.bins = bins; a.per_bin = per_bin; a.experts_end = (uint32_t)(bins * per_bin);
+  slots_chunks(pairs, &a.chunk, &a.chunks);
+  return launched(launch_moe_slots(a, static_cast<hipStream_t>(stream)), op);
+}
+
+/* ------------------------------------------------------------ weighted sum */
+
+// What the combine's forward and backward passes check alike.
+static hocf_status check_combine(const char* op, int64_t T, int topk, int N, int64_t R, hocf_dtype dt,
+                                 hocf_dtype out_dt, const void* index, const hocf_sync* sync) {
+  if (T < 0 || T > kMaxTokens || R < 0 || R > kMaxTokens || topk < 1 || N < 0)
+    return fail(HOCF_ERR_INVALID_ARG, "%s: T=%lld R=%lld topk=%d N=%d out of range", op, (long long)T, (long long)R,
+                topk, N);
+  if (!dt_ok(dt) || !dt_ok(out_dt)) return fail(HOCF_ERR_INVALID_ARG, "%s: unknown dtype", op);
+  if (N % 8) return fail(HOCF_ERR_INVALID_ARG, "%s: N=%d not a multiple of 8", op, N);
+  if (!index && T && R != T * topk)
+    return fail(HOCF_ERR_INVALID_ARG, "%s: without an index R=%lld must be T * topk", op, (long long)R);
+  if (topk > kRouteMaxTopk || N > (1 << 24))
+    return fail(HOCF_ERR_UNSUPPORTED, "%s: topk=%d > %d or N=%d > 2^24", op, topk, kRouteMaxTopk, N);
+  return check_sync(sync, 0);
+}
+
+hocf_status hocf_moe_combine(int64_t T, int topk, int N, int64_t R, hocf_dtype dt, hocf_dtype out_dt,
+                             const void* rows, const float* weights, const int32_t* index, const void* add,
+                             void* out, const hocf_sync* sync, void* stream) {
+  const char* op = "moe_combine";
+  hocf_status st = check_combine(op, T, topk, N, R, dt, out_dt, index, sync);
+  if (st != HOCF_OK) return st;
+  if (T == 0 || N == 0) return ok();
+  if ((R && !rows) || !weights || !out) return fail(HOCF_ERR_INVALID_ARG, "%s: NULL tensor", op);
+  if (!aligned16(rows) || !aligned16(weights) || !aligned16(index) || !aligned16(add) || !aligned16(out))
+    return fail(HOCF_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", op);
+  {
+    Ranges rg;
+    rg.in("rows", 0, rows, R * N * dt_bytes(dt));
+    rg.in("weights", 0, weights, T * topk * 4);
+    rg.in("index", 0, index, T * topk * 4);
+    rg.in("add", 0, add, T * N * dt_bytes(out_dt));
+    rg.out("out", 0, out, T * N * dt_bytes(out_dt));
+    add_sync(rg, sync, 0);
+    if ((st = rg.check(op)) != HOCF_OK) return st;
+  }
+  CombineArgs a{};
+  if ((st = to_sync_args(sync, &a.sync)) != HOCF_OK) return st;
+  a.rows = rows; a.weights = weights; a.index = index; a.add = add; a.out = out;
+  a.T = T; a.R = R; a.topk = topk; a.N = N; a.dt = dt; a.out_dt = out_dt;
+  return launched(launch_moe_combine(a, static_cast<hipStream_t>(stream)), op);
+}
+
+hocf_status hocf_moe_combine_bwd(int64_t T, int topk, int N, int64_t R, hocf_dtype dt, hocf_dtype out_dt,
+                                 const void* rows, const float* weights, const void* dout, const int32_t* index,
+                                 const int32_t* pair, void* drows, float* dweights, const hocf_sync* sync,
+                                 void* stream) {
+  const char* op = "moe_combine_bwd";
+  hocf_status st = check_combine(op, T, topk, N, R, dt, out_dt, index, sync);
+  if (st != HOCF_OK) return st;
+  if (T ? (R && !index != !pair) : (R && !pair))
+    return fail(HOCF_ERR_INVALID_ARG, "%s: index and pair go together", op);
+  if (T == 0 && R == 0) return ok();
+  if ((T && (!weights || !dweights)) || (N && ((T && !dout) || (R && (!rows || !drows)))))
+    return fail(HOCF_ERR_INVALID_ARG, "%s: NULL tensor", op);
+  if (!aligned16(rows) || !aligned16(weights) || !aligned16(dout) || !aligned16(index) || !aligned16(pair) ||
+      !aligned16(drows) || !aligned16(dweights))
+    return fail(HOCF_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", op);
+  {
+    Ranges rg;
+    rg.in("rows", 0, rows, R * N * dt_bytes(dt));
+    rg.in("weights", 0, weights, T * topk * 4);
+    rg.in("dout", 0, dout, T * N * dt_bytes(out_dt));
+    rg.in("index", 0, index, T * topk * 4);
+    rg.in("pair", 0, pair, R * 4);
+    rg.out("drows", 0, drows, R * N * dt_bytes(dt));
+    rg.out("dweights", 0, dweights, T * topk * 4);
+    add_sync(rg, sync, 0);
+    if ((st = rg.check(op)) != HOCF_OK) return st;
+  }
+  CombineArgs a{};
+  if ((st = to_sync_args(sync, &a.sync)) != HOCF_OK) return st;
+  a.rows = rows; a.weights = weights; a.dout = dout; a.index = index; a.pair = pair;
+  a.drows = drows; a.dweights = dweights;
+  a.T = T; a.R = R; a.topk = topk; a.N = N; a.dt = dt; a.out_dt = out_dt;
+  return launched(launch_moe_combine_bwd(a, static_cast<hipStream_t>(stream)), op);
+}
+
 }  // extern "C"

@@ -40,6 +40,7 @@ EXPORTED = [
     "hocf_a2a_gemm", "hocf_a2a_gemm_unfused", "hocf_a2a_gemm_workspace_bytes",
     "hocf_dma_put",
     "hocf_moe_route", "hocf_moe_route_workspace_bytes", "hocf_moe_route_bwd",
+    "hocf_moe_slots", "hocf_moe_slots_workspace_bytes", "hocf_moe_combine", "hocf_moe_combine_bwd",
     "hocf_status_string", "hocf_last_error", "hocf_abi_version",
 ]
 
@@ -121,9 +122,13 @@ def lib():
         L.hocf_moe_route.argtypes = [i64, i, i, i, vp, i64, vp, i, i, i, i, i, f32, vp, vp, vp, S, vp]
         L.hocf_moe_route_workspace_bytes.argtypes = [i]
         L.hocf_moe_route_bwd.argtypes = [i64, i, i, i, vp, i64, vp, vp, i, i, f32, vp, S, vp]
-        for f in ("hocf_moe_route", "hocf_moe_route_bwd"):
+        L.hocf_moe_slots.argtypes = [i64, i, i, i, i64, vp, vp, vp, vp, S, vp]
+        L.hocf_moe_slots_workspace_bytes.argtypes = [i64, i, i]
+        L.hocf_moe_combine.argtypes = [i64, i, i, i64, i, i, vp, vp, vp, vp, vp, S, vp]
+        L.hocf_moe_combine_bwd.argtypes = [i64, i, i, i64, i, i, vp, vp, vp, vp, vp, vp, vp, S, vp]
+        for f in ("hocf_moe_route", "hocf_moe_route_bwd", "hocf_moe_slots", "hocf_moe_combine", "hocf_moe_combine_bwd"):
             getattr(L, f).restype = i
-        for f in ("hocf_moe_route_workspace_bytes",):
+        for f in ("hocf_moe_route_workspace_bytes", "hocf_moe_slots_workspace_bytes"):
             getattr(L, f).restype = sz
         L.hocf_status_string.argtypes = [i]
         L.hocf_status_string.restype = ctypes.c_char_p
@@ -325,6 +330,29 @@ def hocf_moe_route_bwd(T, E, topk, dt, logits, ld, experts, dweights, score, ren
                        stream=None) -> int:
     return lib().hocf_moe_route_bwd(T, E, topk, dt, ptr(logits), ld, ptr(experts), ptr(dweights), score, renorm,
                                     scale, ptr(dlogits), ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_moe_slots_workspace_bytes(T, topk, bins) -> int:
+    return lib().hocf_moe_slots_workspace_bytes(T, topk, bins)
+
+
+def hocf_moe_slots(T, topk, bins, per_bin, cap, experts, index, pair, counts, sync_, stream=None) -> int:
+    """Router choices -> window rows of the pairs, pairs of the rows, pairs of each rank."""
+    return lib().hocf_moe_slots(T, topk, bins, per_bin, cap, ptr(experts), ptr(index), ptr(pair), ptr(counts),
+                                ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_moe_combine(T, topk, N, R, dt, out_dt, rows, weights, index, add, out, sync_, stream=None) -> int:
+    """The tokens' weighted sums of the experts' rows."""
+    return lib().hocf_moe_combine(T, topk, N, R, dt, out_dt, ptr(rows), ptr(weights), ptr(index), ptr(add), ptr(out),
+                                  ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_moe_combine_bwd(T, topk, N, R, dt, out_dt, rows, weights, dout, index, pair, drows, dweights, sync_,
+                         stream=None) -> int:
+    """The gradients of the experts' rows and of the weights."""
+    return lib().hocf_moe_combine_bwd(T, topk, N, R, dt, out_dt, ptr(rows), ptr(weights), ptr(dout), ptr(index),
+                                      ptr(pair), ptr(drows), ptr(dweights), ctypes.byref(sync_), _stream(stream))
 
 
 def _host_i64(a):

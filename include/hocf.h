@@ -38,6 +38,11 @@
  *   hocf_moe_route, hocf_moe_route_bwd
  *                    router logits -> experts and weights of every token, and
  *                    the gradient of the logits
+ *   hocf_moe_slots   router choices -> the combine's receive-window row of
+ *                    every (token, choice) pair, and the pair of every row
+ *   hocf_moe_combine, hocf_moe_combine_bwd
+ *                    the experts' rows -> the tokens' weighted sums, and the
+ *                    gradients of the rows and the weights
  *
  * The method (SC24 abstract; mKernel, section on persistent kernels and
  * tile/chunk overlap): the workgroups of one kernel each finish an output
@@ -578,6 +583,71 @@ size_t hocf_moe_route_workspace_bytes(int E);
 hocf_status hocf_moe_route_bwd(int64_t T, int E, int topk, hocf_dtype dt, const void* logits, int64_t ld,
                                const int32_t* experts, const float* dweights, hocf_score score, int renorm,
                                float scale, void* dlogits, const hocf_sync* sync, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The rows of the combine's receive windows.
+ *
+ * Pair i = t * topk + j is token t's choice j; expert e lives on rank b = e /
+ * per_bin.  hocf_a2a_gemm and hocf_gemm_a2a number a source's pairs on each
+ * rank in pair order, and rank b's results come back as window b's rows in
+ * that order.  With the windows of one source [bins][cap] one after another,
+ * pair i has row index[i] = b * cap + (earlier pairs of rank b):
+ *
+ *   experts  [T][topk] int32; a choice outside [0, bins * per_bin) has no row
+ *   index    [T][topk] int32: the pair's row, -1 for a pair that has none (or
+ *            whose place in its window would be cap or beyond)
+ *   pair     [bins * cap] int32: the pair of each row, -1 for a row without
+ *   counts   [bins] int64: each rank's pairs, those beyond cap included
+ *
+ * The results do not depend on the grid.  Supported: 1 <= bins <= 64,
+ * per_bin >= 1, cap >= 0, topk >= 1; T * topk, bins * per_bin and bins * cap
+ * below 2^31.  The workspace needs no zeroing.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_moe_slots(int64_t T, int topk, int bins, int per_bin, int64_t cap, const int32_t* experts,
+                           int32_t* index, int32_t* pair, int64_t* counts, const hocf_sync* sync, void* stream);
+size_t hocf_moe_slots_workspace_bytes(int64_t T, int topk, int bins);
+
+/* ------------------------------------------------------------------------
+ * The weighted sum of the experts' rows.
+ *
+ *   out[t] = sum_j weights[t][j] * rows[index[t][j]]  (+ add[t])
+ * in fp32, j = 0 .. topk-1 in order, then add, rounded once to out_dt.
+ *
+ *   rows     [R][N] dt                weights  [T][topk] fp32
+ *   index    [T][topk] int32 (-1: the pair adds nothing), or NULL: pair (t, j)
+ *            has row t * topk + j (then R = T * topk)
+ *   add      NULL or [T][N] out_dt (a residual stream)
+ *   out      [T][N] out_dt
+ * What is not named is not read: a row that no pair names may hold anything.
+ * An index outside [-1, R) adds nothing and HOCF_ERR_BAD_INDEX goes to the
+ * status word.
+ * Supported: dt and out_dt F32 or BF16; N a multiple of 8 up to 2^24; 1 <= topk
+ * <= 16; 0 <= T, R < 2^31.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_moe_combine(int64_t T, int topk, int N, int64_t R, hocf_dtype dt, hocf_dtype out_dt,
+                             const void* rows, const float* weights, const int32_t* index, const void* add,
+                             void* out, const hocf_sync* sync, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The weighted sum of the experts' rows, backward.
+ *
+ *   drows[index[t][j]] = weights[t][j] * dout[t]       (rows of no pair: 0)
+ *   dweights[t][j]     = sum_n rows[index[t][j]][n] * dout[t][n]   (no row: 0)
+ * in fp32, drows rounded once to dt; the sums run in a fixed order.  (The
+ * gradient of `add` is dout itself.)
+ *
+ *   dout     [T][N] out_dt            drows  [R][N] dt
+ *   pair     [R] int32: the pair of each row or -1, the inverse of index as
+ *            hocf_moe_slots gives it; NULL exactly when index is NULL
+ * Every row has at most one pair; where index and pair contradict each other
+ * the rows concerned are unspecified (nothing else is written).  An index
+ * outside [-1, R) is taken as -1 and HOCF_ERR_BAD_INDEX goes to the status
+ * word.  Other arguments and support as for hocf_moe_combine.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_moe_combine_bwd(int64_t T, int topk, int N, int64_t R, hocf_dtype dt, hocf_dtype out_dt,
+                                 const void* rows, const float* weights, const void* dout, const int32_t* index,
+                                 const int32_t* pair, void* drows, float* dweights, const hocf_sync* sync,
+                                 void* stream);
 
 /* ---------------------------------------------------------------------- */
 const char* hocf_status_string(hocf_status s); /* static string, never NULL */

@@ -223,3 +223,150 @@ def test_route_bwd_bad_place():
     keep = np.array([[1, -1], [-1, 3]])
     d, size = ref.route_bwd(x.double().cpu().numpy(), keep, np.ones((2, 2)), SIGMOID, False, 1.0)
     near(h.dlogits, d, size, torch.float32, 80)
+
+
+# ------------------------------------------------------------------------------ window rows
+
+def choices(T, topk, E, seed, none=0.0, beyond=0):
+    """Random experts; some places empty, some naming experts beyond E."""
+    g = gen(seed)
+    e = torch.randint(0, E + beyond, (T, topk), generator=g, dtype=torch.int32)
+    if none:
+        e[torch.rand(T, topk, generator=g) < none] = -1
+    return e
+
+
+@pytest.mark.parametrize("T,topk,bins,per_bin,cap", [
+    (0, 2, 3, 2, 5), (1, 1, 1, 1, 1), (1, 1, 64, 1, 1), (31, 3, 5, 3, 20), (64, 1, 2, 1, 64), (513, 2, 8, 4, 200),
+    (1000, 8, 16, 16, 700), (2048, 8, 64, 3, 300), (2049, 8, 64, 3, 300), (4097, 5, 7, 1, 0), (9000, 4, 33, 2, 1200),
+    (70001, 3, 1, 5, 250000), (300000, 8, 9, 7, 300000)])
+def test_slots(T, topk, bins, per_bin, cap):
+    say(f"slots T={T} topk={topk} bins={bins}x{per_bin} cap={cap}")
+    e = choices(T, topk, bins * per_bin, T, none=0.1, beyond=2)
+    if T > 600:
+        e[100:400] = e[0, 0]                     # a run on one bin
+        e[400:500] = -1
+    index, pair, counts = ref.slots(e.numpy(), bins, per_bin, cap)
+    h = bf.MoeSlots(T, topk, bins, per_bin, cap, e.cuda())
+    h.ws.fill_(-1)                               # the workspace needs no zeroing
+    for again in range(2):
+        run(h)
+        assert np.array_equal(h.counts.cpu().numpy(), counts)
+        assert np.array_equal(h.index.cpu().numpy(), index)
+        assert np.array_equal(h.pair.cpu().numpy(), pair)
+
+
+def test_slots_odd_experts():
+    e = torch.tensor([[-1, -2], [2 ** 31 - 1, -2 ** 31], [5, 6]], dtype=torch.int32).cuda()
+    h = run(bf.MoeSlots(3, 2, 3, 2, 2, e))
+    assert h.index.tolist() == [[-1, -1], [-1, -1], [4, -1]] and h.counts.tolist() == [0, 0, 1]
+
+
+# ------------------------------------------------------------------------------ weighted sum
+
+def combine_inputs(T, topk, N, bins, dt, out_dt, seed, none=0.1):
+    """Rows in windows a third larger than needed (bins = 0: in pair order); what no pair names is NaN."""
+    g = gen(seed)
+    w = torch.rand(T, topk, generator=g) + 0.05
+    if bins:
+        cap = T * topk // bins + T * topk // (3 * bins) + 9
+        e = choices(T, topk, bins, seed, none)
+        index, pair, _ = ref.slots(e.numpy(), bins, 1, cap)
+        rows = torch.randn(bins * cap, N, generator=g)
+        rows[torch.from_numpy(pair) < 0] = float("nan")
+    else:
+        index = pair = None
+        rows = torch.randn(T * topk, N, generator=g)
+    return rows.to(dt), w, index, pair, torch.randn(T, N, generator=g).to(out_dt)
+
+
+def dev(a):
+    return None if a is None else (torch.from_numpy(a) if isinstance(a, np.ndarray) else a).cuda()
+
+
+TYPES = {torch.float32: hocf.HOCF_F32, torch.bfloat16: hocf.HOCF_BF16}
+SHAPES = [(1, 1, 8, 0), (3, 2, 16, 2), (4, 2, 4096, 0), (5, 3, 40, 3), (7, 8, 520, 4), (33, 4, 1032, 8), (66, 5, 264, 1),
+          (9, 16, 2056, 8), (10, 9, 128, 0), (300, 6, 64, 8), (2050, 7, 24, 8), (2300, 8, 520, 0), (2, 1, 65544, 1)]
+
+
+@pytest.mark.parametrize("T,topk,N,bins", SHAPES)
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("out_dt", [torch.float32, torch.bfloat16])
+def test_combine(T, topk, N, bins, dt, out_dt):
+    say(f"combine T={T} topk={topk} N={N} bins={bins} {dt} -> {out_dt}")
+    rows, w, index, _, add = combine_inputs(T, topk, N, bins, dt, out_dt, T + N)
+    if index is not None and T > 2:
+        index[1] = -1                            # a token without rows
+    for a in (None, add):
+        h = run(bf.MoeCombine(T, topk, N, dev(rows), dev(w), index=dev(index), add=dev(a), out_dt=TYPES[out_dt]))
+        out, size = ref.combine(rows.float().numpy(), w.numpy(), index, None if a is None else a.float().numpy())
+        near(h.out, out, size, out_dt, topk + 1)  # one rounding for each product-sum and for add
+
+
+@pytest.mark.parametrize("T,topk,N,bins", SHAPES)
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("out_dt", [torch.float32, torch.bfloat16])
+def test_combine_bwd(T, topk, N, bins, dt, out_dt):
+    say(f"combine_bwd T={T} topk={topk} N={N} bins={bins} {dt} <- {out_dt}")
+    rows, w, index, pair, dout = combine_inputs(T, topk, N, bins, dt, out_dt, T + N + 1)
+    h = run(bf.MoeCombineBwd(T, topk, N, dev(rows), dev(w), dev(dout), index=dev(index), pair=dev(pair)))
+    dr, dw, size = ref.combine_bwd(rows.float().numpy(), w.numpy(), dout.float().numpy(), index)
+    near(h.drows, dr, np.abs(dr), dt, 1)
+    near(h.dweights, dw, size, torch.float32, N / 64 + 10)    # a lane's run of products, then the folds
+    first = h.dweights.clone(), h.drows.clone()
+    run(h)
+    assert torch.equal(first[0], h.dweights) and torch.equal(first[1], h.drows), "another call, other bits"
+
+
+def test_combine_gradients_are_the_formulas_differences():
+    """<dout, out> is linear in each weight and each row: unit steps give the gradients."""
+    T, topk, N = 3, 2, 16
+    rows, w, index, pair, dout = combine_inputs(T, topk, N, 2, torch.float32, torch.float32, 3)
+    h = run(bf.MoeCombineBwd(T, topk, N, dev(rows), dev(w), dev(dout), index=dev(index), pair=dev(pair)))
+    x = np.nan_to_num(rows.numpy())
+    for t in range(T):
+        for j in range(topk):
+            up = w.numpy().astype(np.float64).copy()
+            up[t, j] += 1
+            num = ((ref.combine(x, up, index)[0] - ref.combine(x, w.numpy(), index)[0]) * dout.numpy()).sum()
+            assert abs(host(h.dweights)[t, j] - num) <= 30 * 2.0 ** -24 * N * 9
+    for r in range(len(x)):
+        up = x.astype(np.float64).copy()
+        up[r, 5] += 1
+        num = ((ref.combine(up, w.numpy(), index)[0] - ref.combine(x, w.numpy(), index)[0]) * dout.numpy()).sum()
+        assert abs(host(h.drows)[r, 5] - num) <= 2.0 ** -22 * 4 + 1e-12
+
+
+def test_combine_without_rows():
+    """R = 0 and T = 0: nothing is read, everything is written."""
+    w = torch.ones(3, 2).cuda()
+    none = torch.full((3, 2), -1, dtype=torch.int32).cuda()
+    rows, add = torch.empty((0, 16)).cuda(), torch.randn(3, 16).cuda()
+    h = run(bf.MoeCombine(3, 2, 16, rows, w, index=none, add=add, out_dt=hocf.HOCF_F32))
+    assert torch.equal(h.out, add)
+    h = run(bf.MoeCombineBwd(3, 2, 16, rows, w, add, index=none, pair=torch.empty(0, dtype=torch.int32).cuda()))
+    assert not h.dweights.any()
+    e, f = torch.empty((0, 2)).cuda(), torch.empty((0, 2), dtype=torch.int32).cuda()
+    rows, pair = torch.randn(5, 16).cuda(), torch.full((5,), -1, dtype=torch.int32).cuda()
+    h = run(bf.MoeCombineBwd(0, 2, 16, rows, e, torch.empty((0, 16)).cuda(), index=f, pair=pair))
+    assert not h.drows.any()
+    run(bf.MoeCombine(0, 2, 16, rows, e, index=f, out_dt=hocf.HOCF_F32))
+
+
+def test_combine_bad_index():
+    rows, w = torch.randn(4, 8).cuda(), torch.ones(2, 2).cuda()
+    index = torch.tensor([[0, 4], [-2, 3]], dtype=torch.int32).cuda()
+    h = bf.MoeCombine(2, 2, 8, rows, w, index=index, out_dt=hocf.HOCF_F32)
+    h.poison()
+    h.run()
+    torch.cuda.synchronize()
+    assert h.status_value() == hocf.HOCF_ERR_BAD_INDEX
+    assert torch.equal(h.out, rows[[0, 3]])
+    pair = torch.tensor([0, -1, -1, 3], dtype=torch.int32).cuda()
+    h = bf.MoeCombineBwd(2, 2, 8, rows, w, torch.ones(2, 8).cuda(), index=index, pair=pair)
+    h.poison()
+    h.run()
+    torch.cuda.synchronize()
+    assert h.status_value() == hocf.HOCF_ERR_BAD_INDEX
+    assert torch.equal(h.drows, torch.tensor([1.0, 0, 0, 1])[:, None].expand(4, 8).cuda())
+    assert h.dweights[0, 1] == 0 and h.dweights[1, 0] == 0

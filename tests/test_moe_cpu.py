@@ -95,6 +95,97 @@ def test_route_bwd_accepts():
     valid(route_bwd())
 
 
+SLOTS = dict(T=100, topk=2, bins=4, per_bin=2, cap=64, experts=addr(1), index=addr(2), pair=addr(3), counts=addr(4),
+             s=None)
+
+
+def slots(**kw):
+    a = dict(SLOTS, **kw)
+    s = a.pop("s")
+    return hocf.hocf_moe_slots(*a.values(), sync() if s is None else s)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(T=-1), INVALID), (dict(T=1 << 30), INVALID), (dict(topk=0), INVALID), (dict(bins=0), INVALID),
+    (dict(per_bin=0), INVALID), (dict(bins=64, per_bin=1 << 25), INVALID), (dict(cap=-1), INVALID),
+    (dict(cap=1 << 29), INVALID), (dict(bins=65), UNSUPPORTED), (dict(experts=None), INVALID),
+    (dict(index=None), INVALID), (dict(pair=None), INVALID), (dict(counts=None), INVALID),
+    (dict(counts=addr(4) + 8), INVALID), (dict(pair=addr(1)), INVALID), (dict(index=addr(3) + 1008), INVALID),
+    (dict(s=sync(nbytes=16)), INVALID), (dict(s=sync(epoch=0)), INVALID), (dict(s=sync(ws=addr(2))), INVALID),
+])
+def test_slots_rejects(kw, expect):
+    assert slots(**kw) == expect
+
+
+def test_slots_accepts():
+    assert hocf.hocf_moe_slots_workspace_bytes(100, 2, 4) == 64 * 4
+    assert hocf.hocf_moe_slots_workspace_bytes(1 << 20, 8, 4) == 512 * 64 * 4
+    assert hocf.hocf_moe_slots_workspace_bytes(0, 2, 4) == 0
+    valid(slots())
+    valid(slots(T=0, experts=None, index=None, s=sync(ws=0, nbytes=0)))
+    valid(slots(cap=0, pair=None))
+
+
+COMBINE = dict(T=10, topk=2, N=64, R=40, dt=BF16, out_dt=F32, rows=addr(1), weights=addr(2), index=addr(3),
+               add=addr(4), out=addr(5), s=None)
+
+
+def combine(**kw):
+    a = dict(COMBINE, **kw)
+    s = a.pop("s")
+    return hocf.hocf_moe_combine(*a.values(), sync() if s is None else s)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(T=-1), INVALID), (dict(R=-1), INVALID), (dict(topk=0), INVALID), (dict(N=-8), INVALID),
+    (dict(N=60), INVALID), (dict(dt=3), INVALID), (dict(out_dt=-1), INVALID), (dict(index=None), INVALID),
+    (dict(topk=17), UNSUPPORTED), (dict(N=(1 << 24) + 8), UNSUPPORTED), (dict(rows=None), INVALID),
+    (dict(weights=None), INVALID), (dict(out=None), INVALID), (dict(rows=addr(1) + 8), INVALID),
+    (dict(add=addr(4) + 4), INVALID), (dict(out=addr(4)), INVALID), (dict(out=addr(1)), INVALID),
+    (dict(out=addr(3)), INVALID), (dict(s=sync(epoch=0)), INVALID),
+])
+def test_combine_rejects(kw, expect):
+    assert combine(**kw) == expect
+
+
+def test_combine_accepts():
+    assert combine(T=0, rows=None, weights=None, out=None) == OK
+    assert combine(N=0) == OK
+    valid(combine())
+    valid(combine(R=0, rows=None))
+    valid(combine(R=20, index=None, add=None))
+
+
+CBWD = dict(T=10, topk=2, N=64, R=40, dt=BF16, out_dt=F32, rows=addr(1), weights=addr(2), dout=addr(3), index=addr(4),
+            pair=addr(5), drows=addr(6), dweights=addr(7), s=None)
+
+
+def combine_bwd(**kw):
+    a = dict(CBWD, **kw)
+    s = a.pop("s")
+    return hocf.hocf_moe_combine_bwd(*a.values(), sync() if s is None else s)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(T=-1), INVALID), (dict(N=4), INVALID), (dict(dt=2), INVALID), (dict(topk=17), UNSUPPORTED),
+    (dict(index=None), INVALID), (dict(pair=None), INVALID), (dict(index=None, pair=None), INVALID),
+    (dict(R=20, index=None), INVALID), (dict(T=0, pair=None), INVALID), (dict(rows=None), INVALID),
+    (dict(dout=None), INVALID), (dict(drows=None), INVALID), (dict(dweights=None), INVALID),
+    (dict(dweights=addr(7) + 4), INVALID), (dict(drows=addr(1)), INVALID), (dict(dweights=addr(2)), INVALID),
+    (dict(drows=addr(5)), INVALID), (dict(s=sync(epoch=0)), INVALID),
+])
+def test_combine_bwd_rejects(kw, expect):
+    assert combine_bwd(**kw) == expect
+
+
+def test_combine_bwd_accepts():
+    assert combine_bwd(T=0, R=0, index=None, pair=None) == OK
+    valid(combine_bwd())
+    valid(combine_bwd(R=20, index=None, pair=None))
+    valid(combine_bwd(T=0, index=None, weights=None, dout=None, dweights=None))
+    valid(combine_bwd(R=0, rows=None, drows=None, pair=None))
+
+
 def test_null_sync_is_refused():
     L = hocf.lib()
     none = ctypes.POINTER(hocf.hocf_sync)()
