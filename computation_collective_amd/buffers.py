@@ -584,3 +584,50 @@ class MoeCombineBwd(_Moe):
     def call(self, stream=None) -> int:
         s, stream = self._args(stream)
         return hocf.hocf_moe_combine_bwd(*self._a, s, stream)
+
+
+def w4_layout(E, N, K, group):
+    """Shapes of packed 4-bit weights and of their scales (hocf_w4_pack)."""
+    nb = cdiv(N, 16)
+    return (E, nb, cdiv(K, 128), 64, 4), (E, nb, cdiv(K, group), 16)
+
+
+def w4_pack(codes, scales, zeros=None, group=128, stream=None):
+    """hocf_w4_pack: codes [E][K][N] uint8, scales (and zeros) [E][ceil(K/group)][N] bf16 ->
+    (wq, scales, zeros or None) as hocf_gemv_w4 reads them."""
+    E, K, N = codes.shape
+    _dense(torch.uint8, (E, K, N), codes=codes)
+    _dense(torch.bfloat16, (E, cdiv(K, group), N), scales=scales, zeros=zeros)
+    _on(codes.device, scales=scales, zeros=zeros)
+    words, small = w4_layout(E, N, K, group)
+    wq = torch.empty(words, dtype=torch.int32, device=codes.device)
+    s = torch.empty(small, dtype=torch.bfloat16, device=codes.device)
+    z = None if zeros is None else torch.empty(small, dtype=torch.bfloat16, device=codes.device)
+    stream = torch.cuda.current_stream(codes.device) if stream is None else stream
+    hocf.check(hocf.hocf_w4_pack(E, N, K, group, codes, scales, zeros, wq, s, z, stream))
+    return wq, s, z
+
+
+class GemvW4(_Moe):
+    """hocf_gemv_w4: x [R / rows_per_x][K] bf16, experts [R] (None: one matrix), packed
+    weights (w4_pack) -> out [R][N]."""
+
+    def __init__(self, R, rows_per_x, E, e0, N, K, group, x, experts, wq, scales, zeros=None, out_dt=BF16):
+        words, small = w4_layout(E, N, K, group)
+        _dense(torch.bfloat16, (R // rows_per_x, K), x=x)
+        _dense(torch.int32, (R,), experts=experts)
+        _dense(torch.int32, words, wq=wq)
+        _dense(torch.bfloat16, small, scales=scales, zeros=zeros)
+        _on(x.device, experts=experts, wq=wq, scales=scales, zeros=zeros)
+        self.x, self.experts, self.wq, self.scales, self.zeros = x, experts, wq, scales, zeros
+        self.out = torch.empty((R, N), dtype=tdtype(out_dt), device=x.device)
+        self._a = (R, rows_per_x, E, e0, N, K, group, out_dt, x.data_ptr(), hocf.ptr(experts), wq.data_ptr(),
+                   scales.data_ptr(), hocf.ptr(zeros), self.out.data_ptr())
+        self._bind(x.device)
+
+    def poison(self):
+        nan_fill(self.out)
+
+    def call(self, stream=None) -> int:
+        s, stream = self._args(stream)
+        return hocf.hocf_gemv_w4(*self._a, s, stream)

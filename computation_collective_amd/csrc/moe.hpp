@@ -65,6 +65,30 @@ struct CombineArgs {
   SyncArgs sync;
 };
 
+constexpr int kW4MaxRows = 1024;
+
+struct GemvW4Args {
+  const uint16_t* x;       // [R / rows_per_x][K]
+  const int32_t* experts;  // [R] or NULL
+  const uint32_t* wq;      // [E][nb][kb][64][4]
+  const uint16_t* scales;  // [E][nb][groups][16]
+  const uint16_t* zeros;   // the same, or NULL
+  void* out;               // [R][N] out_dt
+  int R, rows_per_x, E, e0, N, K, group, out_dt;
+  int nb, kb, groups;      // ceil(N / 16), ceil(K / 128), ceil(K / group)
+};
+
+struct W4PackArgs {
+  const uint8_t* codes;    // [E][K][N]
+  const uint16_t *scales, *zeros;  // [E][groups][N]
+  uint32_t* wq;
+  uint16_t *scales_out, *zeros_out;
+  int E, N, K, nb, kb, groups;
+};
+
+int launch_gemv_w4(const GemvW4Args& a, hipStream_t s);
+int launch_w4_pack(const W4PackArgs& a, hipStream_t s);
+
 // Pairs of one chunk, and how many chunks, for a number of pairs.
 inline void slots_chunks(int64_t pairs, uint32_t* chunk, int* chunks) {
   int64_t c = 4096;

@@ -230,4 +230,95 @@ hocf_status hocf_moe_combine_bwd(int64_t T, int topk, int N, int64_t R, hocf_dty
   return launched(launch_moe_combine_bwd(a, static_cast<hipStream_t>(stream)), op);
 }
 
+/* ------------------------------------------------------------ 4-bit weights */
+
+// What the product and the packing check alike.
+static hocf_status check_w4(const char* op, int E, int N, int K, int group) {
+  if (E < 1 || N < 0 || K < 0 || N % 8 || K % 8)
+    return fail(HOCF_ERR_INVALID_ARG, "%s: E=%d, N=%d and K=%d: E >= 1, N and K multiples of 8", op, E, N, K);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(HOCF_ERR_UNSUPPORTED, "%s: group=%d is none of 32, 64, 128", op, group);
+  if (N > (1 << 20) || K > (1 << 20)) return fail(HOCF_ERR_UNSUPPORTED, "%s: N=%d or K=%d > 2^20", op, N, K);
+  return HOCF_OK;
+}
+
+hocf_status hocf_gemv_w4(int R, int rows_per_x, int E, int e0, int N, int K, int group, hocf_dtype out_dt,
+                         const void* x, const int32_t* experts, const uint32_t* wq, const void* scales,
+                         const void* zeros, void* out, const hocf_sync* sync, void* stream) {
+  const char* op = "gemv_w4";
+  hocf_status st = check_w4(op, E, N, K, group);
+  if (st != HOCF_OK) return st;
+  if (R < 0 || rows_per_x < 1 || R % rows_per_x)
+    return fail(HOCF_ERR_INVALID_ARG, "%s: R=%d must be a multiple of rows_per_x=%d", op, R, rows_per_x);
+  if (!dt_ok(out_dt)) return fail(HOCF_ERR_INVALID_ARG, "%s: unknown dtype", op);
+  if (e0 < 0 || e0 > kMaxTokens - E) return fail(HOCF_ERR_INVALID_ARG, "%s: e0=%d with E=%d experts", op, e0, E);
+  if (!experts && E != 1) return fail(HOCF_ERR_INVALID_ARG, "%s: E=%d experts need the rows' choices", op, E);
+  if (R > kW4MaxRows) return fail(HOCF_ERR_UNSUPPORTED, "%s: R=%d > %d rows", op, R, kW4MaxRows);
+  if ((st = check_sync(sync, 0)) != HOCF_OK) return st;
+  if (R == 0 || N == 0) return ok();
+  if (!out || (K && (!x || !wq || !scales))) return fail(HOCF_ERR_INVALID_ARG, "%s: NULL tensor", op);
+  if (!aligned16(x) || !aligned16(experts) || !aligned16(wq) || !aligned16(scales) || !aligned16(zeros) ||
+      !aligned16(out))
+    return fail(HOCF_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", op);
+  GemvW4Args a{};
+  a.nb = (int)cdiv(N, 16);
+  a.kb = (int)cdiv(K, 128);
+  a.groups = (int)cdiv(K, group);
+  {
+    const int64_t sc = (int64_t)E * a.nb * a.groups * 32;
+    Ranges rg;
+    rg.in("x", 0, x, (int64_t)(R / rows_per_x) * K * 2);
+    rg.in("experts", 0, experts, (int64_t)R * 4);
+    rg.in("wq", 0, wq, (int64_t)E * a.nb * a.kb * 1024);
+    rg.in("scales", 0, scales, sc);
+    rg.in("zeros", 0, zeros, sc);
+    rg.out("out", 0, out, (int64_t)R * N * dt_bytes(out_dt));
+    add_sync(rg, sync, 0);
+    if ((st = rg.check(op)) != HOCF_OK) return st;
+  }
+  a.x = static_cast<const uint16_t*>(x);
+  a.experts = experts; a.wq = wq;
+  a.scales = static_cast<const uint16_t*>(scales);
+  a.zeros = static_cast<const uint16_t*>(zeros);
+  a.out = out;
+  a.R = R; a.rows_per_x = rows_per_x; a.E = E; a.e0 = e0; a.N = N; a.K = K; a.group = group; a.out_dt = out_dt;
+  return launched(launch_gemv_w4(a, static_cast<hipStream_t>(stream)), op);
+}
+
+hocf_status hocf_w4_pack(int E, int N, int K, int group, const uint8_t* codes, const void* scales, const void* zeros,
+                         uint32_t* wq, void* scales_out, void* zeros_out, void* stream) {
+  const char* op = "w4_pack";
+  hocf_status st = check_w4(op, E, N, K, group);
+  if (st != HOCF_OK) return st;
+  if (!zeros != !zeros_out) return fail(HOCF_ERR_INVALID_ARG, "%s: zeros and zeros_out go together", op);
+  if (N == 0 || K == 0) return ok();
+  if (!codes || !scales || !wq || !scales_out) return fail(HOCF_ERR_INVALID_ARG, "%s: NULL tensor", op);
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(zeros) || !aligned16(wq) || !aligned16(scales_out) ||
+      !aligned16(zeros_out))
+    return fail(HOCF_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", op);
+  W4PackArgs a{};
+  a.E = E; a.N = N; a.K = K;
+  a.nb = (int)cdiv(N, 16);
+  a.kb = (int)cdiv(K, 128);
+  a.groups = (int)cdiv(K, group);
+  {
+    const int64_t in = (int64_t)E * a.groups * N * 2, sc = (int64_t)E * a.nb * a.groups * 32;
+    Ranges rg;
+    rg.in("codes", 0, codes, (int64_t)E * K * N);
+    rg.in("scales", 0, scales, in);
+    rg.in("zeros", 0, zeros, in);
+    rg.out("wq", 0, wq, (int64_t)E * a.nb * a.kb * 1024);
+    rg.out("scales_out", 0, scales_out, sc);
+    rg.out("zeros_out", 0, zeros_out, sc);
+    if ((st = rg.check(op)) != HOCF_OK) return st;
+  }
+  a.codes = codes;
+  a.scales = static_cast<const uint16_t*>(scales);
+  a.zeros = static_cast<const uint16_t*>(zeros);
+  a.wq = wq;
+  a.scales_out = static_cast<uint16_t*>(scales_out);
+  a.zeros_out = static_cast<uint16_t*>(zeros_out);
+  return launched(launch_w4_pack(a, static_cast<hipStream_t>(stream)), op);
+}
+
 }  // extern "C"

@@ -41,6 +41,7 @@ EXPORTED = [
     "hocf_dma_put",
     "hocf_moe_route", "hocf_moe_route_workspace_bytes", "hocf_moe_route_bwd",
     "hocf_moe_slots", "hocf_moe_slots_workspace_bytes", "hocf_moe_combine", "hocf_moe_combine_bwd",
+    "hocf_gemv_w4", "hocf_w4_pack",
     "hocf_status_string", "hocf_last_error", "hocf_abi_version",
 ]
 
@@ -126,7 +127,10 @@ def lib():
         L.hocf_moe_slots_workspace_bytes.argtypes = [i64, i, i]
         L.hocf_moe_combine.argtypes = [i64, i, i, i64, i, i, vp, vp, vp, vp, vp, S, vp]
         L.hocf_moe_combine_bwd.argtypes = [i64, i, i, i64, i, i, vp, vp, vp, vp, vp, vp, vp, S, vp]
-        for f in ("hocf_moe_route", "hocf_moe_route_bwd", "hocf_moe_slots", "hocf_moe_combine", "hocf_moe_combine_bwd"):
+        L.hocf_gemv_w4.argtypes = [i] * 8 + [vp] * 6 + [S, vp]
+        L.hocf_w4_pack.argtypes = [i] * 4 + [vp] * 7
+        for f in ("hocf_moe_route", "hocf_moe_route_bwd", "hocf_moe_slots", "hocf_moe_combine", "hocf_moe_combine_bwd",
+                  "hocf_gemv_w4", "hocf_w4_pack"):
             getattr(L, f).restype = i
         for f in ("hocf_moe_route_workspace_bytes", "hocf_moe_slots_workspace_bytes"):
             getattr(L, f).restype = sz
@@ -353,6 +357,19 @@ def hocf_moe_combine_bwd(T, topk, N, R, dt, out_dt, rows, weights, dout, index, 
     """The gradients of the experts' rows and of the weights."""
     return lib().hocf_moe_combine_bwd(T, topk, N, R, dt, out_dt, ptr(rows), ptr(weights), ptr(dout), ptr(index),
                                       ptr(pair), ptr(drows), ptr(dweights), ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_gemv_w4(R, rows_per_x, E, e0, N, K, group, out_dt, x, experts, wq, scales, zeros, out, sync_,
+                 stream=None) -> int:
+    """Products of a few token rows with their experts' 4-bit weights."""
+    return lib().hocf_gemv_w4(R, rows_per_x, E, e0, N, K, group, out_dt, ptr(x), ptr(experts), ptr(wq), ptr(scales),
+                              ptr(zeros), ptr(out), ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_w4_pack(E, N, K, group, codes, scales, zeros, wq, scales_out, zeros_out, stream=None) -> int:
+    """4-bit codes, scales and zero points in the layout hocf_gemv_w4 reads."""
+    return lib().hocf_w4_pack(E, N, K, group, ptr(codes), ptr(scales), ptr(zeros), ptr(wq), ptr(scales_out),
+                              ptr(zeros_out), _stream(stream))
 
 
 def _host_i64(a):

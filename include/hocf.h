@@ -43,6 +43,10 @@
  *   hocf_moe_combine, hocf_moe_combine_bwd
  *                    the experts' rows -> the tokens' weighted sums, and the
  *                    gradients of the rows and the weights
+ *   hocf_gemv_w4, hocf_w4_pack
+ *                    products of a few token rows with their experts' 4-bit
+ *                    weights (the decode form of the experts' GEMM), and the
+ *                    weights' layout for it
  *
  * The method (SC24 abstract; mKernel, section on persistent kernels and
  * tile/chunk overlap): the workgroups of one kernel each finish an output
@@ -648,6 +652,46 @@ hocf_status hocf_moe_combine_bwd(int64_t T, int topk, int N, int64_t R, hocf_dty
                                  const void* rows, const float* weights, const void* dout, const int32_t* index,
                                  const int32_t* pair, void* drows, float* dweights, const hocf_sync* sync,
                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products of a few token rows with their experts' 4-bit weights.
+ *
+ *   out[r] = x[r / rows_per_x] . W_e,  e = experts[r] - e0,  r = 0 .. R-1
+ *   W_e[k][n] = scale[k / group][n] * (code[k][n] - zero[k / group][n])
+ * with codes 0 .. 15, fp32 accumulation and one rounding to out_dt.  For a
+ * decode step of T tokens: R = T * topk pairs, rows_per_x = topk for the up
+ * projection (the pairs of a token share its row), 1 for the down projection.
+ * Every weight that some row needs is read once for up to 16 of its rows.
+ * A row whose expert is not one of this rank's e0 .. e0+E-1 gets zeros, so
+ * that the ranks' outputs add up.
+ *
+ *   x        [R / rows_per_x][K] bf16
+ *   experts  [R] int32, or NULL: one matrix for every row (E = 1)
+ *   wq, scales, zeros (NULL: every zero is 8)   as hocf_w4_pack lays them out
+ *   out      [R][N] out_dt
+ * Supported: 0 <= R <= 1024 a multiple of rows_per_x; N and K multiples of 8
+ * up to 2^20; group 32, 64 or 128; out_dt F32 or BF16; E >= 1.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_gemv_w4(int R, int rows_per_x, int E, int e0, int N, int K, int group, hocf_dtype out_dt,
+                         const void* x, const int32_t* experts, const uint32_t* wq, const void* scales,
+                         const void* zeros, void* out, const hocf_sync* sync, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The layout of 4-bit weights for hocf_gemv_w4 (once, when they are loaded).
+ *
+ *   codes    [E][K][N] uint8, 0 .. 15 (the low four bits are taken)
+ *   scales   [E][G][N] bf16, G = ceil(K / group); zeros the same, or NULL
+ *   wq       [E][ceil(N/16)][ceil(K/128)][64][4] uint32: a block of 128 rows x
+ *            16 columns is one 1 KB load of a wave; piece q * 16 + n holds
+ *            column n's rows 32 t + 8 q + i (i < 8) in word t, row i in the four
+ *            bits from bit (3 + 16 (i mod 2) + 4 (i div 2)) mod 32, so that a
+ *            rotation and one mask give a pair of bf16 numbers 16 + code
+ *   scales_out, zeros_out   [E][ceil(N/16)][G][16] bf16
+ * Rows and columns beyond K and N hold zero codes, scales and zeros.
+ * Supported: N and K as for hocf_gemv_w4; zeros and zeros_out go together.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_w4_pack(int E, int N, int K, int group, const uint8_t* codes, const void* scales, const void* zeros,
+                         uint32_t* wq, void* scales_out, void* zeros_out, void* stream);
 
 /* ---------------------------------------------------------------------- */
 const char* hocf_status_string(hocf_status s); /* static string, never NULL */

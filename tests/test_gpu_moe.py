@@ -50,6 +50,8 @@ def near(got, want, size, dtype, steps):
     assert not np.isnan(got).any(), "unwritten (NaN) elements"
     room = HALF[dtype] * np.abs(want) + ref.rel_steps(steps) * size + 2.0 ** -126
     off = np.abs(got - want) - room
+    if off.size == 0:
+        return
     at = np.unravel_index(np.argmax(off), off.shape)
     assert off[at] <= 0, (at, got[at], want[at], room[at])
 
@@ -370,3 +372,101 @@ def test_combine_bad_index():
     assert h.status_value() == hocf.HOCF_ERR_BAD_INDEX
     assert torch.equal(h.drows, torch.tensor([1.0, 0, 0, 1])[:, None].expand(4, 8).cuda())
     assert h.dweights[0, 1] == 0 and h.dweights[1, 0] == 0
+
+
+# ------------------------------------------------------------------------------ 4-bit weights
+
+def w4_case(E, N, K, group, zeros, seed):
+    g = gen(seed)
+    groups = -(-K // group)
+    codes = torch.randint(0, 16, (E, K, N), generator=g, dtype=torch.uint8)
+    scales = (0.01 * (0.5 + torch.rand(E, groups, N, generator=g))).bfloat16()
+    z = torch.randint(0, 16, (E, groups, N), generator=g).bfloat16() if zeros else None
+    return codes, scales, z
+
+
+def w4_steps(K, group):
+    """Binary32 half steps, relative to the sum of |x| |scale| (|zero| + 31): the 32 products of a matrix instruction
+    in any order, even truncated (64), four chained (8), zero, scale and fold (8), and the sum over groups."""
+    return 80 + -(-K // group)
+
+
+def check_w4(R, per, E, e0, N, K, group, zeros, experts, out_dt, seed=0):
+    codes, scales, z = w4_case(E, N, K, group, zeros, seed)
+    x = torch.randn(R // per, K, generator=gen(seed + 1)).bfloat16()
+    wq, s, zz = bf.w4_pack(codes.cuda(), scales.cuda(), None if z is None else z.cuda(), group)
+    h = bf.GemvW4(R, per, E, e0, N, K, group, x.cuda(), dev(experts), wq, s, zz, out_dt=TYPES[out_dt])
+    out, size = ref.w4(x.float().numpy(), codes.numpy(), scales.float().numpy(), None if z is None else z.float().numpy(),
+                       None if experts is None else experts.numpy(), e0, per, group)
+    run(h)
+    near(h.out, out, size, out_dt, w4_steps(K, group))
+    first = h.out.clone()
+    run(h)
+    assert torch.equal(h.out, first), "another call, other bits"
+    return h
+
+
+@pytest.mark.parametrize("R,N,K", [(1, 8, 8), (1, 16, 128), (2, 40, 136), (5, 264, 1048), (16, 64, 512), (17, 72, 520),
+                                   (32, 128, 1024), (33, 24, 2056), (64, 520, 264), (65, 16, 384), (200, 48, 160),
+                                   (1, 4096, 4096), (3, 8, 8192)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_one_matrix(R, N, K, group):
+    say(f"w4 R={R} N={N} K={K} group={group}")
+    for zeros, out_dt in ((False, torch.bfloat16), (True, torch.float32)):
+        check_w4(R, 1, 1, 0, N, K, group, zeros, None, out_dt, R + K)
+
+
+@pytest.mark.parametrize("T,topk,E,e0,N,K", [
+    (1, 8, 64, 0, 48, 256), (1, 1, 8, 3, 16, 128), (4, 2, 4, 2, 40, 648), (16, 2, 32, 0, 264, 384), (20, 4, 3, 0, 24, 1160),
+    (40, 2, 2, 1, 72, 136), (128, 8, 5, 0, 16, 64)])
+@pytest.mark.parametrize("up", [True, False])
+def test_w4_experts(T, topk, E, e0, N, K, up):
+    say(f"w4 experts T={T} topk={topk} E={E} from {e0} N={N} K={K} up={up}")
+    e = choices(T, topk, E + e0, T + N, none=0.1, beyond=2).reshape(-1)
+    if T > 4:
+        e[3:3 + T] = e0                          # more rows of one expert than one tile holds
+    for group, zeros, out_dt in ((32, True, torch.bfloat16), (128, False, torch.float32)):
+        check_w4(T * topk, topk if up else 1, E, e0, N, K, group, zeros, e, out_dt, T)
+
+
+def test_w4_all_rows_of_other_ranks():
+    e = torch.tensor([7, -1, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    for E in (2, 6):
+        h = check_w4(4, 2, E, 8, 24, 128, 64, True, e, torch.float32)
+        assert not h.out.any()
+
+
+def test_w4_empty():
+    check_w4(0, 1, 1, 0, 16, 64, 32, False, None, torch.float32)
+    check_w4(3, 1, 1, 0, 16, 0, 32, False, None, torch.float32)
+
+
+def test_w4_padding_is_not_read_into_results():
+    """Codes, scales and zeros beyond K and N may hold anything."""
+    N, K, group = 24, 136, 32
+    codes, scales, z = w4_case(1, N, K, group, True, 5)
+    x = torch.randn(3, K, generator=gen(6)).bfloat16().cuda()
+    wq, s, zz = bf.w4_pack(codes.cuda(), scales.cuda(), z.cuda(), group)
+    clean = run(bf.GemvW4(3, 1, 1, 0, N, K, group, x, None, wq, s, zz)).out.clone()
+    wq[:, 1, :, 8::16] = -1
+    wq[:, 1, :, 9::16] = 0x55555555
+    wq[:, :, 1, 16:] = -1                        # rows from 136 on
+    wq[:, :, 1, :, 1:] = 0x7fffffff
+    for n in range(8, 16):
+        s[:, 1, :, n] = float("nan")
+        zz[:, 1, :, n] = float("inf")
+    assert torch.equal(run(bf.GemvW4(3, 1, 1, 0, N, K, group, x, None, wq, s, zz)).out, clean)
+
+
+def test_w4_pack_places():
+    """One code at a time lands in its four bits."""
+    N, K = 24, 264
+    for n, k in ((0, 0), (3, 1), (17, 130), (23, 263), (5, 39), (15, 127)):
+        codes = torch.zeros((1, K, N), dtype=torch.uint8)
+        codes[0, k, n] = 13
+        wq, _, _ = bf.w4_pack(codes.cuda(), torch.ones(1, 3, N).bfloat16().cuda(), None, 128)
+        at = wq.cpu().nonzero().tolist()
+        assert at == [[0, n // 16, k // 128, (k % 32 // 8) * 16 + n % 16, k % 128 // 32]]
+        bit = (3 + 16 * (k % 2) + 4 * (k % 8 // 2)) % 32
+        want = (13 << bit | 13 >> (32 - bit)) & 0xFFFFFFFF if bit else 13
+        assert int(wq.cpu()[tuple(at[0])]) & 0xFFFFFFFF == want

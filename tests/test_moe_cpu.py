@@ -186,6 +186,54 @@ def test_combine_bwd_accepts():
     valid(combine_bwd(R=0, rows=None, drows=None, pair=None))
 
 
+W4 = dict(R=8, rows_per_x=2, E=4, e0=0, N=64, K=256, group=64, out_dt=F32, x=addr(1), experts=addr(2), wq=addr(3),
+          scales=addr(4), zeros=addr(5), out=addr(6), s=None)
+
+
+def w4(**kw):
+    a = dict(W4, **kw)
+    s = a.pop("s")
+    return hocf.hocf_gemv_w4(*a.values(), sync() if s is None else s)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(R=-2), INVALID), (dict(rows_per_x=0), INVALID), (dict(rows_per_x=3), INVALID), (dict(E=0), INVALID),
+    (dict(e0=-1), INVALID), (dict(e0=2 ** 31 - 4), INVALID), (dict(N=60), INVALID), (dict(K=-8), INVALID),
+    (dict(K=12), INVALID), (dict(out_dt=5), INVALID), (dict(experts=None), INVALID), (dict(group=16), UNSUPPORTED),
+    (dict(group=256), UNSUPPORTED), (dict(R=1026), UNSUPPORTED), (dict(N=(1 << 20) + 8), UNSUPPORTED),
+    (dict(x=None), INVALID), (dict(wq=None), INVALID), (dict(scales=None), INVALID), (dict(out=None), INVALID),
+    (dict(zeros=addr(5) + 2), INVALID), (dict(out=addr(1)), INVALID), (dict(out=addr(3) + 1024), INVALID),
+    (dict(out=addr(2)), INVALID), (dict(s=sync(epoch=0)), INVALID),
+])
+def test_gemv_w4_rejects(kw, expect):
+    assert w4(**kw) == expect
+
+
+def test_gemv_w4_accepts():
+    assert w4(R=0, x=None, out=None) == OK and w4(N=0) == OK
+    valid(w4())
+    valid(w4(E=1, experts=None, zeros=None))
+    valid(w4(K=0, x=None, wq=None, scales=None, zeros=None))
+
+
+PACK = dict(E=2, N=64, K=256, group=64, codes=addr(1), scales=addr(2), zeros=addr(3), wq=addr(4), scales_out=addr(5),
+            zeros_out=addr(6))
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(E=0), INVALID), (dict(N=4), INVALID), (dict(K=4), INVALID), (dict(group=48), UNSUPPORTED),
+    (dict(K=(1 << 20) + 8), UNSUPPORTED), (dict(zeros=None), INVALID), (dict(zeros_out=None), INVALID),
+    (dict(codes=None), INVALID), (dict(scales_out=None), INVALID), (dict(wq=addr(4) + 4), INVALID),
+    (dict(wq=addr(1)), INVALID), (dict(scales_out=addr(2)), INVALID), (dict(zeros_out=addr(5)), INVALID),
+])
+def test_w4_pack_rejects(kw, expect):
+    assert hocf.hocf_w4_pack(*dict(PACK, **kw).values()) == expect
+
+
+def test_w4_pack_accepts():
+    assert hocf.hocf_w4_pack(*dict(PACK, K=0).values()) == OK
+
+
 def test_null_sync_is_refused():
     L = hocf.lib()
     none = ctypes.POINTER(hocf.hocf_sync)()
