@@ -10,6 +10,11 @@ constexpr int kRouteMaxE = 512;     // experts of one router row
 constexpr int kRouteMaxTopk = 16;   // choices of one token
 constexpr int kRouteMaxGroups = 64;
 
+// With counts, the router's workspace: word 0 counts the workgroups that have
+// finished, then kCountCopies tables of the experts' counts; all left zeroed.
+constexpr int kCountWords = 32, kCountCopies = 8;
+__host__ __device__ constexpr int route_count_stride(int E) { return (E + 31) / 32 * 32; }
+
 enum Score : int { kSoftmax = 0, kSigmoid = 1 };
 
 struct RouteArgs {
@@ -18,7 +23,7 @@ struct RouteArgs {
   int32_t* experts;    // [T][topk]
   float* weights;      // [T][topk]
   int32_t* counts;     // [E] or NULL
-  uint32_t* ws;        // with counts: [0] workgroups that have finished, [1 .. 1 + E) their counts; all left zeroed
+  uint32_t* ws;        // with counts
   int64_t T, ld;
   int E, topk, dt, score, n_group, topk_group, group_top, renorm;
   float scale;

@@ -37,7 +37,9 @@ extern "C" {
 
 /* ------------------------------------------------------------ routing */
 
-size_t hocf_moe_route_workspace_bytes(int E) { return E < 1 ? 0 : (size_t)(1 + E) * 4; }
+size_t hocf_moe_route_workspace_bytes(int E) {
+  return E < 1 || E > kRouteMaxE ? 0 : (size_t)(kCountWords + kCountCopies * route_count_stride(E)) * 4;
+}
 
 hocf_status hocf_moe_route(int64_t T, int E, int topk, hocf_dtype dt, const void* logits, int64_t ld,
                            const float* bias, hocf_score score, int n_group, int topk_group, int group_top,

@@ -4,161 +4,510 @@
 // Forward.  s = softmax(x) or sigmoid(x); v = s + bias; the best groups by
 // the sum of their one or two largest v; the topk largest v of what is left,
 // ties to the lower index; w = scale * s of the chosen, over their sum with
-// renorm.  One wave takes one token: lane l holds experts l, l + 64, ... .
-// The choice is the one that 64-bit scores make: v is computed and compared
-// in 64 bits, since two 32-bit sigmoids plus biases can swap near neighbours.
+// renorm.
+//
+// A token has LPT lanes (16, or 64 where a lane's share would be too long);
+// a lane holds a run of adjacent experts of one group.  The choice has to be
+// the one that 64-bit scores make, but 64-bit scores for every expert cost
+// more than everything else here, so it is made on 32-bit integer keys and
+// kept only where they decide it:
+//
+//   key = v in fixed point, its low log2(W) bits replaced by the slot within
+//         the lane (lower slot, larger key), so that a lane's keys differ and
+//         the largest key names its slot.
+//   Order = kByLogit: without a bias, v rises with x, and v = x * 2^26.
+//         Different keys (slots aside) mean the same order of x, so only
+//         equal keys are in doubt; equal keys of bf16 logits that are not
+//         tiny are equal logits.
+//   Order = kByScore: v = (s + bias) * 2^29, off by at most 6.5 * 2^-24 (a
+//         sigmoid in 32 bits: 4 half steps of 1, the sum one or two, the
+//         conversion one), so neighbours nearer than kDoubt are in doubt.
+//
+// A token in doubt (also: a key outside the fixed-point range, a sigmoid
+// beyond 20 where 64 bits begin to saturate) is chosen again in 64 bits by
+// the whole wave: about 0.3 % of tokens with biased sigmoids over 256
+// experts, 1e-5 without a bias.
+#include <algorithm>
+#include <climits>
+
 #include "moe.hpp"
+#include "publish.hpp"
 #include "sync.hpp"
 
 namespace hocf {
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512;
 constexpr int kRouteWaves = kRouteThreads / 64;
+
+enum Order : int { kByLogit, kByScore };
+constexpr float kLogitUnit = 0x1p26f, kScoreUnit = 0x1p29f;
+constexpr int kDoubt = 3 << 8;           // 1.5 * 2^-20 in units of 2^-29
+constexpr int kTiny = 1 << 13;           // logits below 2^-13: bf16 neighbours can share a key
+constexpr int kSaturated = 20 << 26;     // sigmoid(20) is 2e-9 from 1
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kVanished = -709.78f;    // a sigmoid below is 0 in 64 bits too
+constexpr float kMaxF = 3.402823466e38f;
+
+// How a token's experts lie on its lanes.
+struct Spread {
+  int lg;       // log2 of the lanes of one group
+  int run;      // experts of one lane
+  int size;     // experts of one group
+  int vec;      // elements of one load: 8, 4, 2 or 1
+};
+
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dppf(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v)));
+}
+// Reductions over the LPT lanes of a token: pairs, quads, halves and rows of
+// 16 by lane permutes, then across rows.
+template <int LPT>
+__device__ __forceinline__ int row_max(int v) {
+  v = max(v, dpp<0xB1>(v));
+  v = max(v, dpp<0x4E>(v));
+  v = max(v, dpp<0x141>(v));
+  v = max(v, dpp<0x140>(v));
+  if constexpr (LPT == 64) {
+    v = max(v, __shfl_xor(v, 16, 64));
+    v = max(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float row_maxf(float v) {
+  v = fmaxf(v, dppf<0xB1>(v));
+  v = fmaxf(v, dppf<0x4E>(v));
+  v = fmaxf(v, dppf<0x141>(v));
+  v = fmaxf(v, dppf<0x140>(v));
+  if constexpr (LPT == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    v = fmaxf(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float row_sum(float v) {
+  v += dppf<0xB1>(v);
+  v += dppf<0x4E>(v);
+  v += dppf<0x141>(v);
+  v += dppf<0x140>(v);
+  if constexpr (LPT == 64) {
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
+  }
+  return v;
+}
+
+// Toward zero, saturating (-inf gives INT_MIN).
+__device__ __forceinline__ int to_fixed(float f) {
+  int r;
+  __asm__("v_cvt_i32_f32 %0, %1" : "=v"(r) : "v"(f));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t apart(int a, int b) { return (uint32_t)max(a, b) - (uint32_t)min(a, b); }
+
+// A logit as the operators take it: NaN as -inf, +inf as the largest number.
+__device__ __forceinline__ float clean(float x) { return x > -INFINITY ? fminf(x, kMaxF) : -INFINITY; }
+
+// `cnt` logits from `at` of a row of E, the rest of the W as -inf.  Loads are
+// unconditional, inside the row.
+template <int DT, int W, int VE>
+__device__ __forceinline__ void load_run(const void* row, int at, int cnt, float (&x)[W]) {
+  if constexpr (VE <= W) {
+    const int last = max(cnt - VE, 0);
+    const int from = cnt > 0 ? at : 0;
+#pragma unroll
+    for (int i = 0; i < W; i += VE) {
+      const int o = from + min(i, last);
+      if constexpr (DT == kBF16) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + o;
+        if constexpr (VE == 8) {
+          const uint4 u = *reinterpret_cast<const uint4*>(p);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[i + k] = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+        } else if constexpr (VE == 4) {
+          const uint2 u = *reinterpret_cast<const uint2*>(p);
+          const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[i + k] = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+        } else if constexpr (VE == 2) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+          x[i] = __uint_as_float(w << 16);
+          x[i + 1] = __uint_as_float(w & 0xffff0000u);
+        } else {
+          x[i] = bf16_to_f32(*p);
+        }
+      } else {
+        const float* p = reinterpret_cast<const float*>(row) + o;
+        if constexpr (VE == 4) {
+          const float4 u = *reinterpret_cast<const float4*>(p);
+          x[i] = u.x; x[i + 1] = u.y; x[i + 2] = u.z; x[i + 3] = u.w;
+        } else if constexpr (VE == 2) {
+          const float2 u = *reinterpret_cast<const float2*>(p);
+          x[i] = u.x; x[i + 1] = u.y;
+        } else {
+          x[i] = *p;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = i < cnt ? clean(x[i]) : -INFINITY;
+  }
+}
+template <int DT, int W>
+__device__ __forceinline__ void load_logits(const void* row, int at, int cnt, int vec, float (&x)[W]) {
+  if (DT == kBF16 && vec == 8) load_run<DT, W, DT == kBF16 ? 8 : 4>(row, at, cnt, x);
+  else if (vec == 4) load_run<DT, W, 4>(row, at, cnt, x);
+  else if (vec == 2) load_run<DT, W, 2>(row, at, cnt, x);
+  else load_run<DT, W, 1>(row, at, cnt, x);
+}
+
+// Where a row of es-byte elements may be read (or written) `vec` at a time:
+// runs, groups and rows all start on a multiple of it.
+static int vector_width(int es, int w, int run, int size, int64_t ld) {
+  for (int v = 16 / es; v > 1; v /= 2)
+    if (v <= w && run % v == 0 && size % v == 0 && ld % v == 0) return v;
+  return 1;
+}
+
+__device__ __forceinline__ double wave_maxd(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v = fmax(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+// The choice of one token in 64 bits, by a whole wave (lane l: experts l, l +
+// 64, ...); picks to LDS, -1 where none is left.
+template <int DT>
+__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, int* picks) {
+  constexpr int V = kRouteMaxE / 64;
+  const int lane = threadIdx.x & 63;
+  const double kOff = -INFINITY;
+  double v[V];
+  uint32_t live = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 64 * i;
+    const float x = e < a.E ? clean(ld1<DT>(row, e)) : -INFINITY;
+    v[i] = x;
+    live |= (uint32_t)(x > -INFINITY) << i;
+  }
+  if (a.score == kSoftmax) {
+    double top = -(double)kMaxF, sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmax(top, v[i]);
+    top = wave_maxd(top);
+    for (int i = 0; i < V; ++i) {
+      v[i] = live >> i & 1 ? exp(v[i] - top) : 0.0;
+      sum += v[i];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = sum > 0.0 ? v[i] / sum : 0.0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 1.0 / (1.0 + exp(-v[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 64 * i;
+    const double w = v[i] + (a.bias && e < a.E ? (double)a.bias[e] : 0.0);
+    v[i] = live >> i & 1 && w > kOff ? w : kOff;
+  }
+  if (a.n_group > 1) {
+    const int size = a.E / a.n_group;
+    double of = kOff;  // lane g: group g's value
+    for (int g = 0; g < a.n_group; ++g) {
+      double m1 = kOff, m2 = kOff;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const double w = (uint32_t)(lane + 64 * i - g * size) < (uint32_t)size ? v[i] : kOff;
+        m2 = fmax(m2, fmin(m1, w));
+        m1 = fmax(m1, w);
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const double o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
+        m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+        m1 = fmax(m1, o1);
+      }
+      if (lane == g) of = a.group_top == 2 && m2 > kOff ? m1 + m2 : m1;
+    }
+    int ahead = 0;
+    for (int g = 0; g < a.n_group; ++g) {
+      const double other = __shfl(of, g, 64);
+      ahead += other > of || (other == of && g < lane);
+    }
+    const uint64_t kept = __ballot(lane < a.n_group && ahead < a.topk_group);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!(kept >> min((lane + 64 * i) / size, 63) & 1)) v[i] = kOff;
+  }
+  for (int j = 0; j < a.topk; ++j) {
+    double best = kOff;
+    int e = INT_MAX;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (v[i] > best) { best = v[i]; e = lane + 64 * i; }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const double ob = __shfl_xor(best, d, 64);
+      const int oe = __shfl_xor(e, d, 64);
+      if (ob > best || (ob == best && oe < e)) { best = ob; e = oe; }
+    }
+    if (!(best > kOff)) e = -1;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e == lane + 64 * i) v[i] = kOff;
+    if (lane == 0) picks[j] = e;
+  }
+}
 
 // Counts of chosen experts leave a workgroup's LDS histogram through the
 // workspace; the last workgroup to finish copies them out and zeroes the
-// words again.  `finish` is called by every thread of every workgroup.
+// words again.  Additions to one cache line go one after another (some 40 ns
+// each, measured), so there are kCountCopies tables and few workgroups.
 __device__ __forceinline__ void finish_counts(const RouteArgs& a, const uint32_t* s_hist, int* s_last) {
+  const int stride = route_count_stride(a.E);
   __syncthreads();
+  uint32_t* table = a.ws + kCountWords + (int)(blockIdx.x % kCountCopies) * stride;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-    if (s_hist[e]) __hip_atomic_fetch_add(&a.ws[1 + e], s_hist[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __threadfence();
+    if (s_hist[e]) __hip_atomic_fetch_add(&table[e], s_hist[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  wait_memory();  // this thread's additions are done
   __syncthreads();
   if (threadIdx.x == 0) {
-    const uint32_t prev = __hip_atomic_fetch_add(&a.ws[0], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t prev = __hip_atomic_fetch_add(&a.ws[0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const int last = prev == gridDim.x - 1;
     if (last) __hip_atomic_store(&a.ws[0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     *s_last = last;
   }
   __syncthreads();
   if (!uniform(*s_last)) return;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-    a.counts[e] = (int32_t)__hip_atomic_exchange(&a.ws[1 + e], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int c = 0; c < kCountCopies; ++c)
+      n += __hip_atomic_exchange(&a.ws[kCountWords + c * stride + e], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    a.counts[e] = (int32_t)n;
+  }
 }
 
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = fmax(v, __shfl_xor(v, d, 64));
-  return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
-}
-
-template <int DT>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
-  constexpr int V = kRouteMaxE / 64;
-  __shared__ double s_v[kRouteWaves][kRouteMaxE];
+template <int DT, int LPT, int W, Order ORDER>
+__global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Spread sp) {
+  constexpr int TPW = 64 / LPT;  // tokens of one wave
+  constexpr int kLow = INT_MIN + W;
+  __shared__ int s_pick[kRouteWaves * TPW][kRouteMaxTopk];
   __shared__ uint32_t s_hist[kRouteMaxE];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int E = a.E;
-  const double kOff = -INFINITY;
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) s_hist[e] = 0;
-  __syncthreads();
+  const int l = lane & (LPT - 1);
+  int* picks = s_pick[wave * TPW + lane / LPT];
+  if (a.counts) {
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_hist[e] = 0;
+    __syncthreads();
+  }
+  // this lane's run of experts
+  const int g = l >> sp.lg, in_group = (l & ((1 << sp.lg) - 1)) * sp.run;
+  const int cnt = g < a.n_group ? min(max(sp.size - in_group, 0), sp.run) : 0;
+  const int at = g * sp.size + in_group;
+  const bool softmax = a.score == kSoftmax;
+  float bias[W];
+  if constexpr (ORDER == kByScore) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) bias[i] = a.bias ? a.bias[min(at + i, a.E - 1)] : 0.0f;
+  }
 
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < a.T; t += (int64_t)gridDim.x * kRouteWaves) {
-    double s[V], v[V];
+  const int64_t step = (int64_t)gridDim.x * kRouteWaves * TPW;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * TPW; t0 < a.T; t0 += step) {
+    const int64_t t = min(t0 + lane / LPT, a.T - 1);
+    const bool own = t0 + lane / LPT < a.T;
+    const void* row = reinterpret_cast<const char*>(a.logits) + t * a.ld * (DT == kBF16 ? 2 : 4);
+    float x[W];
+    load_logits<DT, W>(row, at, cnt, sp.vec, x);
+
+    // softmax: the row's largest logit and sum
+    float top = 0.0f, inv = 1.0f;
+    if (softmax && (ORDER == kByScore || !a.renorm)) {
+      top = x[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      const float x = e < E ? ld1<DT>(a.logits, t * a.ld + e) : -INFINITY;
-      s[i] = x > -INFINITY ? (double)x : kOff;  // (NaN is off too)
+      for (int i = 1; i < W; ++i) top = fmaxf(top, x[i]);
+      top = fmaxf(row_maxf<LPT>(top), -kMaxF);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) sum += __builtin_amdgcn_exp2f((x[i] - top) * kLog2e);
+      sum = row_sum<LPT>(sum);
+      inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    uint32_t live = 0;
+    int k[W];
 #pragma unroll
-    for (int i = 0; i < V; ++i) live |= (uint32_t)(s[i] > kOff) << i;
-    if (a.score == kSoftmax) {
-      double top = kOff, sum = 0.0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) top = fmax(top, s[i]);
-      top = wave_max(top);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s[i] = !(live >> i & 1) ? 0.0 : s[i] == top ? 1.0 : exp(s[i] - top);
-        sum += s[i];
+    for (int i = 0; i < W; ++i) {
+      float v = x[i] * kLogitUnit;
+      if constexpr (ORDER == kByScore) {
+        const float s = softmax ? __builtin_amdgcn_exp2f((x[i] - top) * kLog2e) * inv
+                                : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[i] * kLog2e));
+        v = x[i] > -INFINITY ? (s + bias[i]) * kScoreUnit : -INFINITY;
       }
-      sum = wave_sum(sum);
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = live >> i & 1 ? 1.0 / (1.0 + exp(-s[i])) : 0.0;
+      k[i] = (to_fixed(v) & -W) | (W - 1 - i);
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      const double w = s[i] + (a.bias && e < E ? (double)a.bias[e] : 0.0);
-      v[i] = live >> i & 1 && w > kOff ? w : kOff;
-    }
+    bool doubt = false, kept = true;
     if (a.n_group > 1) {
-      const int S = E / a.n_group;
+      int m1 = INT_MIN, m2 = INT_MIN;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (lane + 64 * i < E) s_v[wave][lane + 64 * i] = v[i];
-      __builtin_amdgcn_wave_barrier();
-      __threadfence_block();
-      double m1 = kOff, m2 = kOff;  // lane g: the two largest of group g
-      if (lane < a.n_group)
-        for (int i = 0; i < S; ++i) {
-          const double w = s_v[wave][lane * S + i];
-          if (w > m1) { m2 = m1; m1 = w; } else if (w > m2) m2 = w;
-        }
-      const double of = a.group_top == 2 && m2 > kOff ? m1 + m2 : m1;
+      for (int i = 0; i < W; ++i) {
+        m2 = max(m2, min(m1, k[i]));
+        m1 = max(m1, k[i]);
+      }
+      for (int d = 1; d < 1 << sp.lg; d *= 2) {
+        const int o1 = __shfl_xor(m1, d, LPT), o2 = __shfl_xor(m2, d, LPT);
+        m2 = max(min(m1, o1), max(m2, o2));
+        m1 = max(m1, o1);
+      }
+      int of = m1 & -W;
+      if constexpr (ORDER == kByScore) {
+        const bool two = a.group_top == 2 && sp.size > 1;
+        of = (m1 >> 1) + (two && m2 > kLow ? m2 >> 1 : 0);
+        if (a.bias && (m1 <= kLow || (two && m2 <= kLow))) doubt = true;
+      }
+      doubt |= m1 >= (INT_MAX & -W);
+      if (g >= a.n_group) { of = INT_MIN; doubt = false; }
       int ahead = 0;
-      for (int g = 0; g < a.n_group; ++g) {
-        const double o = __shfl(of, g, 64);
-        ahead += o > of || (o == of && g < lane);
+      for (int o = 0; o < a.n_group; ++o) {
+        const int other = __shfl(of, o << sp.lg, LPT);
+        ahead += other > of || (other == of && o < g);
+        if (o != g && m1 > kLow) {
+          if constexpr (ORDER == kByScore) doubt |= apart(other, of) < kDoubt + 2 * W;
+          else if (other == of) doubt |= DT != kBF16 || abs(of) < kTiny;
+        }
       }
-      const uint64_t kept = __ballot(lane < a.n_group && ahead < a.topk_group);
+      kept = ahead < a.topk_group;
+      doubt = row_max<LPT>(doubt);
+    }
+    int before = INT_MAX;
+    bool low = false;
+    for (int j = 0; j <= a.topk; ++j) {
+      int lm = k[0];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        if (e < E && !(kept >> (e / S) & 1)) v[i] = kOff;
+      for (int i = 1; i < W; ++i) lm = max(lm, k[i]);
+      lm = kept ? lm : INT_MIN;
+      const int value = lm & -W;  // equal values go to the lower lane, whatever their slots
+      const int m = row_max<LPT>(value);
+      // neighbours in doubt (the first left out among them)
+      if (m >= kLow) {
+        if constexpr (ORDER == kByScore) doubt |= j > 0 && apart(before, m) < kDoubt + 2 * W;
+        else doubt |= j > 0 && before == m && (DT != kBF16 || abs(m) < kTiny);
+        doubt |= m >= (INT_MAX & -W) || (ORDER == kByLogit && !softmax && m > kSaturated);
+      } else {
+        low = true;
       }
-      __builtin_amdgcn_wave_barrier();
+      if (j == a.topk) break;
+      before = m;
+      const uint64_t b = __ballot(value == m);
+      const uint32_t half = LPT == 64 || lane < 32 ? (uint32_t)b : (uint32_t)(b >> 32);
+      const int first = LPT == 64 ? __builtin_ctzll(b) : __builtin_ctz((half >> (lane & 16)) & 0xffffu);
+      const bool winner = l == first;
+      if (winner) picks[j] = m >= kLow ? at + (W - 1 - (lm & (W - 1))) : -1;
+      const int gone = winner ? lm : INT_MAX;
+#pragma unroll
+      for (int i = 0; i < W; ++i) k[i] = k[i] == gone ? INT_MIN : k[i];
     }
-    double total = 0.0, mine = 0.0;
-    int my_e = -1;
-    for (int j = 0; j < a.topk; ++j) {
-      double best = kOff, bs = 0.0;
-      int at = INT_MAX;
+    // below the keys' range: switched off, unless a live one is down there
+    if (low) {
+      if (ORDER == kByScore) doubt |= a.bias != nullptr;
+      else {
+        int down = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (v[i] > best) { best = v[i]; bs = s[i]; at = lane + 64 * i; }
-#pragma unroll
-      for (int d = 32; d; d >>= 1) {
-        const double ob = __shfl_xor(best, d, 64), os = __shfl_xor(bs, d, 64);
-        const int oa = __shfl_xor(at, d, 64);
-        if (ob > best || (ob == best && oa < at)) { best = ob; bs = os; at = oa; }
+        for (int i = 0; i < W; ++i) down |= x[i] > -INFINITY && x[i] <= -31.0f;
+        doubt |= row_max<LPT>(down) != 0;
       }
-      if (!(best > kOff)) { at = -1; bs = 0.0; }
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (at == lane + 64 * i) v[i] = kOff;
-      total += bs;
-      if (lane == j) { mine = bs; my_e = at; }
     }
-    if (lane < a.topk) {
-      const double w = !a.renorm ? mine : total > 0.0 ? mine / total : 0.0;
-      a.experts[t * a.topk + lane] = my_e;
-      a.weights[t * a.topk + lane] = (float)(w * (double)a.scale);
-      if (a.counts && my_e >= 0) atomicAdd(&s_hist[my_e], 1u);
+    for (uint64_t todo = __ballot(doubt); todo;) {
+      const int r = __builtin_ctzll(todo) / LPT;
+      todo &= LPT == 64 ? 0 : ~(0xffffull << (r * 16));
+      const int64_t tr = min(t0 + r, a.T - 1);
+      choose64<DT>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4), s_pick[wave * TPW + r]);
     }
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+
+    // lane j: place j.  sigmoid(x) e^-c = e^(min(x, 0) - c) / (1 + e^-|x|); with
+    // renorm, c is the largest exponent, so that the sum cannot vanish
+    const bool place = l < a.topk;
+    const int e = place ? picks[l] : -1;
+    const float xe = e >= 0 ? clean(ld1<DT>(row, e)) : -INFINITY;
+    float up = softmax ? xe : fminf(xe, 0.0f);
+    float c = softmax ? top : 0.0f;
+    if (a.renorm) c = fmaxf(row_maxf<LPT>(up), -kMaxF);
+    float w = e >= 0 && (softmax || xe >= kVanished) ? expf(up - c) : 0.0f;
+    if (!softmax) w /= 1.0f + expf(-fabsf(xe));
+    if (a.renorm) {
+      const float sum = row_sum<LPT>(w);
+      inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    }
+    if (place && own) {
+      a.experts[t * a.topk + l] = e;
+      a.weights[t * a.topk + l] = e >= 0 ? w * inv * a.scale : 0.0f;
+      if (a.counts && e >= 0) atomicAdd(&s_hist[e], 1u);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
   if (a.counts) finish_counts(a, s_hist, &s_last);
 }
 
-int launch_moe_route(const RouteArgs& a, hipStream_t s) {
-  auto kern = a.dt == kBF16 ? &route_kernel<kBF16> : &route_kernel<kF32>;
+template <int DT, int LPT, int W>
+static int launch_route(const RouteArgs& a, const Spread& s0, hipStream_t s) {
+  Spread sp = s0;
+  sp.vec = vector_width(DT == kBF16 ? 2 : 4, W, sp.run, sp.size, a.ld);
+  const bool by_score = a.bias || (a.n_group > 1 && a.group_top == 2);
+  auto kern = by_score ? &route_kernel<DT, LPT, W, kByScore> : &route_kernel<DT, LPT, W, kByLogit>;
   int grid = 0;
-  hipError_t e = persistent_grid(reinterpret_cast<const void*>(kern), kRouteThreads,
-                                 (a.T + kRouteWaves - 1) / kRouteWaves, &grid);
+  constexpr int64_t per = kRouteWaves * (64 / LPT);
+  const hipError_t e = persistent_grid(reinterpret_cast<const void*>(kern), kRouteThreads, (a.T + per - 1) / per, &grid,
+                                       a.counts ? 512 : 0);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(kRouteThreads), 0, s, a);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(kRouteThreads), 0, s, a, sp);
   return hipGetLastError();
+}
+
+static int pow2_at_least(int n) {
+  int p = 1;
+  while (p < n) p *= 2;
+  return p;
+}
+
+template <int DT>
+static int launch_route_dt(const RouteArgs& a, hipStream_t s) {
+  Spread sp{};
+  sp.size = a.E / a.n_group;
+  const int groups = pow2_at_least(a.n_group);
+  for (const int lpt : {16, 64}) {
+    if (groups > lpt) continue;
+    const int lanes = lpt / groups;
+    sp.lg = __builtin_ctz(lanes);
+    sp.run = (sp.size + lanes - 1) / lanes;
+    if (lpt == 16) {
+      if (sp.run <= 1) return launch_route<DT, 16, 1>(a, sp, s);
+      if (sp.run <= 2) return launch_route<DT, 16, 2>(a, sp, s);
+      if (sp.run <= 4) return launch_route<DT, 16, 4>(a, sp, s);
+      if (sp.run <= 8) return launch_route<DT, 16, 8>(a, sp, s);
+      if (sp.run <= 16) return launch_route<DT, 16, 16>(a, sp, s);
+    } else {
+      if (sp.run <= 8) return launch_route<DT, 64, 8>(a, sp, s);
+      if (sp.run <= 16) return launch_route<DT, 64, 16>(a, sp, s);
+    }
+  }
+  return kNoKernel;
+}
+
+int launch_moe_route(const RouteArgs& a, hipStream_t s) {
+  return a.dt == kBF16 ? launch_route_dt<kBF16>(a, s) : launch_route_dt<kF32>(a, s);
 }
 
 // Backward.  With p the softmax of the row and g_j = scale * dw_j:
@@ -169,100 +518,128 @@ int launch_moe_route(const RouteArgs& a, hipStream_t s) {
 //                        l = x up to a constant for a softmax, log s for a
 //                        sigmoid (dl/dx = 1 - s); zero elsewhere
 // The log-score form keeps renorm exact where every chosen s underflows.
-// Sums over j run in the order of the places, so results do not vary.
-__device__ __forceinline__ float wave_maxf(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
-}
-__device__ __forceinline__ float wave_sumf(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
-}
+// A token has 16 lanes; lane j holds place j, and its contribution reaches
+// the lane that holds expert e_j through an LDS row of the token.
+constexpr int kBwdThreads = 256;
+constexpr int kBwdTokens = kBwdThreads / 16;
 
-template <int DT>
-__global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(RouteBwdArgs a) {
-  constexpr int V = kRouteMaxE / 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int E = a.E;
-  const float kOff = -INFINITY;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < a.T; t += (int64_t)gridDim.x * kRouteWaves) {
-    // lane j: place j
-    int e_j = -1;
-    float x_j = kOff, g_j = 0.0f;
-    if (lane < a.topk) {
-      e_j = a.experts[t * a.topk + lane];
-      if (e_j < -1 || e_j >= E) { report_status(a.sync, kErrBadIndex); e_j = -1; }
-      if (e_j >= 0) {
-        const float x = ld1<DT>(a.logits, t * a.ld + e_j);
-        if (x > kOff) { x_j = x; g_j = a.dweights[t * a.topk + lane] * a.scale; }
-        else e_j = -1;  // a switched-off logit has no gradient
-      }
-    }
-    const bool dense = a.score == kSoftmax && !a.renorm;
-    float p[V];
-    float top = kOff, inv = 0.0f;
-    if (dense) {
+template <int DT, int W>
+__device__ __forceinline__ void store_run(void* row, int at, int cnt, int vec, const float (&d)[W]) {
+  if (W >= 4 && vec >= 4) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        const float x = e < E ? ld1<DT>(a.logits, t * a.ld + e) : kOff;
-        p[i] = x > kOff ? x : kOff;
-        top = fmaxf(top, p[i]);
-      }
-      top = wave_maxf(top);
-      float sum = 0.0f;
+    for (int i = 0; i + 3 < W; i += 4)
+      if (i < cnt) st4<DT>(row, at + i, floatx4{d[i], d[i + 1], d[i + 2], d[i + 3]});
+  } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        p[i] = !(p[i] > kOff) ? 0.0f : p[i] == top ? 1.0f : expf(p[i] - top);
-        sum += p[i];
-      }
-      sum = wave_sumf(sum);
-      inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    }
-    // lane j: the gradient of log p_j (dense) or of x_j (sparse)
-    float d_j = 0.0f, mean = 0.0f;
-    const float s_j = 1.0f / (1.0f + expf(-x_j)), c_j = 1.0f / (1.0f + expf(x_j));  // sigmoid, 1 - sigmoid
-    if (dense) {
-      const float p_j = e_j < 0 ? 0.0f : x_j == top ? inv : expf(x_j - top) * inv;
-      d_j = g_j;
-      mean = wave_sumf(e_j >= 0 ? p_j * g_j : 0.0f);
-    } else if (a.renorm) {
-      const float l = e_j < 0 ? kOff : a.score == kSoftmax ? x_j : fminf(x_j, 0.0f) - log1pf(expf(-fabsf(x_j)));
-      const float m = wave_maxf(l);
-      float r = !(l > kOff) ? 0.0f : l == m ? 1.0f : expf(l - m);
-      const float sum = wave_sumf(r);
-      r = sum > 0.0f ? r / sum : 0.0f;
-      d_j = r * (g_j - wave_sumf(r * g_j));
-      if (a.score == kSigmoid) d_j *= c_j;
-      if (e_j < 0) d_j = 0.0f;
-    } else {
-      d_j = e_j < 0 ? 0.0f : g_j * s_j * c_j;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      float d = 0.0f;
-      for (int j = 0; j < a.topk; ++j) {
-        const int ej = __shfl(e_j, j, 64);
-        const float dj = __shfl(d_j, j, 64);
-        if (ej == e) d += dj;
-      }
-      if (dense) d = p[i] > 0.0f ? p[i] * inv * (d - mean) : 0.0f;
-      if (e < E) st1<DT>(a.dlogits, t * E + e, d);
-    }
+    for (int i = 0; i < W; ++i)
+      if (i < cnt) st1<DT>(row, at + i, d[i]);
   }
 }
 
-int launch_moe_route_bwd(const RouteBwdArgs& a, hipStream_t s) {
-  auto kern = a.dt == kBF16 ? &route_bwd_kernel<kBF16> : &route_bwd_kernel<kF32>;
+template <int DT, int W>
+__global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(RouteBwdArgs a, int run, int vec, int vec_out) {
+  __shared__ __attribute__((aligned(16))) float s_d[kBwdTokens][16 * W];
+  constexpr int es = DT == kBF16 ? 2 : 4;
+  const int l = threadIdx.x & 15;
+  float* mine = s_d[threadIdx.x >> 4];
+  const int at = l * run, cnt = min(max(a.E - at, 0), run);
+  const int per_run = 65536 / run + 1;  // (exact for e < 512, run <= 32)
+  const bool softmax = a.score == kSoftmax, dense = softmax && !a.renorm;
+  const int64_t step = (int64_t)gridDim.x * kBwdTokens;
+  for (int64_t t0 = (int64_t)blockIdx.x * kBwdTokens + (threadIdx.x >> 6) * 4; t0 < a.T; t0 += step) {
+    const int64_t tt = t0 + (threadIdx.x >> 4 & 3), t = min(tt, a.T - 1);
+    const char* row = reinterpret_cast<const char*>(a.logits) + t * a.ld * es;
+    float p[W];
+    if (dense) load_logits<DT, W>(row, at, cnt, vec, p);
+    // lane j: place j
+    int e = -1;
+    float x = -INFINITY, g = 0.0f;
+    if (l < a.topk) {
+      e = a.experts[t * a.topk + l];
+      if (e < -1 || e >= a.E) { report_status(a.sync, kErrBadIndex); e = -1; }
+      if (e >= 0) {
+        x = clean(ld1<DT>(row, e));
+        if (x > -INFINITY) g = a.dweights[t * a.topk + l] * a.scale;
+        if (x == -INFINITY || (!softmax && x < kVanished)) e = -1;  // a switched-off logit has no gradient
+      }
+    }
+    float top = 0.0f, inv = 0.0f, mean = 0.0f, d = 0.0f;
+    if (dense) {
+      top = p[0];
+#pragma unroll
+      for (int i = 1; i < W; ++i) top = fmaxf(top, p[i]);
+      top = fmaxf(row_maxf<16>(top), -kMaxF);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        p[i] = __builtin_amdgcn_exp2f((p[i] - top) * kLog2e);
+        sum += p[i];
+      }
+      sum = row_sum<16>(sum);
+      inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      d = g;
+      mean = row_sum<16>(e >= 0 ? __builtin_amdgcn_exp2f((x - top) * kLog2e) * inv * g : 0.0f);
+    } else {
+      const float far = expf(-fabsf(x)), s0 = 1.0f / (1.0f + far);  // sigmoid(|x|)
+      const float s1 = far * s0;                                    // 1 - sigmoid(|x|)
+      const float s = x >= 0.0f ? s0 : s1, c = x >= 0.0f ? s1 : s0; // sigmoid(x), 1 - sigmoid(x)
+      if (a.renorm) {
+        const float up = softmax ? x : fminf(x, 0.0f);
+        const float most = fmaxf(row_maxf<16>(e >= 0 ? up : -INFINITY), -kMaxF);
+        float r = e >= 0 ? expf(up - most) * (softmax ? 1.0f : s0) : 0.0f;
+        const float sum = row_sum<16>(r);
+        r = sum > 0.0f ? r / sum : 0.0f;
+        d = r * (g - row_sum<16>(r * g)) * (softmax ? 1.0f : c);
+      } else {
+        d = g * s * c;
+      }
+    }
+    // to the lanes that hold the experts (places that name one expert twice add up)
+#pragma unroll
+    for (int i = 0; i < W; ++i) mine[i * 16 + l] = 0.0f;
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    const int holder = e * per_run >> 16;  // e / run
+    if (e >= 0) atomicAdd(&mine[(e - holder * run) * 16 + holder], d);
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    float o[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      o[i] = mine[i * 16 + l];
+      if (dense) o[i] = p[i] > 0.0f ? p[i] * inv * (o[i] - mean) : 0.0f;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (tt < a.T) store_run<DT, W>(reinterpret_cast<char*>(a.dlogits) + t * a.E * es, at, cnt, vec_out, o);
+  }
+}
+
+template <int DT, int W>
+static int launch_bwd(const RouteBwdArgs& a, hipStream_t s) {
+  const int run = (a.E + 15) / 16, es = DT == kBF16 ? 2 : 4;
+  const int vec = vector_width(es, W, run, a.E, a.ld), vec_out = vector_width(es, W, run, a.E, a.E);
+  auto kern = &route_bwd_kernel<DT, W>;
   int grid = 0;
-  hipError_t e = persistent_grid(reinterpret_cast<const void*>(kern), kRouteThreads,
-                                 (a.T + kRouteWaves - 1) / kRouteWaves, &grid);
+  const hipError_t e = persistent_grid(reinterpret_cast<const void*>(kern), kBwdThreads,
+                                       (a.T + kBwdTokens - 1) / kBwdTokens, &grid);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(kRouteThreads), 0, s, a);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(kBwdThreads), 0, s, a, run, vec, vec_out);
   return hipGetLastError();
+}
+
+template <int DT>
+static int launch_bwd_dt(const RouteBwdArgs& a, hipStream_t s) {
+  const int run = (a.E + 15) / 16;
+  if (run <= 1) return launch_bwd<DT, 1>(a, s);
+  if (run <= 2) return launch_bwd<DT, 2>(a, s);
+  if (run <= 4) return launch_bwd<DT, 4>(a, s);
+  if (run <= 8) return launch_bwd<DT, 8>(a, s);
+  if (run <= 16) return launch_bwd<DT, 16>(a, s);
+  return launch_bwd<DT, 32>(a, s);
+}
+
+int launch_moe_route_bwd(const RouteBwdArgs& a, hipStream_t s) {
+  return a.dt == kBF16 ? launch_bwd_dt<kBF16>(a, s) : launch_bwd_dt<kF32>(a, s);
 }
 
 }  // namespace hocf

@@ -550,7 +550,7 @@ hocf_status hocf_dma_put(int n, const void* const* src, void* const* dst, const 
  * Equal values rank by the lower index, among groups and among experts.  A
  * logit of -inf or NaN switches its expert off for that token; a token with
  * fewer than topk experts left gets expert -1 and weight 0 in the last
- * places.  Logits of +inf share a softmax among themselves.  A bias must be
+ * places.  A logit of +inf counts as the largest finite number.  A bias must be
  * finite (an expert whose v is NaN or -inf is never chosen).
  *
  *   logits   [T][ld] dt, the first E of each row (E <= ld <= 2^24)
