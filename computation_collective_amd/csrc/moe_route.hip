@@ -184,90 +184,74 @@ __device__ __forceinline__ double wave_maxd(double v) {
 }
 
 // The choice of one token in 64 bits, by a whole wave (lane l: experts l, l +
-// 64, ...); picks to LDS, -1 where none is left.
+// 64, ...); picks to LDS, -1 where none is left.  Scores stay in LDS and loops
+// are not unrolled: this path is rare, and registers held for it would cost
+// the others their occupancy.
 template <int DT>
-__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, int* picks) {
-  constexpr int V = kRouteMaxE / 64;
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, double* v, int* picks) {
+  const int lane = threadIdx.x & 63, E = a.E;
   const double kOff = -INFINITY;
-  double v[V];
-  uint32_t live = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 64 * i;
-    const float x = e < a.E ? clean(ld1<DT>(row, e)) : -INFINITY;
-    v[i] = x;
-    live |= (uint32_t)(x > -INFINITY) << i;
-  }
+  double top = -(double)kMaxF, sum = 0.0;
   if (a.score == kSoftmax) {
-    double top = -(double)kMaxF, sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) top = fmax(top, v[i]);
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) top = fmax(top, (double)clean(ld1<DT>(row, e)));
     top = wave_maxd(top);
-    for (int i = 0; i < V; ++i) {
-      v[i] = live >> i & 1 ? exp(v[i] - top) : 0.0;
-      sum += v[i];
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = sum > 0.0 ? v[i] / sum : 0.0;
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 1.0 / (1.0 + exp(-v[i]));
+  }
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) {
+    const double x = clean(ld1<DT>(row, e));
+    const double p = exp(a.score == kSoftmax ? x - top : -x);
+    v[e] = x > kOff ? p : kOff;
+    sum += x > kOff ? p : 0.0;
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 64 * i;
-    const double w = v[i] + (a.bias && e < a.E ? (double)a.bias[e] : 0.0);
-    v[i] = live >> i & 1 && w > kOff ? w : kOff;
+  for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) {
+    const double p = v[e], s = a.score == kSoftmax ? p / sum : 1.0 / (1.0 + p);
+    const double w = s + (a.bias ? (double)a.bias[e] : 0.0);
+    v[e] = p > kOff && w > kOff ? w : kOff;
   }
+  __threadfence_block();
+  __builtin_amdgcn_wave_barrier();
   if (a.n_group > 1) {
-    const int size = a.E / a.n_group;
-    double of = kOff;  // lane g: group g's value
-    for (int g = 0; g < a.n_group; ++g) {
-      double m1 = kOff, m2 = kOff;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const double w = (uint32_t)(lane + 64 * i - g * size) < (uint32_t)size ? v[i] : kOff;
+    const int size = E / a.n_group;
+    double m1 = kOff, m2 = kOff;  // lane g: the two largest of group g
+    if (lane < a.n_group)
+#pragma unroll 1
+      for (int i = 0; i < size; ++i) {
+        const double w = v[lane * size + i];
         m2 = fmax(m2, fmin(m1, w));
         m1 = fmax(m1, w);
       }
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const double o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
-        m2 = fmax(fmin(m1, o1), fmax(m2, o2));
-        m1 = fmax(m1, o1);
-      }
-      if (lane == g) of = a.group_top == 2 && m2 > kOff ? m1 + m2 : m1;
-    }
+    const double of = a.group_top == 2 && m2 > kOff ? m1 + m2 : m1;
     int ahead = 0;
+#pragma unroll 1
     for (int g = 0; g < a.n_group; ++g) {
       const double other = __shfl(of, g, 64);
       ahead += other > of || (other == of && g < lane);
     }
     const uint64_t kept = __ballot(lane < a.n_group && ahead < a.topk_group);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!(kept >> min((lane + 64 * i) / size, 63) & 1)) v[i] = kOff;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64)
+      if (!(kept >> (e / size) & 1)) v[e] = kOff;
   }
+#pragma unroll 1
   for (int j = 0; j < a.topk; ++j) {
     double best = kOff;
-    int e = INT_MAX;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (v[i] > best) { best = v[i]; e = lane + 64 * i; }
+    int at = INT_MAX;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64)
+      if (v[e] > best) { best = v[e]; at = e; }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
       const double ob = __shfl_xor(best, d, 64);
-      const int oe = __shfl_xor(e, d, 64);
-      if (ob > best || (ob == best && oe < e)) { best = ob; e = oe; }
+      const int oa = __shfl_xor(at, d, 64);
+      if (ob > best || (ob == best && oa < at)) { best = ob; at = oa; }
     }
-    if (!(best > kOff)) e = -1;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e == lane + 64 * i) v[i] = kOff;
-    if (lane == 0) picks[j] = e;
+    if (!(best > kOff)) at = -1;
+    if (at >= 0 && (at & 63) == lane) v[at] = kOff;
+    if (lane == 0) picks[j] = at;
   }
 }
 
@@ -304,6 +288,7 @@ template <int DT, int LPT, int W, Order ORDER>
 __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Spread sp) {
   constexpr int TPW = 64 / LPT;  // tokens of one wave
   constexpr int kLow = INT_MIN + W;
+  __shared__ double s_v[kRouteWaves][kRouteMaxE];
   __shared__ int s_pick[kRouteWaves * TPW][kRouteMaxTopk];
   __shared__ uint32_t s_hist[kRouteMaxE];
   __shared__ int s_last;
@@ -432,7 +417,8 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
       const int r = __builtin_ctzll(todo) / LPT;
       todo &= LPT == 64 ? 0 : ~(0xffffull << (r * 16));
       const int64_t tr = min(t0 + r, a.T - 1);
-      choose64<DT>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4), s_pick[wave * TPW + r]);
+      choose64<DT>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4), s_v[wave],
+                   s_pick[wave * TPW + r]);
     }
     __threadfence_block();
     __builtin_amdgcn_wave_barrier();
