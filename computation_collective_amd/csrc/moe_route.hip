@@ -53,7 +53,6 @@ struct Spread {
   int lg;       // log2 of the lanes of one group
   int run;      // experts of one lane
   int size;     // experts of one group
-  int vec;      // elements of one load: 8, 4, 2 or 1
 };
 
 template <int CTRL>
@@ -115,66 +114,39 @@ __device__ __forceinline__ uint32_t apart(int a, int b) { return (uint32_t)max(a
 // A logit as the operators take it: NaN as -inf, +inf as the largest number.
 __device__ __forceinline__ float clean(float x) { return x > -INFINITY ? fminf(x, kMaxF) : -INFINITY; }
 
-// `cnt` logits from `at` of a row of E, the rest of the W as -inf.  Loads are
-// unconditional, inside the row.
-template <int DT, int W, int VE>
-__device__ __forceinline__ void load_run(const void* row, int at, int cnt, float (&x)[W]) {
-  if constexpr (VE <= W) {
-    const int last = max(cnt - VE, 0);
-    const int from = cnt > 0 ? at : 0;
-#pragma unroll
-    for (int i = 0; i < W; i += VE) {
-      const int o = from + min(i, last);
-      if constexpr (DT == kBF16) {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + o;
-        if constexpr (VE == 8) {
-          const uint4 u = *reinterpret_cast<const uint4*>(p);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[i + k] = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
-        } else if constexpr (VE == 4) {
-          const uint2 u = *reinterpret_cast<const uint2*>(p);
-          const uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[i + k] = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
-        } else if constexpr (VE == 2) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-          x[i] = __uint_as_float(w << 16);
-          x[i + 1] = __uint_as_float(w & 0xffff0000u);
-        } else {
-          x[i] = bf16_to_f32(*p);
-        }
-      } else {
-        const float* p = reinterpret_cast<const float*>(row) + o;
-        if constexpr (VE == 4) {
-          const float4 u = *reinterpret_cast<const float4*>(p);
-          x[i] = u.x; x[i + 1] = u.y; x[i + 2] = u.z; x[i + 3] = u.w;
-        } else if constexpr (VE == 2) {
-          const float2 u = *reinterpret_cast<const float2*>(p);
-          x[i] = u.x; x[i + 1] = u.y;
-        } else {
-          x[i] = *p;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = i < cnt ? clean(x[i]) : -INFINITY;
-  }
-}
-template <int DT, int W>
-__device__ __forceinline__ void load_logits(const void* row, int at, int cnt, int vec, float (&x)[W]) {
-  if (DT == kBF16 && vec == 8) load_run<DT, W, DT == kBF16 ? 8 : 4>(row, at, cnt, x);
-  else if (vec == 4) load_run<DT, W, 4>(row, at, cnt, x);
-  else if (vec == 2) load_run<DT, W, 2>(row, at, cnt, x);
-  else load_run<DT, W, 1>(row, at, cnt, x);
+// A lane's experts: `cnt` from expert `at` on, held in the W slots from expert
+// `from` on (where at + W would leave the row, the slots start earlier, so
+// that one load of W logits stays inside it; slots outside [lo, lo + cnt) are
+// other lanes').
+struct Run {
+  int from, lo, cnt;
+  __device__ __forceinline__ bool has(int i) const { return (uint32_t)(i - lo) < (uint32_t)cnt; }
+};
+template <int W>
+__device__ __forceinline__ Run run_at(int at, int cnt, int E) {
+  const int from = max(0, min(at, E - W));
+  return Run{from, at - from, cnt};
 }
 
-// Where a row of es-byte elements may be read (or written) `vec` at a time:
-// runs, groups and rows all start on a multiple of it.
-static int vector_width(int es, int w, int run, int size, int64_t ld) {
-  for (int v = 16 / es; v > 1; v /= 2)
-    if (v <= w && run % v == 0 && size % v == 0 && ld % v == 0) return v;
-  return 1;
+// W adjacent elements as fp32, at any alignment.
+template <int DT, int W>
+__device__ __forceinline__ void load_row(const void* p, float (&x)[W]) {
+  if constexpr (DT == kBF16) {
+    uint16_t u[W];
+    __builtin_memcpy(u, p, sizeof u);
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = bf16_to_f32(u[i]);
+  } else {
+    __builtin_memcpy(x, p, sizeof x);
+  }
+}
+
+// A lane's logits, -inf in the slots that are not its own.
+template <int DT, int W>
+__device__ __forceinline__ void load_logits(const char* row, const Run& r, float (&x)[W]) {
+  load_row<DT, W>(row + r.from * (DT == kBF16 ? 2 : 4), x);
+#pragma unroll
+  for (int i = 0; i < W; ++i) x[i] = r.has(i) ? clean(x[i]) : -INFINITY;
 }
 
 __device__ __forceinline__ double wave_maxd(double v) {
@@ -292,7 +264,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
   __shared__ int s_pick[kRouteWaves * TPW][kRouteMaxTopk];
   __shared__ uint32_t s_hist[kRouteMaxE];
   __shared__ int s_last;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int l = lane & (LPT - 1);
   int* picks = s_pick[wave * TPW + lane / LPT];
   if (a.counts) {
@@ -302,21 +274,21 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
   // this lane's run of experts
   const int g = l >> sp.lg, in_group = (l & ((1 << sp.lg) - 1)) * sp.run;
   const int cnt = g < a.n_group ? min(max(sp.size - in_group, 0), sp.run) : 0;
-  const int at = g * sp.size + in_group;
+  const Run mine = run_at<W>(cnt > 0 ? g * sp.size + in_group : 0, cnt, a.E);
   const bool softmax = a.score == kSoftmax;
   float bias[W];
   if constexpr (ORDER == kByScore) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) bias[i] = a.bias ? a.bias[min(at + i, a.E - 1)] : 0.0f;
+    for (int i = 0; i < W; ++i) bias[i] = a.bias ? a.bias[min(mine.from + i, a.E - 1)] : 0.0f;
   }
 
   const int64_t step = (int64_t)gridDim.x * kRouteWaves * TPW;
   for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * TPW; t0 < a.T; t0 += step) {
     const int64_t t = min(t0 + lane / LPT, a.T - 1);
     const bool own = t0 + lane / LPT < a.T;
-    const void* row = reinterpret_cast<const char*>(a.logits) + t * a.ld * (DT == kBF16 ? 2 : 4);
+    const char* row = reinterpret_cast<const char*>(a.logits) + t * a.ld * (DT == kBF16 ? 2 : 4);
     float x[W];
-    load_logits<DT, W>(row, at, cnt, sp.vec, x);
+    load_logits<DT, W>(row, mine, x);
 
     // softmax: the row's largest logit and sum
     float top = 0.0f, inv = 1.0f;
@@ -398,7 +370,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
       const uint32_t half = LPT == 64 || lane < 32 ? (uint32_t)b : (uint32_t)(b >> 32);
       const int first = LPT == 64 ? __builtin_ctzll(b) : __builtin_ctz((half >> (lane & 16)) & 0xffffu);
       const bool winner = l == first;
-      if (winner) picks[j] = m >= kLow ? at + (W - 1 - (lm & (W - 1))) : -1;
+      if (winner) picks[j] = m >= kLow ? mine.from + (W - 1 - (lm & (W - 1))) : -1;
       const int gone = winner ? lm : INT_MAX;
 #pragma unroll
       for (int i = 0; i < W; ++i) k[i] = k[i] == gone ? INT_MIN : k[i];
@@ -448,9 +420,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
 }
 
 template <int DT, int LPT, int W>
-static int launch_route(const RouteArgs& a, const Spread& s0, hipStream_t s) {
-  Spread sp = s0;
-  sp.vec = vector_width(DT == kBF16 ? 2 : 4, W, sp.run, sp.size, a.ld);
+static int launch_route(const RouteArgs& a, const Spread& sp, hipStream_t s) {
   const bool by_score = a.bias || (a.n_group > 1 && a.group_top == 2);
   auto kern = by_score ? &route_kernel<DT, LPT, W, kByScore> : &route_kernel<DT, LPT, W, kByLogit>;
   int grid = 0;
@@ -509,26 +479,37 @@ int launch_moe_route(const RouteArgs& a, hipStream_t s) {
 constexpr int kBwdThreads = 256;
 constexpr int kBwdTokens = kBwdThreads / 16;
 
+// A lane's own elements: W at once, at any alignment, where all are its own.
 template <int DT, int W>
-__device__ __forceinline__ void store_run(void* row, int at, int cnt, int vec, const float (&d)[W]) {
-  if (W >= 4 && vec >= 4) {
+__device__ __forceinline__ void store_row(char* row, const Run& r, const float (&d)[W]) {
+  constexpr int es = DT == kBF16 ? 2 : 4;
+  if (r.cnt == W) {
+    char* p = row + r.from * es;
+    if constexpr (DT == kBF16 && W > 1) {
+      uint32_t u[W / 2];
 #pragma unroll
-    for (int i = 0; i + 3 < W; i += 4)
-      if (i < cnt) st4<DT>(row, at + i, floatx4{d[i], d[i + 1], d[i + 2], d[i + 3]});
+      for (int i = 0; i < W; i += 2) u[i / 2] = pack_bf16x2(d[i], d[i + 1]);
+      __builtin_memcpy(p, u, sizeof u);
+    } else if constexpr (DT == kBF16) {
+      st1<DT>(p, 0, d[0]);
+    } else {
+      __builtin_memcpy(p, d, sizeof d);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < W; ++i)
-      if (i < cnt) st1<DT>(row, at + i, d[i]);
+      if (r.has(i)) st1<DT>(row, r.from + i, d[i]);
   }
 }
 
 template <int DT, int W>
-__global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(RouteBwdArgs a, int run, int vec, int vec_out) {
+__global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(RouteBwdArgs a, int run) {
   __shared__ __attribute__((aligned(16))) float s_d[kBwdTokens][16 * W];
   constexpr int es = DT == kBF16 ? 2 : 4;
   const int l = threadIdx.x & 15;
   float* mine = s_d[threadIdx.x >> 4];
-  const int at = l * run, cnt = min(max(a.E - at, 0), run);
+  const int cnt = min(max(a.E - l * run, 0), run);
+  const Run held = run_at<W>(cnt > 0 ? l * run : 0, cnt, a.E);
   const int per_run = 65536 / run + 1;  // (exact for e < 512, run <= 32)
   const bool softmax = a.score == kSoftmax, dense = softmax && !a.renorm;
   const int64_t step = (int64_t)gridDim.x * kBwdTokens;
@@ -536,7 +517,7 @@ __global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(RouteBwdArgs a, 
     const int64_t tt = t0 + (threadIdx.x >> 4 & 3), t = min(tt, a.T - 1);
     const char* row = reinterpret_cast<const char*>(a.logits) + t * a.ld * es;
     float p[W];
-    if (dense) load_logits<DT, W>(row, at, cnt, vec, p);
+    if (dense) load_logits<DT, W>(row, held, p);
     // lane j: place j
     int e = -1;
     float x = -INFINITY, g = 0.0f;
@@ -586,7 +567,7 @@ __global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(RouteBwdArgs a, 
     __threadfence_block();
     __builtin_amdgcn_wave_barrier();
     const int holder = e * per_run >> 16;  // e / run
-    if (e >= 0) atomicAdd(&mine[(e - holder * run) * 16 + holder], d);
+    if (e >= 0) atomicAdd(&mine[(e - max(0, min(holder * run, a.E - W))) * 16 + holder], d);
     __threadfence_block();
     __builtin_amdgcn_wave_barrier();
     float o[W];
@@ -596,20 +577,19 @@ __global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(RouteBwdArgs a, 
       if (dense) o[i] = p[i] > 0.0f ? p[i] * inv * (o[i] - mean) : 0.0f;
     }
     __builtin_amdgcn_wave_barrier();
-    if (tt < a.T) store_run<DT, W>(reinterpret_cast<char*>(a.dlogits) + t * a.E * es, at, cnt, vec_out, o);
+    if (tt < a.T) store_row<DT, W>(reinterpret_cast<char*>(a.dlogits) + t * a.E * es, held, o);
   }
 }
 
 template <int DT, int W>
 static int launch_bwd(const RouteBwdArgs& a, hipStream_t s) {
-  const int run = (a.E + 15) / 16, es = DT == kBF16 ? 2 : 4;
-  const int vec = vector_width(es, W, run, a.E, a.ld), vec_out = vector_width(es, W, run, a.E, a.E);
+  const int run = (a.E + 15) / 16;
   auto kern = &route_bwd_kernel<DT, W>;
   int grid = 0;
   const hipError_t e = persistent_grid(reinterpret_cast<const void*>(kern), kBwdThreads,
                                        (a.T + kBwdTokens - 1) / kBwdTokens, &grid);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(kBwdThreads), 0, s, a, run, vec, vec_out);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(kBwdThreads), 0, s, a, run);
   return hipGetLastError();
 }
 
