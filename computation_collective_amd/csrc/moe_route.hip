@@ -132,10 +132,14 @@ __device__ __forceinline__ Run run_at(int at, int cnt, int E) {
 template <int DT, int W>
 __device__ __forceinline__ void load_row(const void* p, float (&x)[W]) {
   if constexpr (DT == kBF16) {
-    uint16_t u[W];
-    __builtin_memcpy(u, p, sizeof u);
+    if constexpr (W == 1) {
+      x[0] = bf16_to_f32(*reinterpret_cast<const uint16_t*>(p));
+    } else {
+      uint32_t u[W / 2];
+      __builtin_memcpy(u, p, sizeof u);
 #pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = bf16_to_f32(u[i]);
+      for (int i = 0; i < W; ++i) x[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    }
   } else {
     __builtin_memcpy(x, p, sizeof x);
   }
@@ -149,82 +153,123 @@ __device__ __forceinline__ void load_logits(const char* row, const Run& r, float
   for (int i = 0; i < W; ++i) x[i] = r.has(i) ? clean(x[i]) : -INFINITY;
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dppd(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)dpp<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp<CTRL>((int)(uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_maxd(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v = fmax(v, __shfl_xor(v, d, 64));
-  return v;
+  v = fmax(v, dppd<0xB1>(v));
+  v = fmax(v, dppd<0x4E>(v));
+  v = fmax(v, dppd<0x141>(v));
+  v = fmax(v, dppd<0x140>(v));
+  v = fmax(v, __shfl_xor(v, 16, 64));
+  return fmax(v, __shfl_xor(v, 32, 64));
 }
 
 // The choice of one token in 64 bits, by a whole wave (lane l: experts l, l +
-// 64, ...); picks to LDS, -1 where none is left.  Scores stay in LDS and loops
-// are not unrolled: this path is rare, and registers held for it would cost
-// the others their occupancy.
-template <int DT>
-__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, double* v, int* picks) {
+// 64, ...; V of them); picks to LDS, -1 where none is left.  Few tokens come
+// here, but a wave that has one is the last to finish: it is laid out for a
+// short chain of dependent steps (some 3 us), not for few instructions.
+template <int DT, int V>
+__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, double* lds, int* picks) {
   const int lane = threadIdx.x & 63, E = a.E;
   const double kOff = -INFINITY;
-  double top = -(double)kMaxF, sum = 0.0;
-  if (a.score == kSoftmax) {
-#pragma unroll 1
-    for (int e = lane; e < E; e += 64) top = fmax(top, (double)clean(ld1<DT>(row, e)));
-    top = wave_maxd(top);
-  }
-#pragma unroll 1
-  for (int e = lane; e < E; e += 64) {
-    const double x = clean(ld1<DT>(row, e));
-    const double p = exp(a.score == kSoftmax ? x - top : -x);
-    v[e] = x > kOff ? p : kOff;
-    sum += x > kOff ? p : 0.0;
+  float x[V], bias[V];
+  double v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = min(lane + 64 * i, E - 1);
+    x[i] = ld1<DT>(row, e);
+    bias[i] = a.bias ? a.bias[e] : 0.0f;
   }
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
-#pragma unroll 1
-  for (int e = lane; e < E; e += 64) {
-    const double p = v[e], s = a.score == kSoftmax ? p / sum : 1.0 / (1.0 + p);
-    const double w = s + (a.bias ? (double)a.bias[e] : 0.0);
-    v[e] = p > kOff && w > kOff ? w : kOff;
+  for (int i = 0; i < V; ++i) x[i] = lane + 64 * i < E ? clean(x[i]) : -INFINITY;
+  if (a.score == kSoftmax) {
+    double top = -(double)kMaxF, sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmax(top, (double)x[i]);
+    top = wave_maxd(top);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] = exp((double)x[i] - top);
+      sum += v[i];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = v[i] / sum;  // (sum = 0: every logit is off)
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 1.0 / (1.0 + exp(-(double)x[i]));
   }
-  __threadfence_block();
-  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const double w = v[i] + (double)bias[i];
+    v[i] = x[i] > -INFINITY && w > kOff ? w : kOff;
+  }
   if (a.n_group > 1) {
+    // 1 << lg lanes on each group, strided through it
     const int size = E / a.n_group;
-    double m1 = kOff, m2 = kOff;  // lane g: the two largest of group g
-    if (lane < a.n_group)
-#pragma unroll 1
-      for (int i = 0; i < size; ++i) {
-        const double w = v[lane * size + i];
+    int lg = 6;
+    while ((64 >> lg) < a.n_group) --lg;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane + 64 * i < E) lds[lane + 64 * i] = v[i];
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    const int g = lane >> lg, step = 1 << lg;
+    double m1 = kOff, m2 = kOff;
+    if (g < a.n_group)
+#pragma unroll 4
+      for (int i = lane & (step - 1); i < size; i += step) {
+        const double w = lds[g * size + i];
         m2 = fmax(m2, fmin(m1, w));
         m1 = fmax(m1, w);
       }
+    for (int d = 1; d < step; d *= 2) {
+      const double o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
+      m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+      m1 = fmax(m1, o1);
+    }
     const double of = a.group_top == 2 && m2 > kOff ? m1 + m2 : m1;
     int ahead = 0;
-#pragma unroll 1
-    for (int g = 0; g < a.n_group; ++g) {
-      const double other = __shfl(of, g, 64);
-      ahead += other > of || (other == of && g < lane);
+#pragma unroll 4
+    for (int o = 0; o < a.n_group; ++o) {
+      const double other = __shfl(of, o << lg, 64);
+      ahead += other > of || (other == of && o < g);
     }
-    const uint64_t kept = __ballot(lane < a.n_group && ahead < a.topk_group);
-#pragma unroll 1
-    for (int e = lane; e < E; e += 64)
-      if (!(kept >> (e / size) & 1)) v[e] = kOff;
-  }
-#pragma unroll 1
-  for (int j = 0; j < a.topk; ++j) {
-    double best = kOff;
-    int at = INT_MAX;
-#pragma unroll 1
-    for (int e = lane; e < E; e += 64)
-      if (v[e] > best) { best = v[e]; at = e; }
+    const uint64_t kept = __ballot(g < a.n_group && ahead < a.topk_group);
+    const float per = 1.0f / (float)size;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const double ob = __shfl_xor(best, d, 64);
-      const int oa = __shfl_xor(at, d, 64);
-      if (ob > best || (ob == best && oa < at)) { best = ob; at = oa; }
+    for (int i = 0; i < V; ++i) {
+      const int of_e = min((int)(((float)(lane + 64 * i) + 0.5f) * per), a.n_group - 1);  // (lane + 64 i) / size
+      if (!(kept >> (of_e << lg) & 1)) v[i] = kOff;
     }
-    if (!(best > kOff)) at = -1;
-    if (at >= 0 && (at & 63) == lane) v[at] = kOff;
-    if (lane == 0) picks[j] = at;
   }
+  int mine = -1;
+  for (int j = 0; j < a.topk; ++j) {
+    double best = v[0];
+    int at = lane;
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      if (v[i] > best) { best = v[i]; at = lane + 64 * i; }
+    const double m = wave_maxd(best);
+    const uint64_t who = __ballot(best == m);
+    int e = __builtin_amdgcn_readlane(at, __builtin_ctzll(who));
+    if (who & (who - 1)) {  // several: the lowest index
+      int low = best == m ? at : INT_MAX;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) low = min(low, __shfl_xor(low, d, 64));
+      e = uniform(low);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane + 64 * i == e) v[i] = kOff;
+    if (lane == j) mine = m > kOff ? e : -1;
+  }
+  if (lane < a.topk) picks[lane] = mine;
 }
 
 // Counts of chosen experts leave a workgroup's LDS histogram through the
@@ -389,7 +434,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
       const int r = __builtin_ctzll(todo) / LPT;
       todo &= LPT == 64 ? 0 : ~(0xffffull << (r * 16));
       const int64_t tr = min(t0 + r, a.T - 1);
-      choose64<DT>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4), s_v[wave],
+      choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4), s_v[wave],
                    s_pick[wave * TPW + r]);
     }
     __threadfence_block();
