@@ -432,16 +432,15 @@ class _Moe(_Common):
     where they are (no copy); a call goes to the current stream of their device
     unless it is given one."""
 
-    def _bind(self, device, ws_bytes=0):
-        self.device = device
+    def _bind(self, entry, args, device, ws_bytes=0):
         self._alloc_sync(ws_bytes, device)
         self._sync = self.next_sync()
+        self._fn = hocf.bind(entry, args, self._sync)
+        self._index = torch.cuda.current_device() if device.index is None else device.index
 
-    def _args(self, stream):
-        """The call's sync block (one per handle, read during the call) and stream."""
-        self.epoch = (self.epoch % 0xFFFFFFF0) + 1
-        self._sync.epoch = self.epoch
-        return self._sync, torch.cuda.current_stream(self.device) if stream is None else stream
+    def call(self, stream=None) -> int:
+        self.epoch = self._sync.epoch = (self.epoch % 0xFFFFFFF0) + 1
+        return self._fn(torch._C._cuda_getCurrentRawStream(self._index) if stream is None else hocf._stream(stream))
 
     def run(self, stream=None):
         hocf.check(self.call(stream))
@@ -469,10 +468,10 @@ class MoeRoute(_Moe):
         self.experts = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
         self.weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
         self.counts = torch.empty(E, dtype=torch.int32, device=logits.device) if counts else None
-        self._a = (T, E, topk, torch_dt(logits), logits.data_ptr(), ld, hocf.ptr(bias), score, n_group, topk_group,
-                   group_top, int(renorm), scale, self.experts.data_ptr(), self.weights.data_ptr(),
-                   hocf.ptr(self.counts))
-        self._bind(logits.device, hocf.hocf_moe_route_workspace_bytes(E) if counts else 0)
+        args = (T, E, topk, torch_dt(logits), logits.data_ptr(), ld, hocf.ptr(bias), score, n_group, topk_group,
+                group_top, int(renorm), scale, self.experts.data_ptr(), self.weights.data_ptr(),
+                hocf.ptr(self.counts))
+        self._bind("hocf_moe_route", args, logits.device, hocf.hocf_moe_route_workspace_bytes(E) if counts else 0)
 
     def poison(self):
         self.experts.fill_(-77)
@@ -480,9 +479,6 @@ class MoeRoute(_Moe):
         if self.counts is not None:
             self.counts.fill_(-77)
 
-    def call(self, stream=None) -> int:
-        s, stream = self._args(stream)
-        return hocf.hocf_moe_route(*self._a, s, stream)
 
 
 class MoeRouteBwd(_Moe):
@@ -496,16 +492,13 @@ class MoeRouteBwd(_Moe):
         _on(logits.device, experts=experts, dweights=dweights)
         self.logits, self.experts, self.dweights = logits, experts, dweights
         self.dlogits = torch.empty((T, E), dtype=tdtype(torch_dt(logits)), device=logits.device)
-        self._a = (T, E, topk, torch_dt(logits), logits.data_ptr(), ld, experts.data_ptr(), dweights.data_ptr(), score,
-                   int(renorm), scale, self.dlogits.data_ptr())
-        self._bind(logits.device)
+        args = (T, E, topk, torch_dt(logits), logits.data_ptr(), ld, experts.data_ptr(), dweights.data_ptr(), score,
+                int(renorm), scale, self.dlogits.data_ptr())
+        self._bind("hocf_moe_route_bwd", args, logits.device)
 
     def poison(self):
         nan_fill(self.dlogits)
 
-    def call(self, stream=None) -> int:
-        s, stream = self._args(stream)
-        return hocf.hocf_moe_route_bwd(*self._a, s, stream)
 
 
 class MoeSlots(_Moe):
@@ -518,17 +511,14 @@ class MoeSlots(_Moe):
         self.index = torch.empty((T, topk), dtype=torch.int32, device=dev)
         self.pair = torch.empty(bins * cap, dtype=torch.int32, device=dev)
         self.counts = torch.empty(bins, dtype=torch.int64, device=dev)
-        self._a = (T, topk, bins, per_bin, cap, experts.data_ptr(), self.index.data_ptr(), self.pair.data_ptr(),
-                   self.counts.data_ptr())
-        self._bind(dev, hocf.hocf_moe_slots_workspace_bytes(T, topk, bins))
+        args = (T, topk, bins, per_bin, cap, experts.data_ptr(), self.index.data_ptr(), self.pair.data_ptr(),
+                self.counts.data_ptr())
+        self._bind("hocf_moe_slots", args, dev, hocf.hocf_moe_slots_workspace_bytes(T, topk, bins))
 
     def poison(self):
         for t in (self.index, self.pair, self.counts):
             t.fill_(-77)
 
-    def call(self, stream=None) -> int:
-        s, stream = self._args(stream)
-        return hocf.hocf_moe_slots(*self._a, s, stream)
 
 
 class MoeCombine(_Moe):
@@ -546,16 +536,13 @@ class MoeCombine(_Moe):
             raise TypeError(f"add is {add.dtype}, not of the output's type")
         self.rows, self.weights, self.index, self.add = rows, weights, index, add
         self.out = torch.empty((T, N), dtype=tdtype(out_dt), device=rows.device)
-        self._a = (T, topk, N, R, torch_dt(rows), out_dt, rows.data_ptr(), weights.data_ptr(), hocf.ptr(index),
-                   hocf.ptr(add), self.out.data_ptr())
-        self._bind(rows.device)
+        args = (T, topk, N, R, torch_dt(rows), out_dt, rows.data_ptr(), weights.data_ptr(), hocf.ptr(index),
+                hocf.ptr(add), self.out.data_ptr())
+        self._bind("hocf_moe_combine", args, rows.device)
 
     def poison(self):
         nan_fill(self.out)
 
-    def call(self, stream=None) -> int:
-        s, stream = self._args(stream)
-        return hocf.hocf_moe_combine(*self._a, s, stream)
 
 
 class MoeCombineBwd(_Moe):
@@ -573,17 +560,14 @@ class MoeCombineBwd(_Moe):
         self.rows, self.weights, self.dout, self.index, self.pair = rows, weights, dout, index, pair
         self.drows = torch.empty((R, N), dtype=tdtype(torch_dt(rows)), device=rows.device)
         self.dweights = torch.empty((T, topk), dtype=torch.float32, device=rows.device)
-        self._a = (T, topk, N, R, torch_dt(rows), torch_dt(dout), rows.data_ptr(), weights.data_ptr(),
-                   dout.data_ptr(), hocf.ptr(index), hocf.ptr(pair), self.drows.data_ptr(), self.dweights.data_ptr())
-        self._bind(rows.device)
+        args = (T, topk, N, R, torch_dt(rows), torch_dt(dout), rows.data_ptr(), weights.data_ptr(),
+                dout.data_ptr(), hocf.ptr(index), hocf.ptr(pair), self.drows.data_ptr(), self.dweights.data_ptr())
+        self._bind("hocf_moe_combine_bwd", args, rows.device)
 
     def poison(self):
         nan_fill(self.drows)
         nan_fill(self.dweights)
 
-    def call(self, stream=None) -> int:
-        s, stream = self._args(stream)
-        return hocf.hocf_moe_combine_bwd(*self._a, s, stream)
 
 
 def w4_layout(E, N, K, group):
@@ -621,13 +605,9 @@ class GemvW4(_Moe):
         _on(x.device, experts=experts, wq=wq, scales=scales, zeros=zeros)
         self.x, self.experts, self.wq, self.scales, self.zeros = x, experts, wq, scales, zeros
         self.out = torch.empty((R, N), dtype=tdtype(out_dt), device=x.device)
-        self._a = (R, rows_per_x, E, e0, N, K, group, out_dt, x.data_ptr(), hocf.ptr(experts), wq.data_ptr(),
-                   scales.data_ptr(), hocf.ptr(zeros), self.out.data_ptr())
-        self._bind(x.device)
+        args = (R, rows_per_x, E, e0, N, K, group, out_dt, x.data_ptr(), hocf.ptr(experts), wq.data_ptr(),
+                scales.data_ptr(), hocf.ptr(zeros), self.out.data_ptr())
+        self._bind("hocf_gemv_w4", args, x.device)
 
     def poison(self):
         nan_fill(self.out)
-
-    def call(self, stream=None) -> int:
-        s, stream = self._args(stream)
-        return hocf.hocf_gemv_w4(*self._a, s, stream)

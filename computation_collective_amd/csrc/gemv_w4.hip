@@ -9,17 +9,23 @@
 //   sum x (code - zero) = sum x (16 + code)  -  (16 + zero) sx
 // in fp32, then times the group's scale.
 //
-// A workgroup takes one block of 16 columns of one expert; its four waves
-// take every fourth block of rows and fold through LDS in a fixed order.
+// A workgroup takes CB blocks of 16 columns of one expert, four waves on each:
+// a wave takes every fourth block of rows, and the four fold through LDS in a
+// fixed order.  K goes in chunks of up to kW4Chunk rows (fewer with many token
+// rows): the chunk's weights are loaded into registers all at once, x and the
+// scales through LDS meanwhile.
 #include <algorithm>
 
 #include "moe.hpp"
+#include "publish.hpp"
 #include "sync.hpp"
 
 namespace hocf {
 
-constexpr int kW4Threads = 256;
-constexpr int kW4Waves = kW4Threads / 64;
+constexpr int kW4Chunk = 4096;               // rows of W of one pass at most: 8 loads of a lane
+constexpr int kW4XElems = 2 * kW4Chunk;      // x in LDS: token rows x chunk, 16 KB
+constexpr int kW4U = kW4Chunk / 512;         // blocks of a wave in one pass
+constexpr int kW4Pack = 256;                 // threads of the packing kernel
 
 // Eight codes of one packed word as 16 + code, in row order.
 __device__ __forceinline__ bf16x8 codes_plus16(uint32_t w) {
@@ -37,96 +43,131 @@ __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
   return e < (uint32_t)a.E ? (int)e : -1;
 }
 
-template <int ODT, int GROUP, bool ZEROS>
-__global__ __launch_bounds__(kW4Threads) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
+template <int ODT, int GROUP, bool ZEROS, int CB>
+__global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
+  constexpr int kThreads = 256 * CB;
+  constexpr int WPG = GROUP / 32;            // words of one group
+  constexpr int GPB = 4 / WPG;               // groups of one block
+  constexpr int kScales = kW4Chunk / GROUP;  // groups of one chunk
+  __shared__ __attribute__((aligned(16))) uint16_t s_x[kW4XElems + 16 * 8];
+  __shared__ __attribute__((aligned(16))) uint16_t s_sc[CB][kScales * 16];
+  __shared__ __attribute__((aligned(16))) uint16_t s_zp[ZEROS ? CB : 1][ZEROS ? kScales * 16 : 8];
+  __shared__ float s_part[CB][4][16][17];
   __shared__ uint16_t s_rows[kW4MaxRows];
-  __shared__ int s_n;
-  __shared__ float s_part[kW4Waves][16][17];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cb = blockIdx.x, y = blockIdx.y;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int y = blockIdx.y, cb0 = blockIdx.x * CB;
   // this workgroup's expert: the y-th local one, or row y's (and then only
   // for the first of the rows that chose it)
-  const int want = !a.experts ? 0 : by_row ? local_expert(a, y) : y;
-  if (wave == 0) {
-    int n = 0;
-    bool first = true;
-    for (int r0 = 0; r0 < a.R; r0 += 64) {
-      const int r = r0 + lane;
-      const int e = r >= a.R ? -1 : a.experts ? local_expert(a, r) : 0;
-      const bool mine = r < a.R && e >= 0 && e == want;
-      const uint64_t m = __ballot(mine);
-      if (by_row && m && n == 0 && r0 + __builtin_ctzll(m) < y) first = false;
-      if (mine) s_rows[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = (uint16_t)r;
-      n += __popcll(m);
-      // rows of other ranks' experts: zeros, by the row's own workgroup or the first expert's
-      if (a.experts && e < 0 && r < a.R && (by_row ? r == y : y == 0))
-        for (int c = cb * 16; c < min(a.N, cb * 16 + 16); ++c) st1<ODT>(a.out, (int64_t)r * a.N + c, 0.0f);
-    }
-    if (lane == 0) s_n = first ? n : 0;
+  const int want = !a.experts ? 0 : by_row ? uniform(local_expert(a, y)) : y;
+  int n_rows = 0;
+  bool first = true;
+  for (int r0 = 0; r0 < a.R; r0 += 64) {
+    const int r = r0 + lane;
+    const int e = r >= a.R ? -1 : a.experts ? local_expert(a, r) : 0;
+    const bool mine = r < a.R && e >= 0 && e == want;
+    const uint64_t m = __ballot(mine);
+    if (by_row && m && n_rows == 0 && r0 + __builtin_ctzll(m) < y) first = false;
+    if (wave == 0 && mine)
+      s_rows[n_rows + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = (uint16_t)r;
+    n_rows += __popcll(m);
+    // rows of other ranks' experts: zeros, by the row's own workgroup or the first expert's
+    if (wave == 0 && a.experts && e < 0 && r < a.R && (by_row ? r == y : y == 0))
+      for (int c = cb0 * 16; c < min(a.N, (cb0 + CB) * 16); ++c) st1<ODT>(a.out, (int64_t)r * a.N + c, 0.0f);
   }
-  __syncthreads();
-  const int n_rows = uniform(s_n);
-  if (n_rows == 0) return;
+  if (!first || n_rows == 0) return;  // (the same in every wave)
 
-  constexpr int WPG = GROUP / 32;  // words of one group
   const int q = lane >> 4, c = lane & 15;
+  const int kq = wave & 3, col = wave >> 2;       // this wave's quarter of K, its block of columns
+  const int cb = min(cb0 + col, a.nb - 1);        // (blocks past the last repeat it, unused)
   const uint4* w = reinterpret_cast<const uint4*>(a.wq) + ((int64_t)want * a.nb + cb) * a.kb * 64 + lane;
-  const uint16_t* sc = a.scales + ((int64_t)want * a.nb + cb) * a.groups * 16 + c;
-  const uint16_t* zp = ZEROS ? a.zeros + ((int64_t)want * a.nb + cb) * a.groups * 16 + c : nullptr;
   bf16x8 ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 
   for (int r0 = 0; r0 < n_rows; r0 += 16) {
-    // A operand: lane's token row c (rows past the last repeat it, unused) at k = 32 t + 8 q
-    const int row = s_rows[min(r0 + c, n_rows - 1)];
-    const uint16_t* x = a.x + (int64_t)(row / a.rows_per_x) * a.K;
+    const int rows = min(16, n_rows - r0);
+    // rows of W of one pass: a multiple of 512 that fits x's rows
+    const int chunk = min(kW4Chunk, max(512, kW4XElems / rows / 512 * 512));
+    const int ldx = chunk + 8;                    // (rows of x start on different LDS banks)
+    const int row_of = min(c, rows - 1) * ldx;    // (token rows past the last repeat it, unused)
     floatx4 total = {0.f, 0.f, 0.f, 0.f};
-    for (int kb = wave; kb < a.kb; kb += kW4Waves) {
-      const uint4 wv = w[(int64_t)kb * 64];
-      const uint32_t word[4] = {wv.x, wv.y, wv.z, wv.w};
+    for (int k0 = 0; k0 < a.K; k0 += chunk) {
+      const int blocks = min(chunk, a.kb * 128 - k0) / 128;  // of this pass
+      uint4 wv[kW4U];
 #pragma unroll
-      for (int g = 0; g < 4 / WPG; ++g) {
-        const int gi = min((kb * 128 + g * GROUP) / GROUP, a.groups - 1);
-        const float s = bf16_to_f32(sc[gi * 16]);
-        const float z = 16.0f + (ZEROS ? bf16_to_f32(zp[gi * 16]) : 8.0f);
-        floatx4 acc = {0.f, 0.f, 0.f, 0.f}, sx = {0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < kW4U; ++u)
+        if (kq + 4 * u < blocks) wv[u] = w[(int64_t)(k0 / 128 + kq + 4 * u) * 64];
+      lds_barrier();  // the row list is there; the last pass is done with x
+      const int pieces = blocks * 16;             // 16-byte pieces of one row of x
+      for (int i = threadIdx.x; i < rows * pieces; i += kThreads) {
+        const int r = i / pieces, k = k0 + (i - r * pieces) * 8;
+        const uint16_t* x = a.x + (int64_t)(s_rows[r0 + r] / a.rows_per_x) * a.K;
+        uint4 v = *reinterpret_cast<const uint4*>(x + min(k, a.K - 8));
+        if (k >= a.K) v = make_uint4(0, 0, 0, 0);  // rows of W beyond K
+        *reinterpret_cast<uint4*>(&s_x[r * ldx + k - k0]) = v;
+      }
+      const int g0 = k0 / GROUP, gn = min(a.groups - g0, blocks * GPB);
+      for (int i = threadIdx.x; i < CB * gn * 2; i += kThreads) {
+        const int b = i / (gn * 2), o = (i - b * gn * 2) * 8;
+        const int64_t from = (((int64_t)want * a.nb + min(cb0 + b, a.nb - 1)) * a.groups + g0) * 16 + o;
+        *reinterpret_cast<uint4*>(&s_sc[b][o]) = *reinterpret_cast<const uint4*>(a.scales + from);
+        if constexpr (ZEROS) *reinterpret_cast<uint4*>(&s_zp[b][o]) = *reinterpret_cast<const uint4*>(a.zeros + from);
+      }
+      lds_barrier();
 #pragma unroll
-        for (int t = g * WPG; t < (g + 1) * WPG; ++t) {
-          const int k = kb * 128 + t * 32 + q * 8;
-          uint4 xv = *reinterpret_cast<const uint4*>(x + min(k, a.K - 8));
-          if (k >= a.K) xv = make_uint4(0, 0, 0, 0);  // rows beyond K
-          const bf16x8 av = __builtin_bit_cast(bf16x8, xv);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, codes_plus16(word[t]), acc, 0, 0, 0);
-          sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, sx, 0, 0, 0);
+      for (int u = 0; u < kW4U; ++u) {
+        const int b = kq + 4 * u;
+        if (b >= blocks) break;
+        const uint32_t word[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+#pragma unroll
+        for (int g = 0; g < GPB; ++g) {
+          floatx4 acc = {0.f, 0.f, 0.f, 0.f}, sx = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int t = g * WPG; t < (g + 1) * WPG; ++t) {
+            const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&s_x[row_of + b * 128 + t * 32 + q * 8]);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, codes_plus16(word[t]), acc, 0, 0, 0);
+            sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, sx, 0, 0, 0);
+          }
+          const int gi = b * GPB + g;
+          if (gi < gn) {  // (groups wholly beyond K have no scale)
+            const float s = bf16_to_f32(s_sc[col][gi * 16 + c]);
+            const float z = 16.0f + (ZEROS ? bf16_to_f32(s_zp[ZEROS ? col : 0][gi * 16 + c]) : 8.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) total[i] = fmaf(s, fmaf(-z, sx[i], acc[i]), total[i]);
+          }
         }
-        // groups wholly beyond K have acc = sx = 0 and a repeated scale
-        if (kb * 128 + g * GROUP < a.K)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) total[i] = fmaf(s, fmaf(-z, sx[i], acc[i]), total[i]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_part[wave][q * 4 + i][c] = total[i];
-    __syncthreads();
-    const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-    if (r0 + tr < n_rows && cb * 16 + tc < a.N) {
-      float v = s_part[0][tr][tc];
+    for (int i = 0; i < 4; ++i) s_part[col][kq][q * 4 + i][c] = total[i];
+    lds_barrier();
+    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4 & 15, tb = threadIdx.x >> 8;
+    if (tr < rows && (cb0 + tb) * 16 + tc < a.N) {
+      float v = s_part[tb][0][tr][tc];
 #pragma unroll
-      for (int k = 1; k < kW4Waves; ++k) v += s_part[k][tr][tc];
-      st1<ODT>(a.out, (int64_t)s_rows[r0 + tr] * a.N + cb * 16 + tc, v);
+      for (int k = 1; k < 4; ++k) v += s_part[tb][k][tr][tc];
+      st1<ODT>(a.out, (int64_t)s_rows[r0 + tr] * a.N + (cb0 + tb) * 16 + tc, v);
     }
-    __syncthreads();
+    lds_barrier();
   }
+}
+
+template <int ODT, int GROUP, bool ZEROS>
+static int launch_zeros(const GemvW4Args& a, hipStream_t s) {
+  const bool by_row = a.experts && a.R < a.E;
+  const int y = !a.experts ? 1 : std::min(a.R, a.E);
+  // Many rows of one matrix: four blocks of columns share what a workgroup
+  // reads of x, which is then more than it reads of the weights.
+  if (!a.experts && a.R > 16)
+    hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, 4>), dim3((a.nb + 3) / 4, y), dim3(1024), 0, s, a, by_row);
+  else
+    hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, 1>), dim3(a.nb, y), dim3(256), 0, s, a, by_row);
+  return hipGetLastError();
 }
 
 template <int ODT, int GROUP>
 static int launch_group(const GemvW4Args& a, hipStream_t s) {
-  const bool by_row = a.experts && a.R < a.E;
-  const dim3 grid(a.nb, !a.experts ? 1 : std::min(a.R, a.E));
-  if (a.zeros) hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, true>), grid, dim3(kW4Threads), 0, s, a, by_row);
-  else hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, false>), grid, dim3(kW4Threads), 0, s, a, by_row);
-  return hipGetLastError();
+  return a.zeros ? launch_zeros<ODT, GROUP, true>(a, s) : launch_zeros<ODT, GROUP, false>(a, s);
 }
 
 template <int ODT>
@@ -141,9 +182,9 @@ int launch_gemv_w4(const GemvW4Args& a, hipStream_t s) {
 }
 
 // The layout: one thread per packed word, then one per scale and zero point.
-__global__ __launch_bounds__(kW4Threads) void w4_pack_kernel(W4PackArgs a) {
+__global__ __launch_bounds__(kW4Pack) void w4_pack_kernel(W4PackArgs a) {
   const int64_t words = (int64_t)a.E * a.nb * a.kb * 256;
-  for (int64_t i = (int64_t)blockIdx.x * kW4Threads + threadIdx.x; i < words; i += (int64_t)gridDim.x * kW4Threads) {
+  for (int64_t i = (int64_t)blockIdx.x * kW4Pack + threadIdx.x; i < words; i += (int64_t)gridDim.x * kW4Pack) {
     const int n = (int)(i & 15), q = (int)(i >> 4 & 3), t = (int)(i >> 6 & 3);  // (columns fastest: reads coalesce)
     const int64_t block = i >> 8;                                               // (e * nb + cb) * kb + kb_
     const int kb = (int)(block % a.kb), cb = (int)(block / a.kb % a.nb);
@@ -159,7 +200,7 @@ __global__ __launch_bounds__(kW4Threads) void w4_pack_kernel(W4PackArgs a) {
     a.wq[(block * 64 + q * 16 + n) * 4 + t] = w;
   }
   const int64_t scales = (int64_t)a.E * a.nb * a.groups * 16;
-  for (int64_t i = (int64_t)blockIdx.x * kW4Threads + threadIdx.x; i < scales; i += (int64_t)gridDim.x * kW4Threads) {
+  for (int64_t i = (int64_t)blockIdx.x * kW4Pack + threadIdx.x; i < scales; i += (int64_t)gridDim.x * kW4Pack) {
     const int64_t g = i >> 4;
     const int gi = (int)(g % a.groups), cb = (int)(g / a.groups % a.nb);
     const int64_t e = g / a.groups / a.nb;
@@ -172,8 +213,8 @@ __global__ __launch_bounds__(kW4Threads) void w4_pack_kernel(W4PackArgs a) {
 
 int launch_w4_pack(const W4PackArgs& a, hipStream_t s) {
   const int64_t words = (int64_t)a.E * a.nb * a.kb * 256;
-  const uint32_t grid = (uint32_t)std::min<int64_t>((words + kW4Threads - 1) / kW4Threads, 16384);
-  hipLaunchKernelGGL(w4_pack_kernel, dim3(grid), dim3(kW4Threads), 0, s, a);
+  const uint32_t grid = (uint32_t)std::min<int64_t>((words + kW4Pack - 1) / kW4Pack, 16384);
+  hipLaunchKernelGGL(w4_pack_kernel, dim3(grid), dim3(kW4Pack), 0, s, a);
   return hipGetLastError();
 }
 

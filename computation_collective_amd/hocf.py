@@ -372,6 +372,14 @@ def hocf_w4_pack(E, N, K, group, codes, scales, zeros, wq, scales_out, zeros_out
                               ptr(zeros_out), _stream(stream))
 
 
+def bind(name, args, sync_):
+    """The C entry point `name` with its leading arguments and its sync block held ready: a
+    function of the stream's address.  (Marshalling a dozen arguments anew costs a third of a
+    small call.)"""
+    fn, ref = getattr(lib(), name), ctypes.byref(sync_)
+    return lambda stream: fn(*args, ref, stream)
+
+
 def _host_i64(a):
     """A host int64 array for the call (kept alive by the caller's reference)."""
     import numpy as np
