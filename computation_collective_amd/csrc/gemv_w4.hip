@@ -9,11 +9,13 @@
 //   sum x (code - zero) = sum x (16 + code)  -  (16 + zero) sx
 // in fp32, then times the group's scale.
 //
-// A workgroup takes CB blocks of 16 columns of one expert, four waves on each:
+// A workgroup has four waves for each of CB blocks of 16 columns of an expert:
 // a wave takes every fourth block of rows, and the four fold through LDS in a
-// fixed order.  K goes in chunks of up to kW4Chunk rows (fewer with many token
-// rows): the chunk's weights are loaded into registers all at once, x and the
-// scales through LDS meanwhile.
+// fixed order.  K goes in passes of up to U blocks of a wave (fewer with many
+// token rows, whose x is in LDS).  What a wave waits for first is loaded
+// first -- x, then scales, then weights, each a straight run of loads, since
+// loads come back in order and a load under a condition is waited for at once
+// -- so that its products start with the first weights.
 #include <algorithm>
 
 #include "moe.hpp"
@@ -22,10 +24,8 @@
 
 namespace hocf {
 
-constexpr int kW4Chunk = 4096;               // rows of W of one pass at most: 8 loads of a lane
-constexpr int kW4XElems = 2 * kW4Chunk;      // x in LDS: token rows x chunk, 16 KB
-constexpr int kW4U = kW4Chunk / 512;         // blocks of a wave in one pass
-constexpr int kW4Pack = 256;                 // threads of the packing kernel
+constexpr int kW4XElems = 8192;   // x in LDS: token rows x rows of W, 16 KB
+constexpr int kW4Pack = 256;      // threads of the packing kernel
 
 // Eight codes of one packed word as 16 + code, in row order.
 __device__ __forceinline__ bf16x8 codes_plus16(uint32_t w) {
@@ -43,15 +43,13 @@ __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
   return e < (uint32_t)a.E ? (int)e : -1;
 }
 
-template <int ODT, int GROUP, bool ZEROS, int CB>
+template <int ODT, int GROUP, bool ZEROS, int U, int CB>
 __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
   constexpr int kThreads = 256 * CB;
-  constexpr int WPG = GROUP / 32;            // words of one group
-  constexpr int GPB = 4 / WPG;               // groups of one block
-  constexpr int kScales = kW4Chunk / GROUP;  // groups of one chunk
+  constexpr int WPG = GROUP / 32;  // words of one group
+  constexpr int GPB = 4 / WPG;     // groups of one block
+  constexpr int XP = kW4XElems / 8 / kThreads;  // 16-byte pieces of x that a thread moves
   __shared__ __attribute__((aligned(16))) uint16_t s_x[kW4XElems + 16 * 8];
-  __shared__ __attribute__((aligned(16))) uint16_t s_sc[CB][kScales * 16];
-  __shared__ __attribute__((aligned(16))) uint16_t s_zp[ZEROS ? CB : 1][ZEROS ? kScales * 16 : 8];
   __shared__ float s_part[CB][4][16][17];
   __shared__ uint16_t s_rows[kW4MaxRows];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -67,7 +65,8 @@ __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by
     const bool mine = r < a.R && e >= 0 && e == want;
     const uint64_t m = __ballot(mine);
     if (by_row && m && n_rows == 0 && r0 + __builtin_ctzll(m) < y) first = false;
-    if (wave == 0 && mine)
+    // (every wave writes the same list: each can use it without waiting for the others)
+    if (mine)
       s_rows[n_rows + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = (uint16_t)r;
     n_rows += __popcll(m);
     // rows of other ranks' experts: zeros, by the row's own workgroup or the first expert's
@@ -75,65 +74,75 @@ __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by
       for (int c = cb0 * 16; c < min(a.N, (cb0 + CB) * 16); ++c) st1<ODT>(a.out, (int64_t)r * a.N + c, 0.0f);
   }
   if (!first || n_rows == 0) return;  // (the same in every wave)
+  __builtin_amdgcn_wave_barrier();
 
   const int q = lane >> 4, c = lane & 15;
-  const int kq = wave & 3, col = wave >> 2;       // this wave's quarter of K, its block of columns
-  const int cb = min(cb0 + col, a.nb - 1);        // (blocks past the last repeat it, unused)
-  const uint4* w = reinterpret_cast<const uint4*>(a.wq) + ((int64_t)want * a.nb + cb) * a.kb * 64 + lane;
+  const int kq = wave & 3, col = wave >> 2;  // this wave's quarter of K, its block of columns
+  const int64_t at = (int64_t)want * a.nb + min(cb0 + col, a.nb - 1);  // (past the last block: repeated, unused)
+  const uint4* wq = reinterpret_cast<const uint4*>(a.wq) + at * a.kb * 64 + lane;
+  const int64_t small = at * a.groups * 16 + c;
   bf16x8 ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 
   for (int r0 = 0; r0 < n_rows; r0 += 16) {
     const int rows = min(16, n_rows - r0);
-    // rows of W of one pass: a multiple of 512 that fits x's rows
-    const int chunk = min(kW4Chunk, max(512, kW4XElems / rows / 512 * 512));
-    const int ldx = chunk + 8;                    // (rows of x start on different LDS banks)
-    const int row_of = min(c, rows - 1) * ldx;    // (token rows past the last repeat it, unused)
+    // rows of W of one pass: a multiple of 512 (a block of each wave) that fits x's rows
+    const int chunk = min(512 * U, max(512, kW4XElems / rows / 512 * 512));
+    const int ldx = chunk + 8;                  // (rows of x start on different LDS banks)
+    const int row_of = min(c, rows - 1) * ldx;  // (token rows past the last repeat it, unused)
     floatx4 total = {0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < a.K; k0 += chunk) {
       const int blocks = min(chunk, a.kb * 128 - k0) / 128;  // of this pass
-      uint4 wv[kW4U];
+      const int pieces = blocks * 16, all = rows * pieces;   // of x
+      uint4 v[XP];
+      int to[XP];
 #pragma unroll
-      for (int u = 0; u < kW4U; ++u)
-        if (kq + 4 * u < blocks) wv[u] = w[(int64_t)(k0 / 128 + kq + 4 * u) * 64];
-      lds_barrier();  // the row list is there; the last pass is done with x
-      const int pieces = blocks * 16;             // 16-byte pieces of one row of x
-      for (int i = threadIdx.x; i < rows * pieces; i += kThreads) {
-        const int r = i / pieces, k = k0 + (i - r * pieces) * 8;
-        const uint16_t* x = a.x + (int64_t)(s_rows[r0 + r] / a.rows_per_x) * a.K;
-        uint4 v = *reinterpret_cast<const uint4*>(x + min(k, a.K - 8));
-        if (k >= a.K) v = make_uint4(0, 0, 0, 0);  // rows of W beyond K
-        *reinterpret_cast<uint4*>(&s_x[r * ldx + k - k0]) = v;
+      for (int p = 0; p < XP; ++p) {  // (pieces past the last repeat it)
+        const int i = min((int)threadIdx.x + p * kThreads, all - 1);
+        const int r = rows == 1 ? 0 : i / pieces, k = (i - r * pieces) * 8;
+        to[p] = r * ldx + k;
+        v[p] = *reinterpret_cast<const uint4*>(a.x + (int64_t)(s_rows[r0 + r] / a.rows_per_x) * a.K + min(k0 + k, a.K - 8));
       }
-      const int g0 = k0 / GROUP, gn = min(a.groups - g0, blocks * GPB);
-      for (int i = threadIdx.x; i < CB * gn * 2; i += kThreads) {
-        const int b = i / (gn * 2), o = (i - b * gn * 2) * 8;
-        const int64_t from = (((int64_t)want * a.nb + min(cb0 + b, a.nb - 1)) * a.groups + g0) * 16 + o;
-        *reinterpret_cast<uint4*>(&s_sc[b][o]) = *reinterpret_cast<const uint4*>(a.scales + from);
-        if constexpr (ZEROS) *reinterpret_cast<uint4*>(&s_zp[b][o]) = *reinterpret_cast<const uint4*>(a.zeros + from);
+      uint4 wv[U];
+      uint32_t sz[U], zz[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // lanes of quarter q take the block's group q mod GPB (past the last: repeated, unused)
+        const int g = min((k0 / 128 + kq + 4 * u) * GPB + (q & (GPB - 1)), a.groups - 1);
+        sz[u] = a.scales[small + g * 16];
+        zz[u] = ZEROS ? a.zeros[small + g * 16] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) wv[u] = wq[(int64_t)(k0 / 128 + min(kq + 4 * u, blocks - 1)) * 64];
+      lds_barrier();  // the last pass is done with x
+#pragma unroll
+      for (int p = 0; p < XP; ++p) {
+        if (k0 + to[p] % ldx >= a.K) v[p] = make_uint4(0, 0, 0, 0);  // rows of W beyond K
+        *reinterpret_cast<uint4*>(&s_x[to[p]]) = v[p];
       }
       lds_barrier();
 #pragma unroll
-      for (int u = 0; u < kW4U; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int b = kq + 4 * u;
-        if (b >= blocks) break;
-        const uint32_t word[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+        if (b < blocks) {
+          const uint32_t word[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
 #pragma unroll
-        for (int g = 0; g < GPB; ++g) {
-          floatx4 acc = {0.f, 0.f, 0.f, 0.f}, sx = {0.f, 0.f, 0.f, 0.f};
+          for (int g = 0; g < GPB; ++g) {
+            floatx4 acc = {0.f, 0.f, 0.f, 0.f}, sx = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int t = g * WPG; t < (g + 1) * WPG; ++t) {
-            const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&s_x[row_of + b * 128 + t * 32 + q * 8]);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, codes_plus16(word[t]), acc, 0, 0, 0);
-            sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, sx, 0, 0, 0);
-          }
-          const int gi = b * GPB + g;
-          if (gi < gn) {  // (groups wholly beyond K have no scale)
-            const float s = bf16_to_f32(s_sc[col][gi * 16 + c]);
-            const float z = 16.0f + (ZEROS ? bf16_to_f32(s_zp[ZEROS ? col : 0][gi * 16 + c]) : 8.0f);
+            for (int t = g * WPG; t < (g + 1) * WPG; ++t) {
+              const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&s_x[row_of + b * 128 + t * 32 + q * 8]);
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, codes_plus16(word[t]), acc, 0, 0, 0);
+              sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, sx, 0, 0, 0);
+            }
+            const uint32_t mine = sz[u] | zz[u] << 16;
+            const uint32_t both = GPB == 1 ? mine : (uint32_t)__shfl((int)mine, g * 16 + c, 64);
+            const float s = bf16_to_f32(both & 0xffffu);
+            const float z = 16.0f + (ZEROS ? __uint_as_float(both & 0xffff0000u) : 8.0f);
+            if (GPB == 1 || k0 + b * 128 + g * GROUP < a.K)  // (groups wholly beyond K have no scale)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) total[i] = fmaf(s, fmaf(-z, sx[i], acc[i]), total[i]);
+              for (int i = 0; i < 4; ++i) total[i] = fmaf(s, fmaf(-z, sx[i], acc[i]), total[i]);
           }
         }
       }
@@ -148,21 +157,28 @@ __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by
       for (int k = 1; k < 4; ++k) v += s_part[tb][k][tr][tc];
       st1<ODT>(a.out, (int64_t)s_rows[r0 + tr] * a.N + (cb0 + tb) * 16 + tc, v);
     }
-    lds_barrier();
+    if (r0 + 16 < n_rows) lds_barrier();
   }
 }
 
-template <int ODT, int GROUP, bool ZEROS>
-static int launch_zeros(const GemvW4Args& a, hipStream_t s) {
+template <int ODT, int GROUP, bool ZEROS, int U>
+static int launch_u(const GemvW4Args& a, hipStream_t s) {
   const bool by_row = a.experts && a.R < a.E;
   const int y = !a.experts ? 1 : std::min(a.R, a.E);
   // Many rows of one matrix: four blocks of columns share what a workgroup
   // reads of x, which is then more than it reads of the weights.
   if (!a.experts && a.R > 16)
-    hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, 4>), dim3((a.nb + 3) / 4, y), dim3(1024), 0, s, a, by_row);
+    hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, 2, 4>), dim3((a.nb + 3) / 4, y), dim3(1024), 0, s, a, by_row);
   else
-    hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, 1>), dim3(a.nb, y), dim3(256), 0, s, a, by_row);
+    hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, U, 1>), dim3(a.nb, y), dim3(256), 0, s, a, by_row);
   return hipGetLastError();
+}
+
+template <int ODT, int GROUP, bool ZEROS>
+static int launch_zeros(const GemvW4Args& a, hipStream_t s) {
+  if (a.kb <= 8) return launch_u<ODT, GROUP, ZEROS, 2>(a, s);
+  if (a.kb <= 16) return launch_u<ODT, GROUP, ZEROS, 4>(a, s);
+  return launch_u<ODT, GROUP, ZEROS, 8>(a, s);
 }
 
 template <int ODT, int GROUP>
