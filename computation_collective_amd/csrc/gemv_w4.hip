@@ -51,9 +51,10 @@ __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by
   constexpr int XP = kW4XElems / 8 / kThreads;  // 16-byte pieces of x that a thread moves
   __shared__ __attribute__((aligned(16))) uint16_t s_x[kW4XElems + 16 * 8];
   __shared__ float s_part[CB][4][16][17];
-  __shared__ uint16_t s_rows[kW4MaxRows];
+  __shared__ uint16_t s_rows[kW4MaxRows], s_xrow[kW4MaxRows];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int y = blockIdx.y, cb0 = blockIdx.x * CB;
+  const float per_x = 1.0f / (float)a.rows_per_x;
   // this workgroup's expert: the y-th local one, or row y's (and then only
   // for the first of the rows that chose it)
   const int want = !a.experts ? 0 : by_row ? uniform(local_expert(a, y)) : y;
@@ -66,8 +67,11 @@ __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by
     const uint64_t m = __ballot(mine);
     if (by_row && m && n_rows == 0 && r0 + __builtin_ctzll(m) < y) first = false;
     // (every wave writes the same list: each can use it without waiting for the others)
-    if (mine)
-      s_rows[n_rows + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = (uint16_t)r;
+    if (mine) {
+      const int i = n_rows + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+      s_rows[i] = (uint16_t)r;
+      s_xrow[i] = (uint16_t)(((float)r + 0.5f) * per_x);  // r / rows_per_x
+    }
     n_rows += __popcll(m);
     // rows of other ranks' experts: zeros, by the row's own workgroup or the first expert's
     if (wave == 0 && a.experts && e < 0 && r < a.R && (by_row ? r == y : y == 0))
@@ -79,47 +83,49 @@ __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by
   const int q = lane >> 4, c = lane & 15;
   const int kq = wave & 3, col = wave >> 2;  // this wave's quarter of K, its block of columns
   const int64_t at = (int64_t)want * a.nb + min(cb0 + col, a.nb - 1);  // (past the last block: repeated, unused)
-  const uint4* wq = reinterpret_cast<const uint4*>(a.wq) + at * a.kb * 64 + lane;
-  const int64_t small = at * a.groups * 16 + c;
+  const char* wq = reinterpret_cast<const char*>(a.wq) + at * a.kb * 1024;
+  const uint16_t* scales = a.scales + at * a.groups * 16;
+  const uint16_t* zeros = ZEROS ? a.zeros + at * a.groups * 16 : nullptr;
   bf16x8 ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 
   for (int r0 = 0; r0 < n_rows; r0 += 16) {
     const int rows = min(16, n_rows - r0);
-    // rows of W of one pass: a multiple of 512 (a block of each wave) that fits x's rows
-    const int chunk = min(512 * U, max(512, kW4XElems / rows / 512 * 512));
+    // a pass takes U >> sh blocks of every wave: what fits x's rows
+    int sh = 0;
+    while (rows > (kW4XElems / 512 / U) << sh) ++sh;
+    const int chunk = (512 * U) >> sh, lp = __builtin_ctz(64 * U) - sh;  // rows of W; log2 of a row of x in pieces
     const int ldx = chunk + 8;                  // (rows of x start on different LDS banks)
     const int row_of = min(c, rows - 1) * ldx;  // (token rows past the last repeat it, unused)
     floatx4 total = {0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < a.K; k0 += chunk) {
       const int blocks = min(chunk, a.kb * 128 - k0) / 128;  // of this pass
-      const int pieces = blocks * 16, all = rows * pieces;   // of x
       uint4 v[XP];
-      int to[XP];
 #pragma unroll
-      for (int p = 0; p < XP; ++p) {  // (pieces past the last repeat it)
-        const int i = min((int)threadIdx.x + p * kThreads, all - 1);
-        const int r = rows == 1 ? 0 : i / pieces, k = (i - r * pieces) * 8;
-        to[p] = r * ldx + k;
-        v[p] = *reinterpret_cast<const uint4*>(a.x + (int64_t)(s_rows[r0 + r] / a.rows_per_x) * a.K + min(k0 + k, a.K - 8));
+      for (int p = 0; p < XP; ++p) {  // (past the last row or piece: repeated or unused)
+        const int i = threadIdx.x + p * kThreads, r = min(i >> lp, rows - 1), k = k0 + (i & ((1 << lp) - 1)) * 8;
+        v[p] = *reinterpret_cast<const uint4*>(a.x + (int64_t)s_xrow[r0 + r] * a.K + min(k, a.K - 8));
+        if (k >= a.K) v[p] = make_uint4(0, 0, 0, 0);  // rows of W beyond K
       }
       uint4 wv[U];
       uint32_t sz[U], zz[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         // lanes of quarter q take the block's group q mod GPB (past the last: repeated, unused)
-        const int g = min((k0 / 128 + kq + 4 * u) * GPB + (q & (GPB - 1)), a.groups - 1);
-        sz[u] = a.scales[small + g * 16];
-        zz[u] = ZEROS ? a.zeros[small + g * 16] : 0;
+        const int g0 = (k0 / 128 + min(kq + 4 * u, blocks - 1)) * GPB;
+        const uint32_t o = min(q & (GPB - 1), a.groups - 1 - g0) * 16 + c;
+        sz[u] = scales[g0 * 16 + o];
+        zz[u] = ZEROS ? zeros[g0 * 16 + o] : 0;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) wv[u] = wq[(int64_t)(k0 / 128 + min(kq + 4 * u, blocks - 1)) * 64];
+      for (int u = 0; u < U; ++u)
+        wv[u] = *reinterpret_cast<const uint4*>(wq + (int64_t)(k0 / 128 + min(kq + 4 * u, blocks - 1)) * 1024 + (uint32_t)lane * 16);
       lds_barrier();  // the last pass is done with x
 #pragma unroll
       for (int p = 0; p < XP; ++p) {
-        if (k0 + to[p] % ldx >= a.K) v[p] = make_uint4(0, 0, 0, 0);  // rows of W beyond K
-        *reinterpret_cast<uint4*>(&s_x[to[p]]) = v[p];
+        const int i = threadIdx.x + p * kThreads, r = i >> lp;
+        if (r < rows) *reinterpret_cast<uint4*>(&s_x[r * ldx + (i & ((1 << lp) - 1)) * 8]) = v[p];
       }
       lds_barrier();
 #pragma unroll
