@@ -27,15 +27,25 @@ namespace hocf {
 constexpr int kW4XElems = 8192;   // x in LDS: token rows x rows of W, 16 KB
 constexpr int kW4Pack = 256;      // threads of the packing kernel
 
-// Eight codes of one packed word as 16 + code, in row order.
-__device__ __forceinline__ bf16x8 codes_plus16(uint32_t w) {
-  uint4 r;
-  r.x = (w & 0x00780078u) | 0x41804180u;
-  r.y = (__builtin_amdgcn_alignbit(w, w, 4) & 0x00780078u) | 0x41804180u;
-  r.z = (__builtin_amdgcn_alignbit(w, w, 8) & 0x00780078u) | 0x41804180u;
-  r.w = (__builtin_amdgcn_alignbit(w, w, 12) & 0x00780078u) | 0x41804180u;
-  return __builtin_bit_cast(bf16x8, r);
-}
+// Eight codes of one packed word as 16 + code, in row order: a rotation and one
+// and-or per pair.  (The instruction takes no literal: the mask stays in a
+// scalar register and the 16s in a vector one, which the compiler would
+// otherwise split into two instructions with a literal each.)
+struct Codes {
+  uint32_t mask = 0x00780078u, sixteens = 0x41804180u;
+  __device__ __forceinline__ Codes() {
+    __asm__ volatile("" : "+s"(mask));
+    __asm__ volatile("" : "+v"(sixteens));
+  }
+  __device__ __forceinline__ bf16x8 operator()(uint32_t w) const {
+    uint4 r;
+    r.x = (w & mask) | sixteens;
+    r.y = (__builtin_amdgcn_alignbit(w, w, 4) & mask) | sixteens;
+    r.z = (__builtin_amdgcn_alignbit(w, w, 8) & mask) | sixteens;
+    r.w = (__builtin_amdgcn_alignbit(w, w, 12) & mask) | sixteens;
+    return __builtin_bit_cast(bf16x8, r);
+  }
+};
 
 // Row r's expert among this rank's, or -1.
 __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
@@ -44,7 +54,7 @@ __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
 }
 
 template <int ODT, int GROUP, bool ZEROS, int U, int CB>
-__global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
+__global__ __launch_bounds__(256 * CB, 4) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
   constexpr int kThreads = 256 * CB;
   constexpr int WPG = GROUP / 32;  // words of one group
   constexpr int GPB = 4 / WPG;     // groups of one block
@@ -86,6 +96,7 @@ __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by
   const char* wq = reinterpret_cast<const char*>(a.wq) + at * a.kb * 1024;
   const uint16_t* scales = a.scales + at * a.groups * 16;
   const uint16_t* zeros = ZEROS ? a.zeros + at * a.groups * 16 : nullptr;
+  const Codes codes;
   bf16x8 ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
@@ -139,7 +150,7 @@ __global__ __launch_bounds__(256 * CB) void gemv_w4_kernel(GemvW4Args a, bool by
 #pragma unroll
             for (int t = g * WPG; t < (g + 1) * WPG; ++t) {
               const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&s_x[row_of + b * 128 + t * 32 + q * 8]);
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, codes_plus16(word[t]), acc, 0, 0, 0);
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, codes(word[t]), acc, 0, 0, 0);
               sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, sx, 0, 0, 0);
             }
             const uint32_t mine = sz[u] | zz[u] << 16;
