@@ -9,8 +9,8 @@
 //   sum x (code - zero) = sum x (16 + code)  -  (16 + zero) sx
 // in fp32, then times the group's scale.
 //
-// A workgroup has four waves for each of CB blocks of 16 columns of an expert:
-// a wave takes every fourth block of rows, and the four fold through LDS in a
+// A workgroup's four waves take C blocks of 16 columns of an expert together: a
+// wave takes every fourth block of rows, and the four fold through LDS in a
 // fixed order.  K goes in passes of up to U blocks of a wave (fewer with many
 // token rows, whose x is in LDS).  What a wave waits for first is loaded
 // first -- x, then scales, then weights, each a straight run of loads, since
@@ -25,6 +25,7 @@
 namespace hocf {
 
 constexpr int kW4XElems = 8192;   // x in LDS: token rows x rows of W, 16 KB
+constexpr int kW4Many = 2048;     // (column block, expert) pairs from which a workgroup takes two blocks
 constexpr int kW4Pack = 256;      // threads of the packing kernel
 
 // Eight codes of one packed word as 16 + code, in row order: a rotation and one
@@ -53,17 +54,17 @@ __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
   return e < (uint32_t)a.E ? (int)e : -1;
 }
 
-template <int ODT, int GROUP, bool ZEROS, int U, int CB>
-__global__ __launch_bounds__(256 * CB, 4) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
-  constexpr int kThreads = 256 * CB;
+template <int ODT, int GROUP, bool ZEROS, int U, int C>
+__global__ __launch_bounds__(256, C * U > 8 ? 2 : 4) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
+  constexpr int kThreads = 256;
   constexpr int WPG = GROUP / 32;  // words of one group
   constexpr int GPB = 4 / WPG;     // groups of one block
   constexpr int XP = kW4XElems / 8 / kThreads;  // 16-byte pieces of x that a thread moves
   __shared__ __attribute__((aligned(16))) uint16_t s_x[kW4XElems + 16 * 8];
-  __shared__ float s_part[CB][4][16][17];
+  __shared__ float s_part[C][4][16][17];
   __shared__ uint16_t s_rows[kW4MaxRows], s_xrow[kW4MaxRows];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int y = blockIdx.y, cb0 = blockIdx.x * CB;
+  const int y = blockIdx.y, cb0 = blockIdx.x * C;
   const float per_x = 1.0f / (float)a.rows_per_x;
   // this workgroup's expert: the y-th local one, or row y's (and then only
   // for the first of the rows that chose it)
@@ -85,17 +86,14 @@ __global__ __launch_bounds__(256 * CB, 4) void gemv_w4_kernel(GemvW4Args a, bool
     n_rows += __popcll(m);
     // rows of other ranks' experts: zeros, by the row's own workgroup or the first expert's
     if (wave == 0 && a.experts && e < 0 && r < a.R && (by_row ? r == y : y == 0))
-      for (int c = cb0 * 16; c < min(a.N, (cb0 + CB) * 16); ++c) st1<ODT>(a.out, (int64_t)r * a.N + c, 0.0f);
+      for (int c = cb0 * 16; c < min(a.N, (cb0 + C) * 16); ++c) st1<ODT>(a.out, (int64_t)r * a.N + c, 0.0f);
   }
   if (!first || n_rows == 0) return;  // (the same in every wave)
   __builtin_amdgcn_wave_barrier();
 
   const int q = lane >> 4, c = lane & 15;
-  const int kq = wave & 3, col = wave >> 2;  // this wave's quarter of K, its block of columns
-  const int64_t at = (int64_t)want * a.nb + min(cb0 + col, a.nb - 1);  // (past the last block: repeated, unused)
-  const char* wq = reinterpret_cast<const char*>(a.wq) + at * a.kb * 1024;
-  const uint16_t* scales = a.scales + at * a.groups * 16;
-  const uint16_t* zeros = ZEROS ? a.zeros + at * a.groups * 16 : nullptr;
+  const int kq = wave;                         // this wave's quarter of K
+  const int64_t at0 = (int64_t)want * a.nb;    // (blocks of columns past the last repeat it, unused)
   const Codes codes;
   bf16x8 ones;
 #pragma unroll
@@ -109,7 +107,9 @@ __global__ __launch_bounds__(256 * CB, 4) void gemv_w4_kernel(GemvW4Args a, bool
     const int chunk = (512 * U) >> sh, lp = __builtin_ctz(64 * U) - sh;  // rows of W; log2 of a row of x in pieces
     const int ldx = chunk + 8;                  // (rows of x start on different LDS banks)
     const int row_of = min(c, rows - 1) * ldx;  // (token rows past the last repeat it, unused)
-    floatx4 total = {0.f, 0.f, 0.f, 0.f};
+    floatx4 total[C];
+#pragma unroll
+    for (int n = 0; n < C; ++n) total[n] = floatx4{0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < a.K; k0 += chunk) {
       const int blocks = min(chunk, a.kb * 128 - k0) / 128;  // of this pass
       uint4 v[XP];
@@ -119,19 +119,29 @@ __global__ __launch_bounds__(256 * CB, 4) void gemv_w4_kernel(GemvW4Args a, bool
         v[p] = *reinterpret_cast<const uint4*>(a.x + (int64_t)s_xrow[r0 + r] * a.K + min(k, a.K - 8));
         if (k >= a.K) v[p] = make_uint4(0, 0, 0, 0);  // rows of W beyond K
       }
-      uint4 wv[U];
-      uint32_t sz[U], zz[U];
+      uint4 wv[C][U];
+      uint32_t sz[C][U];  // scale and zero
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // lanes of quarter q take the block's group q mod GPB (past the last: repeated, unused)
-        const int g0 = (k0 / 128 + min(kq + 4 * u, blocks - 1)) * GPB;
-        const uint32_t o = min(q & (GPB - 1), a.groups - 1 - g0) * 16 + c;
-        sz[u] = scales[g0 * 16 + o];
-        zz[u] = ZEROS ? zeros[g0 * 16 + o] : 0;
+      for (int n = 0; n < C; ++n) {
+        const int64_t small = (at0 + min(cb0 + n, a.nb - 1)) * a.groups * 16;
+        const uint16_t *scales = a.scales + small, *zeros = ZEROS ? a.zeros + small : nullptr;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          // lanes of quarter q take the block's group q mod GPB (past the last: repeated, unused)
+          const int g0 = (k0 / 128 + min(kq + 4 * u, blocks - 1)) * GPB;
+          const uint32_t o = min(q & (GPB - 1), a.groups - 1 - g0) * 16 + c;
+          sz[n][u] = scales[g0 * 16 + o];
+          if constexpr (ZEROS) sz[n][u] |= (uint32_t)zeros[g0 * 16 + o] << 16;
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        wv[u] = *reinterpret_cast<const uint4*>(wq + (int64_t)(k0 / 128 + min(kq + 4 * u, blocks - 1)) * 1024 + (uint32_t)lane * 16);
+#pragma unroll
+        for (int n = 0; n < C; ++n) {
+          const char* wq = reinterpret_cast<const char*>(a.wq) +
+                           ((at0 + min(cb0 + n, a.nb - 1)) * a.kb + k0 / 128 + min(kq + 4 * u, blocks - 1)) * 1024;
+          wv[n][u] = *reinterpret_cast<const uint4*>(wq + (uint32_t)lane * 16);
+        }
       lds_barrier();  // the last pass is done with x
 #pragma unroll
       for (int p = 0; p < XP; ++p) {
@@ -143,59 +153,74 @@ __global__ __launch_bounds__(256 * CB, 4) void gemv_w4_kernel(GemvW4Args a, bool
       for (int u = 0; u < U; ++u) {
         const int b = kq + 4 * u;
         if (b < blocks) {
-          const uint32_t word[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
 #pragma unroll
           for (int g = 0; g < GPB; ++g) {
-            floatx4 acc = {0.f, 0.f, 0.f, 0.f}, sx = {0.f, 0.f, 0.f, 0.f};
+            floatx4 acc[C], sx = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < C; ++n) acc[n] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int t = g * WPG; t < (g + 1) * WPG; ++t) {
               const bf16x8 xv = *reinterpret_cast<const bf16x8*>(&s_x[row_of + b * 128 + t * 32 + q * 8]);
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, codes(word[t]), acc, 0, 0, 0);
               sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, sx, 0, 0, 0);
-            }
-            const uint32_t mine = sz[u] | zz[u] << 16;
-            const uint32_t both = GPB == 1 ? mine : (uint32_t)__shfl((int)mine, g * 16 + c, 64);
-            const float s = bf16_to_f32(both & 0xffffu);
-            const float z = 16.0f + (ZEROS ? __uint_as_float(both & 0xffff0000u) : 8.0f);
-            if (GPB == 1 || k0 + b * 128 + g * GROUP < a.K)  // (groups wholly beyond K have no scale)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) total[i] = fmaf(s, fmaf(-z, sx[i], acc[i]), total[i]);
+              for (int n = 0; n < C; ++n) {
+                const uint4& v4 = wv[n][u];
+                acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    xv, codes(t == 0 ? v4.x : t == 1 ? v4.y : t == 2 ? v4.z : v4.w), acc[n], 0, 0, 0);
+              }
+            }
+            if (GPB > 1 && k0 + b * 128 + g * GROUP >= a.K) break;  // (groups wholly beyond K have no scale)
+#pragma unroll
+            for (int n = 0; n < C; ++n) {
+              const uint32_t both = GPB == 1 ? sz[n][u] : (uint32_t)__shfl((int)sz[n][u], g * 16 + c, 64);
+              const float s = bf16_to_f32(both & 0xffffu);
+              const float z = 16.0f + (ZEROS ? __uint_as_float(both & 0xffff0000u) : 8.0f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) total[n][i] = fmaf(s, fmaf(-z, sx[i], acc[n][i]), total[n][i]);
+            }
           }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_part[col][kq][q * 4 + i][c] = total[i];
-    lds_barrier();
-    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4 & 15, tb = threadIdx.x >> 8;
-    if (tr < rows && (cb0 + tb) * 16 + tc < a.N) {
-      float v = s_part[tb][0][tr][tc];
+    for (int n = 0; n < C; ++n)
 #pragma unroll
-      for (int k = 1; k < 4; ++k) v += s_part[tb][k][tr][tc];
-      st1<ODT>(a.out, (int64_t)s_rows[r0 + tr] * a.N + (cb0 + tb) * 16 + tc, v);
+      for (int i = 0; i < 4; ++i) s_part[n][kq][q * 4 + i][c] = total[n][i];
+    lds_barrier();
+    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;
+    if (tr < rows) {
+      const int64_t out = (int64_t)s_rows[r0 + tr] * a.N;
+#pragma unroll
+      for (int n = 0; n < C; ++n) {
+        const int column = (cb0 + n) * 16 + tc;
+        float v = s_part[n][0][tr][tc];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) v += s_part[n][k][tr][tc];
+        if (column < a.N) st1<ODT>(a.out, out + column, v);
+      }
     }
     if (r0 + 16 < n_rows) lds_barrier();
   }
 }
 
-template <int ODT, int GROUP, bool ZEROS, int U>
-static int launch_u(const GemvW4Args& a, hipStream_t s) {
+template <int ODT, int GROUP, bool ZEROS, int U, int C>
+static int launch_c(const GemvW4Args& a, hipStream_t s) {
   const bool by_row = a.experts && a.R < a.E;
   const int y = !a.experts ? 1 : std::min(a.R, a.E);
-  // Many rows of one matrix: four blocks of columns share what a workgroup
-  // reads of x, which is then more than it reads of the weights.
-  if (!a.experts && a.R > 16)
-    hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, 2, 4>), dim3((a.nb + 3) / 4, y), dim3(1024), 0, s, a, by_row);
-  else
-    hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, U, 1>), dim3(a.nb, y), dim3(256), 0, s, a, by_row);
+  hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, U, C>), dim3((a.nb + C - 1) / C, y), dim3(256), 0, s, a, by_row);
   return hipGetLastError();
 }
 
+// Few workgroups: one block of columns each, a whole row of blocks in flight.
+// Many (more than a device of 256 CUs holds at once): two blocks each, which
+// share x, its sums and what a workgroup costs by itself.
 template <int ODT, int GROUP, bool ZEROS>
 static int launch_zeros(const GemvW4Args& a, hipStream_t s) {
-  if (a.kb <= 8) return launch_u<ODT, GROUP, ZEROS, 2>(a, s);
-  if (a.kb <= 16) return launch_u<ODT, GROUP, ZEROS, 4>(a, s);
-  return launch_u<ODT, GROUP, ZEROS, 8>(a, s);
+  const int64_t items = (int64_t)a.nb * (!a.experts ? (a.R + 15) / 16 : std::min(a.R, a.E));
+  if (items >= kW4Many) return a.kb <= 8 ? launch_c<ODT, GROUP, ZEROS, 2, 2>(a, s) : launch_c<ODT, GROUP, ZEROS, 4, 2>(a, s);
+  if (a.kb <= 8) return launch_c<ODT, GROUP, ZEROS, 2, 1>(a, s);
+  if (a.kb <= 16) return launch_c<ODT, GROUP, ZEROS, 4, 1>(a, s);
+  return launch_c<ODT, GROUP, ZEROS, 8, 1>(a, s);
 }
 
 template <int ODT, int GROUP>
