@@ -24,8 +24,10 @@
 
 namespace hocf {
 
-constexpr int kW4XElems = 8192;   // x in LDS: token rows x rows of W, 16 KB
+// x in LDS, token rows x rows of W: 16 KB, or 64 KB for more rows than fit
+constexpr int kW4X = 8192, kW4XLarge = 32768;
 constexpr int kW4Many = 2048;     // (column block, expert) pairs from which a workgroup takes two blocks
+constexpr int kW4Few = 512;       // pairs up to which the large x area fits them all at once
 constexpr int kW4Pack = 256;      // threads of the packing kernel
 
 // Eight codes of one packed word as 16 + code, in row order: a rotation and one
@@ -54,13 +56,13 @@ __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
   return e < (uint32_t)a.E ? (int)e : -1;
 }
 
-template <int ODT, int GROUP, bool ZEROS, int U, int C>
-__global__ __launch_bounds__(256, C * U > 8 ? 2 : 4) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
+template <int ODT, int GROUP, bool ZEROS, int U, int C, int X>
+__global__ __launch_bounds__(256, X > kW4X ? 2 : C == 2 ? 3 : 4) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
   constexpr int kThreads = 256;
   constexpr int WPG = GROUP / 32;  // words of one group
   constexpr int GPB = 4 / WPG;     // groups of one block
-  constexpr int XP = kW4XElems / 8 / kThreads;  // 16-byte pieces of x that a thread moves
-  __shared__ __attribute__((aligned(16))) uint16_t s_x[kW4XElems + 16 * 8];
+  constexpr int XP = X / 8 / kThreads;  // 16-byte pieces of x that a thread moves
+  __shared__ __attribute__((aligned(16))) uint16_t s_x[X + 16 * 8];
   __shared__ float s_part[C][4][16][17];
   __shared__ uint16_t s_rows[kW4MaxRows], s_xrow[kW4MaxRows];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -99,11 +101,11 @@ __global__ __launch_bounds__(256, C * U > 8 ? 2 : 4) void gemv_w4_kernel(GemvW4A
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 
-  for (int r0 = 0; r0 < n_rows; r0 += 16) {
+  for (int r0 = blockIdx.z * 16; r0 < n_rows; r0 += gridDim.z * 16) {
     const int rows = min(16, n_rows - r0);
     // a pass takes U >> sh blocks of every wave: what fits x's rows
     int sh = 0;
-    while (rows > (kW4XElems / 512 / U) << sh) ++sh;
+    while (rows > (X / 512 / U) << sh) ++sh;
     const int chunk = (512 * U) >> sh, lp = __builtin_ctz(64 * U) - sh;  // rows of W; log2 of a row of x in pieces
     const int ldx = chunk + 8;                  // (rows of x start on different LDS banks)
     const int row_of = min(c, rows - 1) * ldx;  // (token rows past the last repeat it, unused)
@@ -115,6 +117,7 @@ __global__ __launch_bounds__(256, C * U > 8 ? 2 : 4) void gemv_w4_kernel(GemvW4A
       uint4 v[XP];
 #pragma unroll
       for (int p = 0; p < XP; ++p) {  // (past the last row or piece: repeated or unused)
+        if (p * kThreads >= rows << lp) break;
         const int i = threadIdx.x + p * kThreads, r = min(i >> lp, rows - 1), k = k0 + (i & ((1 << lp) - 1)) * 8;
         v[p] = *reinterpret_cast<const uint4*>(a.x + (int64_t)s_xrow[r0 + r] * a.K + min(k, a.K - 8));
         if (k >= a.K) v[p] = make_uint4(0, 0, 0, 0);  // rows of W beyond K
@@ -145,6 +148,7 @@ __global__ __launch_bounds__(256, C * U > 8 ? 2 : 4) void gemv_w4_kernel(GemvW4A
       lds_barrier();  // the last pass is done with x
 #pragma unroll
       for (int p = 0; p < XP; ++p) {
+        if (p * kThreads >= rows << lp) break;
         const int i = threadIdx.x + p * kThreads, r = i >> lp;
         if (r < rows) *reinterpret_cast<uint4*>(&s_x[r * ldx + (i & ((1 << lp) - 1)) * 8]) = v[p];
       }
@@ -199,28 +203,37 @@ __global__ __launch_bounds__(256, C * U > 8 ? 2 : 4) void gemv_w4_kernel(GemvW4A
         if (column < a.N) st1<ODT>(a.out, out + column, v);
       }
     }
-    if (r0 + 16 < n_rows) lds_barrier();
+    lds_barrier();
   }
 }
 
-template <int ODT, int GROUP, bool ZEROS, int U, int C>
-static int launch_c(const GemvW4Args& a, hipStream_t s) {
+template <int ODT, int GROUP, bool ZEROS, int U, int C, int X>
+static int launch_c(const GemvW4Args& a, int tiles, hipStream_t s) {
   const bool by_row = a.experts && a.R < a.E;
   const int y = !a.experts ? 1 : std::min(a.R, a.E);
-  hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, U, C>), dim3((a.nb + C - 1) / C, y), dim3(256), 0, s, a, by_row);
+  hipLaunchKernelGGL((gemv_w4_kernel<ODT, GROUP, ZEROS, U, C, X>), dim3((a.nb + C - 1) / C, y, tiles), dim3(256), 0, s, a,
+                     by_row);
   return hipGetLastError();
 }
 
 // Few workgroups: one block of columns each, a whole row of blocks in flight.
 // Many (more than a device of 256 CUs holds at once): two blocks each, which
-// share x, its sums and what a workgroup costs by itself.
+// share x, its sums and what a workgroup costs by itself.  Rows are expected
+// to spread evenly over the experts: tiles of 16 go to workgroups of their
+// own, and more than a tile's share of the small x area takes the large one.
 template <int ODT, int GROUP, bool ZEROS>
 static int launch_zeros(const GemvW4Args& a, hipStream_t s) {
-  const int64_t items = (int64_t)a.nb * (!a.experts ? (a.R + 15) / 16 : std::min(a.R, a.E));
-  if (items >= kW4Many) return a.kb <= 8 ? launch_c<ODT, GROUP, ZEROS, 2, 2>(a, s) : launch_c<ODT, GROUP, ZEROS, 4, 2>(a, s);
-  if (a.kb <= 8) return launch_c<ODT, GROUP, ZEROS, 2, 1>(a, s);
-  if (a.kb <= 16) return launch_c<ODT, GROUP, ZEROS, 4, 1>(a, s);
-  return launch_c<ODT, GROUP, ZEROS, 8, 1>(a, s);
+  const int rows = (a.R + a.E - 1) / a.E, tiles = (rows + 15) / 16;
+  const int64_t items = (int64_t)a.nb * std::min(a.R, a.E) * tiles;
+  const int u = a.kb <= 8 ? 2 : a.kb <= 16 ? 4 : 8;
+  if (std::min(rows, 16) * u * 512 > kW4X && (items <= kW4Few || rows > 8))
+    return a.kb <= 8 ? launch_c<ODT, GROUP, ZEROS, 2, 1, kW4XLarge>(a, tiles, s)
+                     : launch_c<ODT, GROUP, ZEROS, 4, 1, kW4XLarge>(a, tiles, s);
+  if (items >= kW4Many)
+    return u == 2 ? launch_c<ODT, GROUP, ZEROS, 2, 2, kW4X>(a, tiles, s) : launch_c<ODT, GROUP, ZEROS, 4, 2, kW4X>(a, tiles, s);
+  if (u == 2) return launch_c<ODT, GROUP, ZEROS, 2, 1, kW4X>(a, tiles, s);
+  if (u == 4) return launch_c<ODT, GROUP, ZEROS, 4, 1, kW4X>(a, tiles, s);
+  return launch_c<ODT, GROUP, ZEROS, 8, 1, kW4X>(a, tiles, s);
 }
 
 template <int ODT, int GROUP>
