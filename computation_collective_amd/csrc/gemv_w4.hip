@@ -57,7 +57,7 @@ __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
 }
 
 template <int ODT, int GROUP, bool ZEROS, int U, int C, int X>
-__global__ __launch_bounds__(256, X > kW4X ? 2 : C == 2 ? 3 : 4) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
+__global__ __launch_bounds__(256, X > kW4X ? 2 : 4) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
   constexpr int kThreads = 256;
   constexpr int WPG = GROUP / 32;  // words of one group
   constexpr int GPB = 4 / WPG;     // groups of one block
