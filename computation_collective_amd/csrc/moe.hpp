@@ -2,6 +2,8 @@
 // checks the arguments, the moe_*.hip and gemv_w4.hip units launch).
 #pragma once
 
+#include <algorithm>
+
 #include "internal.hpp"
 
 namespace hocf {
@@ -42,14 +44,14 @@ struct RouteBwdArgs {
 
 constexpr int kSlotsMaxBins = 64;   // one lane counts one bin
 constexpr int kSlotsThreads = 1024;
-constexpr int kSlotsMaxChunks = 512;
+constexpr int kSlotsMaxChunks = 256;
 
 struct SlotsArgs {
   const int32_t* experts;  // [pairs]
   int32_t* index;          // [pairs]
   int32_t* pair;           // [bins * cap]
   int64_t* counts;         // [bins]
-  uint32_t* hist;          // workspace: [chunks][64] pairs of each bin (chunked form only)
+  uint32_t* hist;          // workspace (chunked form only): the chunks' pairs of each bin
   uint32_t pairs, chunk;   // chunk: pairs of one workgroup, a multiple of kSlotsThreads
   uint32_t cap, experts_end;  // experts_end = bins * per_bin
   int bins, per_bin, chunks;
@@ -94,13 +96,12 @@ struct W4PackArgs {
 int launch_gemv_w4(const GemvW4Args& a, hipStream_t s);
 int launch_w4_pack(const W4PackArgs& a, hipStream_t s);
 
-// Pairs of one chunk, and how many chunks, for a number of pairs.
+// Pairs of one chunk, and how many chunks, for a number of pairs: a chunk for
+// every CU, and at most kSlotsMaxChunks.
 inline void slots_chunks(int64_t pairs, uint32_t* chunk, int* chunks) {
-  int64_t c = 4096;
-  if (pairs > c * kSlotsMaxChunks)
-    c = (pairs + (int64_t)kSlotsMaxChunks * kSlotsThreads - 1) / ((int64_t)kSlotsMaxChunks * kSlotsThreads) * kSlotsThreads;
-  *chunk = (uint32_t)c;
-  *chunks = (int)((pairs + c - 1) / c);
+  const int64_t c = (pairs + (int64_t)kSlotsMaxChunks * kSlotsThreads - 1) / ((int64_t)kSlotsMaxChunks * kSlotsThreads);
+  *chunk = (uint32_t)(std::max<int64_t>(c, 1) * kSlotsThreads);
+  *chunks = (int)((pairs + *chunk - 1) / *chunk);
 }
 
 int launch_moe_slots(const SlotsArgs& a, hipStream_t s);

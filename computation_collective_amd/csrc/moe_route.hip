@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "lanes.hpp"
 #include "moe.hpp"
 #include "publish.hpp"
 #include "sync.hpp"
@@ -54,53 +55,6 @@ struct Spread {
   int run;      // experts of one lane
   int size;     // experts of one group
 };
-
-template <int CTRL>
-__device__ __forceinline__ int dpp(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
-}
-template <int CTRL>
-__device__ __forceinline__ float dppf(float v) {
-  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v)));
-}
-// Reductions over the LPT lanes of a token: pairs, quads, halves and rows of
-// 16 by lane permutes, then across rows.
-template <int LPT>
-__device__ __forceinline__ int row_max(int v) {
-  v = max(v, dpp<0xB1>(v));
-  v = max(v, dpp<0x4E>(v));
-  v = max(v, dpp<0x141>(v));
-  v = max(v, dpp<0x140>(v));
-  if constexpr (LPT == 64) {
-    v = max(v, __shfl_xor(v, 16, 64));
-    v = max(v, __shfl_xor(v, 32, 64));
-  }
-  return v;
-}
-template <int LPT>
-__device__ __forceinline__ float row_maxf(float v) {
-  v = fmaxf(v, dppf<0xB1>(v));
-  v = fmaxf(v, dppf<0x4E>(v));
-  v = fmaxf(v, dppf<0x141>(v));
-  v = fmaxf(v, dppf<0x140>(v));
-  if constexpr (LPT == 64) {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    v = fmaxf(v, __shfl_xor(v, 32, 64));
-  }
-  return v;
-}
-template <int LPT>
-__device__ __forceinline__ float row_sum(float v) {
-  v += dppf<0xB1>(v);
-  v += dppf<0x4E>(v);
-  v += dppf<0x141>(v);
-  v += dppf<0x140>(v);
-  if constexpr (LPT == 64) {
-    v += __shfl_xor(v, 16, 64);
-    v += __shfl_xor(v, 32, 64);
-  }
-  return v;
-}
 
 // Toward zero, saturating (-inf gives INT_MIN).
 __device__ __forceinline__ int to_fixed(float f) {

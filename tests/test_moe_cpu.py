@@ -119,7 +119,7 @@ def test_slots_rejects(kw, expect):
 
 def test_slots_accepts():
     assert hocf.hocf_moe_slots_workspace_bytes(100, 2, 4) == 64 * 4
-    assert hocf.hocf_moe_slots_workspace_bytes(1 << 20, 8, 4) == 512 * 64 * 4
+    assert hocf.hocf_moe_slots_workspace_bytes(1 << 20, 8, 4) == 256 * 64 * 4
     assert hocf.hocf_moe_slots_workspace_bytes(0, 2, 4) == 0
     valid(slots())
     valid(slots(T=0, experts=None, index=None, s=sync(ws=0, nbytes=0)))
