@@ -16,46 +16,43 @@ namespace hocf {
 constexpr int kCombineThreads = 256;
 constexpr int64_t kMaxGrid = 1 << 23;  // workgroups of one launch (2^32 threads are too many)
 
+// 16-byte accesses of what is read or written once and not used again soon.
+typedef uint32_t uint32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint32x4 ld_once(const void* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const uint32x4*>(p));
+}
+__device__ __forceinline__ void st_once(void* p, uint32x4 v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<uint32x4*>(p));
+}
+
 // Eight consecutive elements: as loaded, and as fp32.
 template <int DT>
-struct Raw8;
-template <>
-struct Raw8<kBF16> {
-  uint4 u;
+struct Raw8 {
+  static constexpr int kPieces = DT == kBF16 ? 1 : 2;
+  uint32x4 u[kPieces];
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
-  }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const char* q = reinterpret_cast<const char*>(p) + i * (DT == kBF16 ? 2 : 4);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(w[k] << 16);
-      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-  }
-};
-template <>
-struct Raw8<kF32> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-    a = q[0];
-    b = q[1];
+    for (int k = 0; k < kPieces; ++k) u[k] = ld_once(q + 16 * k);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (DT == kBF16) f[k] = __uint_as_float(k & 1 ? u[0][k / 2] & 0xffff0000u : u[0][k / 2] << 16);
+      else f[k] = __uint_as_float(u[k / 4 % kPieces][k % 4]);
+    }
   }
 };
 template <int DT>
 __device__ __forceinline__ void st8(void* p, int64_t i, const float (&f)[8]) {
-  st4<DT>(p, i, floatx4{f[0], f[1], f[2], f[3]});
-  st4<DT>(p, i + 4, floatx4{f[4], f[5], f[6], f[7]});
-}
-template <>
-__device__ __forceinline__ void st8<kBF16>(void* p, int64_t i, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) =
-      make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  char* q = reinterpret_cast<char*>(p) + i * (DT == kBF16 ? 2 : 4);
+  if constexpr (DT == kBF16) {
+    st_once(q, uint32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])});
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; k += 4)
+      st_once(q + 4 * k, uint32x4{__float_as_uint(f[k]), __float_as_uint(f[k + 1]), __float_as_uint(f[k + 2]), __float_as_uint(f[k + 3])});
+  }
 }
 
 // Row of place j of token t, or -1.
