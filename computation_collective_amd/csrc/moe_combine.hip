@@ -35,6 +35,11 @@ struct Raw8 {
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) u[k] = ld_once(q + 16 * k);
   }
+  __device__ __forceinline__ void load_again(const void* p, int64_t i) {  // (stays in the caches)
+    const char* q = reinterpret_cast<const char*>(p) + i * (DT == kBF16 ? 2 : 4);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) u[k] = *reinterpret_cast<const uint32x4*>(q + 16 * k);
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -152,15 +157,25 @@ int launch_moe_combine(const CombineArgs& a, hipStream_t s) {
 // Backward.  The first workgroups zero the rows without a pair (kZeroRows
 // rows each, from the inverse map); the others take a token each (4 waves on
 // it) or a token per wave, read its dout and rows once, and write the rows'
-// gradients and the dot products.  A dot product's partial sums fold in a
+// gradients and the dot products.
+//
+// Rows that are not whole cache lines (kShifted): a wave's pieces of each row
+// start where the row's lines start, so that only a row's ends are written as
+// parts of lines (8191 x 8 rows of 4112 bytes: 152 us unshifted, where rows of
+// 4096 bytes take 134); dout is then read again at every row's pieces.  A dot product's partial sums fold in a
 // fixed order (a lane's pieces, the lanes by halves, the waves in order).
 constexpr int kZeroRows = 16;
+constexpr int kLine = 128;  // bytes of a cache line
 
-template <int DT, int ODT, int K, bool WIDE>
+enum BwdForm { kWide, kRows, kShifted };
+
+template <int DT, int ODT, int K, BwdForm FORM>
 __global__ __launch_bounds__(kCombineThreads) void combine_bwd_kernel(CombineArgs a, int64_t zero_blocks,
                                                                          int64_t blocks) {
+  constexpr bool WIDE = FORM == kWide;
+  constexpr int kPiece = 8 * (DT == kBF16 ? 2 : 4);  // bytes of a piece of a row
   __shared__ float s_dot[4][K];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int N = a.N;
   for (int64_t q = blockIdx.x; q < blocks; q += gridDim.x) {
     if (q < zero_blocks) {
@@ -188,27 +203,58 @@ __global__ __launch_bounds__(kCombineThreads) void combine_bwd_kernel(CombineArg
       w[j] = a.weights[t * a.topk + jj];
       dot[j] = 0.0f;
     }
-    for (int n = (WIDE ? (int)threadIdx.x : lane) * 8; n < N; n += (WIDE ? kCombineThreads : 64) * 8) {
-      Raw8<DT> v[K];
-      Raw8<ODT> d;
-      d.load(a.dout, t * N + n);
-      if (a.R > 0) {
+    if constexpr (FORM == kShifted) {
+      int lead[K];  // elements from the line's start to the row's
 #pragma unroll
-        for (int j = 0; j < K; ++j) v[j].load(a.rows, off[j] + n);
-      }
-      float g[8];
-      d.get(g);
+      for (int j = 0; j < K; ++j)
+        lead[j] = (int)((reinterpret_cast<uintptr_t>(a.drows) + off[j] * (kPiece / 8)) % kLine / kPiece) * 8;
+      for (int n0 = lane * 8; n0 - lane * 8 < N + kLine / kPiece * 8 - 8; n0 += 64 * 8) {
+        Raw8<DT> v[K];
+        Raw8<ODT> d[K];
 #pragma unroll
-      for (int j = 0; j < K; ++j) {
-        if (!live[j]) continue;
-        float f[8], o[8];
-        v[j].get(f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dot[j] = fmaf(f[i], g[i], dot[j]);
-          o[i] = w[j] * g[i];
+        for (int j = 0; j < K; ++j) {
+          const int n = min(max(n0 - lead[j], 0), N - 8);
+          d[j].load_again(a.dout, t * N + n);
+          v[j].load(a.rows, off[j] + n);
         }
-        st8<DT>(a.drows, off[j] + n, o);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          const int n = n0 - lead[j];
+          if (!live[j] || n < 0 || n >= N) continue;
+          float f[8], g[8], o[8];
+          v[j].get(f);
+          d[j].get(g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot[j] = fmaf(f[i], g[i], dot[j]);
+            o[i] = w[j] * g[i];
+          }
+          st8<DT>(a.drows, off[j] + n, o);
+        }
+      }
+    } else {
+      for (int n = (WIDE ? (int)threadIdx.x : lane) * 8; n < N; n += (WIDE ? kCombineThreads : 64) * 8) {
+        Raw8<DT> v[K];
+        Raw8<ODT> d;
+        d.load(a.dout, t * N + n);
+        if (a.R > 0) {
+#pragma unroll
+          for (int j = 0; j < K; ++j) v[j].load(a.rows, off[j] + n);
+        }
+        float g[8];
+        d.get(g);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          if (!live[j]) continue;
+          float f[8], o[8];
+          v[j].get(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot[j] = fmaf(f[i], g[i], dot[j]);
+            o[i] = w[j] * g[i];
+          }
+          st8<DT>(a.drows, off[j] + n, o);
+        }
       }
     }
 #pragma unroll
@@ -232,17 +278,21 @@ __global__ __launch_bounds__(kCombineThreads) void combine_bwd_kernel(CombineArg
   }
 }
 
+template <int DT, int ODT, int K, BwdForm FORM>
+static int launch_form(const CombineArgs& a, hipStream_t s) {
+  const int64_t zero = a.pair ? (a.R + kZeroRows - 1) / kZeroRows : 0;
+  const int64_t blocks = zero + (FORM == kWide ? a.T : (a.T + 3) / 4);
+  hipLaunchKernelGGL((combine_bwd_kernel<DT, ODT, K, FORM>), dim3((uint32_t)std::min(blocks, kMaxGrid)),
+                     dim3(kCombineThreads), 0, s, a, zero, blocks);
+  return hipGetLastError();
+}
+
+// Four waves on a token where tokens alone would not fill the device.
 template <int DT, int ODT, int K>
 static int launch_bwd(const CombineArgs& a, hipStream_t s) {
-  const int64_t zero = a.pair ? (a.R + kZeroRows - 1) / kZeroRows : 0;
-  const bool wide = a.T < 2048;
-  const int64_t blocks = zero + (wide ? a.T : (a.T + 3) / 4);
-  const uint32_t grid = (uint32_t)std::min(blocks, kMaxGrid);
-  if (wide)
-    hipLaunchKernelGGL((combine_bwd_kernel<DT, ODT, K, true>), dim3(grid), dim3(kCombineThreads), 0, s, a, zero, blocks);
-  else
-    hipLaunchKernelGGL((combine_bwd_kernel<DT, ODT, K, false>), dim3(grid), dim3(kCombineThreads), 0, s, a, zero, blocks);
-  return hipGetLastError();
+  if (a.T < 2048 || a.R == 0) return launch_form<DT, ODT, K, kWide>(a, s);
+  const bool lines = (int64_t)a.N * (DT == kBF16 ? 2 : 4) % kLine == 0 && reinterpret_cast<uintptr_t>(a.drows) % kLine == 0;
+  return lines ? launch_form<DT, ODT, K, kRows>(a, s) : launch_form<DT, ODT, K, kShifted>(a, s);
 }
 
 template <int DT, int ODT>
