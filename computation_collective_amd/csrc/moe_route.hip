@@ -19,14 +19,19 @@
 //         Different keys (slots aside) mean the same order of x, so only
 //         equal keys are in doubt; equal keys of bf16 logits that are not
 //         tiny are equal logits.
-//   Order = kByScore: v = (s + bias) * 2^29, off by at most 6.5 * 2^-24 (a
-//         sigmoid in 32 bits: 4 half steps of 1, the sum one or two, the
-//         conversion one), so neighbours nearer than kDoubt are in doubt.
+//   Order = kByScore: v = (s + bias) * 2^29.  A sigmoid in 32 bits is off by at
+//         most 3.1 * 2^-24 (exponent, sum and reciprocal), a sum below 4 by 2
+//         more, the conversion by one unit; a softmax by 35 * 2^-24 (the row's
+//         sum of up to 512 terms).  Neighbours nearer than that allows are in
+//         doubt.
 //
-// A token in doubt (also: a key outside the fixed-point range, a sigmoid
-// beyond 20 where 64 bits begin to saturate) is chosen again in 64 bits by
-// the whole wave: about 0.3 % of tokens with biased sigmoids over 256
-// experts, 1e-5 without a bias.
+// Neighbours in doubt are put in order by their exact values: a few more places
+// are chosen until the next one is clearly below, the lanes evaluate the
+// candidates in 64 bits and rank them.  What that cannot settle (a group's
+// place in doubt, a key outside the fixed-point range, a sigmoid beyond 20
+// where 64 bits begin to saturate, a softmax with a bias) is chosen again in
+// 64 bits by the whole wave: about 1e-4 of the tokens with biased sigmoids in
+// groups, none without.
 #include <algorithm>
 #include <climits>
 
@@ -42,7 +47,9 @@ constexpr int kRouteWaves = kRouteThreads / 64;
 
 enum Order : int { kByLogit, kByScore };
 constexpr float kLogitUnit = 0x1p26f, kScoreUnit = 0x1p29f;
-constexpr int kDoubt = 3 << 8;           // 1.5 * 2^-20 in units of 2^-29
+// Twice the error of a score, in units of 2^-29 (and of a group's half sum of
+// two scores, in units of 2^-28), without the keys' slots.
+constexpr int kDoubtSigmoid = 2 * 7 << 5, kDoubtSoftmax = 2 * 38 << 5;
 constexpr int kTiny = 1 << 13;           // logits below 2^-13: bf16 neighbours can share a key
 constexpr int kSaturated = 20 << 26;     // sigmoid(20) is 2e-9 from 1
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -66,7 +73,7 @@ __device__ __forceinline__ int to_fixed(float f) {
 __device__ __forceinline__ uint32_t apart(int a, int b) { return (uint32_t)max(a, b) - (uint32_t)min(a, b); }
 
 // A logit as the operators take it: NaN as -inf, +inf as the largest number.
-__device__ __forceinline__ float clean(float x) { return x > -INFINITY ? fminf(x, kMaxF) : -INFINITY; }
+__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINITY), kMaxF); }
 
 // A lane's experts: `cnt` from expert `at` on, held in the W slots from expert
 // `from` on (where at + W would leave the row, the slots start earlier, so
@@ -104,7 +111,11 @@ template <int DT, int W>
 __device__ __forceinline__ void load_logits(const char* row, const Run& r, float (&x)[W]) {
   load_row<DT, W>(row + r.from * (DT == kBF16 ? 2 : 4), x);
 #pragma unroll
-  for (int i = 0; i < W; ++i) x[i] = r.has(i) ? clean(x[i]) : -INFINITY;
+  for (int i = 0; i < W; ++i) x[i] = clean(x[i]);
+  if (!__all(r.cnt == W)) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = r.has(i) ? x[i] : -INFINITY;
+  }
 }
 
 template <int CTRL>
@@ -256,11 +267,12 @@ __device__ __forceinline__ void finish_counts(const RouteArgs& a, const uint32_t
 }
 
 template <int DT, int LPT, int W, Order ORDER>
-__global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Spread sp) {
+__global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 2 : 4) void route_kernel(RouteArgs a, Spread sp) {
   constexpr int TPW = 64 / LPT;  // tokens of one wave
   constexpr int kLow = INT_MIN + W;
   __shared__ double s_v[kRouteWaves][kRouteMaxE];
   __shared__ int s_pick[kRouteWaves * TPW][kRouteMaxTopk];
+  __shared__ float s_bias[ORDER == kByScore ? kRouteMaxE + W : 1];
   __shared__ uint32_t s_hist[kRouteMaxE];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -275,11 +287,11 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
   const int cnt = g < a.n_group ? min(max(sp.size - in_group, 0), sp.run) : 0;
   const Run mine = run_at<W>(cnt > 0 ? g * sp.size + in_group : 0, cnt, a.E);
   const bool softmax = a.score == kSoftmax;
-  float bias[W];
-  if constexpr (ORDER == kByScore) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) bias[i] = a.bias ? a.bias[min(mine.from + i, a.E - 1)] : 0.0f;
+  if constexpr (ORDER == kByScore) {  // (a NaN is as good as no expert)
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_bias[e] = a.bias ? fmaxf(a.bias[e], -INFINITY) : 0.0f;
+    __syncthreads();
   }
+  const uint32_t unsure = (softmax ? kDoubtSoftmax : kDoubtSigmoid) + 2 * W;
 
   const int64_t step = (int64_t)gridDim.x * kRouteWaves * TPW;
   for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * TPW; t0 < a.T; t0 += step) {
@@ -303,6 +315,8 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
       inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
     int k[W];
+    float bias[W];
+    if constexpr (ORDER == kByScore) __builtin_memcpy(bias, s_bias + mine.from, sizeof bias);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       float v = x[i] * kLogitUnit;
@@ -313,7 +327,8 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
       }
       k[i] = (to_fixed(v) & -W) | (W - 1 - i);
     }
-    bool doubt = false, kept = true;
+    // hard: to be chosen in 64 bits (the same in every lane of the token)
+    bool hard = false, kept = true;
     if (a.n_group > 1) {
       int m1 = INT_MIN, m2 = INT_MIN;
 #pragma unroll
@@ -326,65 +341,91 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Sp
         m2 = max(min(m1, o1), max(m2, o2));
         m1 = max(m1, o1);
       }
-      int of = m1 & -W;
+      const bool group = g < a.n_group;
+      int of = m1 & -W, low_of = kLow, unclear = m1 >= (INT_MAX & -W);
       if constexpr (ORDER == kByScore) {
         const bool two = a.group_top == 2 && sp.size > 1;
-        of = (m1 >> 1) + (two && m2 > kLow ? m2 >> 1 : 0);
-        if (a.bias && (m1 <= kLow || (two && m2 <= kLow))) doubt = true;
+        of = (m1 >> 1) + (two && m2 >= kLow ? m2 >> 1 : 0);
+        low_of = (kLow >> 1) + W;
+        unclear |= a.bias && (m1 < kLow || (two && m2 < kLow));
       }
-      doubt |= m1 >= (INT_MAX & -W);
-      if (g >= a.n_group) { of = INT_MIN; doubt = false; }
       int ahead = 0;
       for (int o = 0; o < a.n_group; ++o) {
         const int other = __shfl(of, o << sp.lg, LPT);
         ahead += other > of || (other == of && o < g);
-        if (o != g && m1 > kLow) {
-          if constexpr (ORDER == kByScore) doubt |= apart(other, of) < kDoubt + 2 * W;
-          else if (other == of) doubt |= DT != kBF16 || abs(of) < kTiny;
-        }
       }
       kept = ahead < a.topk_group;
-      doubt = row_max<LPT>(doubt);
+      // the last group that stays and the first that does not
+      const int in = ~row_max<LPT>(group && kept ? ~of : INT_MIN), out = row_max<LPT>(group && !kept ? of : INT_MIN);
+      hard = row_max<LPT>(group && unclear) != 0;
+      if (out > low_of) {
+        if constexpr (ORDER == kByScore) hard |= apart(in, out) < unsure;
+        else hard |= in == out && (DT != kBF16 || abs(in) < kTiny);
+      }
     }
-    int before = INT_MAX;
-    bool low = false;
-    for (int j = 0; j <= a.topk; ++j) {
+    int before = INT_MAX, n = 0;
+    bool low = false, near = false, open = false;
+    for (;; ++n) {
       int lm = k[0];
 #pragma unroll
       for (int i = 1; i < W; ++i) lm = max(lm, k[i]);
       lm = kept ? lm : INT_MIN;
       const int value = lm & -W;  // equal values go to the lower lane, whatever their slots
       const int m = row_max<LPT>(value);
-      // neighbours in doubt (the first left out among them)
-      if (m >= kLow) {
-        if constexpr (ORDER == kByScore) doubt |= j > 0 && apart(before, m) < kDoubt + 2 * W;
-        else doubt |= j > 0 && before == m && (DT != kBF16 || abs(m) < kTiny);
-        doubt |= m >= (INT_MAX & -W) || (ORDER == kByLogit && !softmax && m > kSaturated);
-      } else {
-        low = true;
+      const bool live = m >= kLow;
+      bool close = false;  // to the place before
+      if constexpr (ORDER == kByScore) close = live && apart(before, m) < unsure;
+      else close = live && before == m && (DT != kBF16 || abs(m) < kTiny);
+      if (n == 0) {
+        close = false;
+        hard |= live && (m >= (INT_MAX & -W) || (ORDER == kByLogit && !softmax && m > kSaturated));
       }
-      if (j == a.topk) break;
+      if (n < a.topk) {
+        near |= close;
+        low |= !live;
+      } else {  // beyond the last place: as far as it is in doubt
+        open = close && (open || n == a.topk);
+        near |= open;
+        hard |= open && n == kRouteMaxTopk;
+        if (n == kRouteMaxTopk || !__any(open)) break;
+      }
       before = m;
       const uint64_t b = __ballot(value == m);
       const uint32_t half = LPT == 64 || lane < 32 ? (uint32_t)b : (uint32_t)(b >> 32);
       const int first = LPT == 64 ? __builtin_ctzll(b) : __builtin_ctz((half >> (lane & 16)) & 0xffffu);
       const bool winner = l == first;
-      if (winner) picks[j] = m >= kLow ? mine.from + (W - 1 - (lm & (W - 1))) : -1;
+      if (winner) picks[n] = live ? mine.from + (W - 1 - (lm & (W - 1))) : -1;
       const int gone = winner ? lm : INT_MAX;
 #pragma unroll
       for (int i = 0; i < W; ++i) k[i] = k[i] == gone ? INT_MIN : k[i];
     }
     // below the keys' range: switched off, unless a live one is down there
     if (low) {
-      if (ORDER == kByScore) doubt |= a.bias != nullptr;
+      if (ORDER == kByScore) hard |= a.bias != nullptr;
       else {
         int down = 0;
 #pragma unroll
         for (int i = 0; i < W; ++i) down |= x[i] > -INFINITY && x[i] <= -31.0f;
-        doubt |= row_max<LPT>(down) != 0;
+        hard |= row_max<LPT>(down) != 0;
       }
     }
-    for (uint64_t todo = __ballot(doubt); todo;) {
+    if (ORDER == kByScore && softmax) hard |= near;  // (exact values need the row's exact sum)
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    if (__any(near && !hard)) {
+      // lane i: candidate i, ranked by its exact value, ties to the lower index
+      const int e = l < n ? picks[min(l, kRouteMaxTopk - 1)] : -1;
+      double v = e >= 0 ? (double)clean(ld1<DT>(row, e)) : -INFINITY;
+      if (ORDER == kByScore && e >= 0) v = 1.0 / (1.0 + exp(-v)) + (a.bias ? (double)a.bias[e] : 0.0);
+      int rank = 0;
+      for (int i = 0; i < n; ++i) {
+        const double o = __shfl(v, i, LPT);
+        const int oe = __shfl(e, i, LPT);
+        rank += o > v || (o == v && oe < e);
+      }
+      if (near && e >= 0 && rank < kRouteMaxTopk) picks[rank] = e;
+    }
+    for (uint64_t todo = __ballot(hard); todo;) {
       const int r = __builtin_ctzll(todo) / LPT;
       todo &= LPT == 64 ? 0 : ~(0xffffull << (r * 16));
       const int64_t tr = min(t0 + r, a.T - 1);
