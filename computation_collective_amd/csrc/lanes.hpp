@@ -8,7 +8,7 @@ namespace hocf {
 
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);  // (folds into the instruction that uses it)
 }
 template <int CTRL>
 __device__ __forceinline__ float dppf(float v) {

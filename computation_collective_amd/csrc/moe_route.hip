@@ -12,11 +12,13 @@
 // more than everything else here, so it is made on 32-bit integer keys and
 // kept only where they decide it:
 //
-//   key = v in fixed point, its low log2(W) bits replaced by the slot within
-//         the lane (lower slot, larger key), so that a lane's keys differ and
-//         the largest key names its slot.
+//   key = v in fixed point, its low bits (four, six with 64 lanes) replaced by
+//         the slot within the lane (lower slot, larger key), so that a lane's
+//         keys differ and the largest names its slot; for the comparison of
+//         the lanes' largest keys those bits hold the lane (lower lane, larger
+//         key), so that the largest names its lane.
 //   Order = kByLogit: without a bias, v rises with x, and v = x * 2^26.
-//         Different keys (slots aside) mean the same order of x, so only
+//         Different keys (low bits aside) mean the same order of x, so only
 //         equal keys are in doubt; equal keys of bf16 logits that are not
 //         tiny are equal logits.
 //   Order = kByScore: v = (s + bias) * 2^29.  A sigmoid in 32 bits is off by at
@@ -134,11 +136,13 @@ __device__ __forceinline__ double wave_maxd(double v) {
 }
 
 // The choice of one token in 64 bits, by a whole wave (lane l: experts l, l +
-// 64, ...; V of them); picks to LDS, -1 where none is left.  Few tokens come
-// here, but a wave that has one is the last to finish: it is laid out for a
-// short chain of dependent steps (some 3 us), not for few instructions.
+// 64, ...; V of them); picks to LDS, -1 where none is left, and a softmax's
+// largest logit and one over its sum.  Few tokens come here, but a wave that
+// has one is the last to finish: it is laid out for a short chain of dependent
+// steps (some 3 us), not for few instructions.
 template <int DT, int V>
-__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, double* lds, int* picks) {
+__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, double* lds, int* picks, float* top_out,
+                                         float* inv_out) {
   const int lane = threadIdx.x & 63, E = a.E;
   const double kOff = -INFINITY;
   float x[V], bias[V];
@@ -156,6 +160,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, do
 #pragma unroll
     for (int i = 0; i < V; ++i) top = fmax(top, (double)x[i]);
     top = wave_maxd(top);
+    *top_out = (float)top;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       v[i] = exp((double)x[i] - top);
@@ -165,6 +170,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, do
     for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = v[i] / sum;  // (sum = 0: every logit is off)
+    *inv_out = sum > 0.0 ? (float)(1.0 / sum) : 0.0f;
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 1.0 / (1.0 + exp(-(double)x[i]));
@@ -266,12 +272,52 @@ __device__ __forceinline__ void finish_counts(const RouteArgs& a, const uint32_t
   }
 }
 
+// Lane l of a token's lanes has the expert of place l: its weight, and both to
+// the outputs.  sigmoid(x) e^-c = e^(min(x, 0) - c) / (1 + e^-|x|); with renorm, c is the
+// largest exponent, so that the sum cannot vanish.
+template <int DT, int LPT>
+__device__ __forceinline__ void emit(const RouteArgs& a, int64_t t, bool own, int l, int e, float top, float inv, uint32_t* hist) {
+  const char* row = reinterpret_cast<const char*>(a.logits) + t * a.ld * (DT == kBF16 ? 2 : 4);
+  const bool softmax = a.score == kSoftmax, place = l < a.topk;
+  if (!place) e = -1;
+  const float x = e >= 0 ? clean(ld1<DT>(row, e)) : -INFINITY;
+  const float up = softmax ? x : fminf(x, 0.0f);
+  float c = softmax ? top : 0.0f;
+  if (a.renorm) c = fmaxf(row_maxf<LPT>(up), -kMaxF);
+  float w = e >= 0 && (softmax || x >= kVanished) ? expf(up - c) : 0.0f;
+  if (!softmax) {
+    w /= 1.0f + expf(-fabsf(x));
+    inv = 1.0f;
+  }
+  if (a.renorm) {
+    const float sum = row_sum<LPT>(w);
+    inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  }
+  if (place && own) {
+    a.experts[t * a.topk + l] = e;
+    a.weights[t * a.topk + l] = e >= 0 ? w * inv * a.scale : 0.0f;
+    if (a.counts && e >= 0) atomicAdd(&hist[e], 1u);
+  }
+}
+
+// A token whose candidates a wave has found but not ranked yet.
+struct Candidates {
+  int64_t t;
+  int n;
+  float top, inv;
+  int16_t e[kRouteMaxTopk];
+};
+constexpr int kWaveList = 8;       // of them, a wave (any more: chosen in 64 bits)
+constexpr int kLater = INT_MIN;    // stands in a token's first place until it is chosen in 64 bits
+
 template <int DT, int LPT, int W, Order ORDER>
-__global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 2 : 4) void route_kernel(RouteArgs a, Spread sp) {
+__global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel(RouteArgs a, Spread sp) {
   constexpr int TPW = 64 / LPT;  // tokens of one wave
-  constexpr int kLow = INT_MIN + W;
-  __shared__ double s_v[kRouteWaves][kRouteMaxE];
-  __shared__ int s_pick[kRouteWaves * TPW][kRouteMaxTopk];
+  constexpr int Q = LPT > W ? LPT : W;    // units of a key that hold the slot or the lane
+  constexpr int kLow = INT_MIN + Q;       // below: switched off (or far down)
+  __shared__ double s_v[kRouteWaves][LPT == 16 ? 256 : kRouteMaxE];
+  __shared__ int s_pick[kRouteWaves * TPW][kRouteMaxTopk + 1];  // (the last one: what nobody reads)
+  __shared__ Candidates s_list[kRouteWaves][kWaveList];
   __shared__ float s_bias[ORDER == kByScore ? kRouteMaxE + W : 1];
   __shared__ uint32_t s_hist[kRouteMaxE];
   __shared__ int s_last;
@@ -291,13 +337,19 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 2 : 4) void route_kernel
     for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_bias[e] = a.bias ? fmaxf(a.bias[e], -INFINITY) : 0.0f;
     __syncthreads();
   }
-  const uint32_t unsure = (softmax ? kDoubtSoftmax : kDoubtSigmoid) + 2 * W;
+  const uint32_t unsure = (softmax ? kDoubtSoftmax : kDoubtSigmoid) + 2 * Q;
 
-  const int64_t step = (int64_t)gridDim.x * kRouteWaves * TPW;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * TPW; t0 < a.T; t0 += step) {
+  // The 64-bit work waits until the wave's other tokens are done: here, its
+  // registers (the exponential's constants above all) would halve the waves.
+  int listed = 0;
+  bool left = false;
+  const int64_t begin = ((int64_t)blockIdx.x * kRouteWaves + wave) * TPW, step = (int64_t)gridDim.x * kRouteWaves * TPW;
+  for (int64_t t0 = begin; t0 < a.T; t0 += step) {
     const int64_t t = min(t0 + lane / LPT, a.T - 1);
     const bool own = t0 + lane / LPT < a.T;
-    const char* row = reinterpret_cast<const char*>(a.logits) + t * a.ld * (DT == kBF16 ? 2 : 4);
+    // (the wave's first row, and the lane's offset from it: up to 3 * 2^24 logits)
+    const char* row = reinterpret_cast<const char*>(a.logits) + t0 * a.ld * (DT == kBF16 ? 2 : 4) +
+                      (uint32_t)(t - t0) * (uint32_t)a.ld * (DT == kBF16 ? 2u : 4u);
     float x[W];
     load_logits<DT, W>(row, mine, x);
 
@@ -325,7 +377,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 2 : 4) void route_kernel
                                 : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[i] * kLog2e));
         v = x[i] > -INFINITY ? (s + bias[i]) * kScoreUnit : -INFINITY;
       }
-      k[i] = (to_fixed(v) & -W) | (W - 1 - i);
+      k[i] = (to_fixed(v) & -Q) | (Q - 1 - i);
     }
     // hard: to be chosen in 64 bits (the same in every lane of the token)
     bool hard = false, kept = true;
@@ -342,11 +394,11 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 2 : 4) void route_kernel
         m1 = max(m1, o1);
       }
       const bool group = g < a.n_group;
-      int of = m1 & -W, low_of = kLow, unclear = m1 >= (INT_MAX & -W);
+      int of = m1 & -Q, low_of = kLow, unclear = m1 >= (INT_MAX & -Q);
       if constexpr (ORDER == kByScore) {
         const bool two = a.group_top == 2 && sp.size > 1;
         of = (m1 >> 1) + (two && m2 >= kLow ? m2 >> 1 : 0);
-        low_of = (kLow >> 1) + W;
+        low_of = (kLow >> 1) + Q;
         unclear |= a.bias && (m1 < kLow || (two && m2 < kLow));
       }
       int ahead = 0;
@@ -363,41 +415,51 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 2 : 4) void route_kernel
         else hard |= in == out && (DT != kBF16 || abs(in) < kTiny);
       }
     }
-    int before = INT_MAX, n = 0;
-    bool low = false, near = false, open = false;
-    for (;; ++n) {
-      int lm = k[0];
+    // The next largest key, its place (losers write where nobody reads) and its removal.
+    auto largest = [&](int& lm) {
+      lm = k[0];
 #pragma unroll
       for (int i = 1; i < W; ++i) lm = max(lm, k[i]);
       lm = kept ? lm : INT_MIN;
-      const int value = lm & -W;  // equal values go to the lower lane, whatever their slots
-      const int m = row_max<LPT>(value);
-      const bool live = m >= kLow;
-      bool close = false;  // to the place before
-      if constexpr (ORDER == kByScore) close = live && apart(before, m) < unsure;
-      else close = live && before == m && (DT != kBF16 || abs(m) < kTiny);
-      if (n == 0) {
-        close = false;
-        hard |= live && (m >= (INT_MAX & -W) || (ORDER == kByLogit && !softmax && m > kSaturated));
-      }
-      if (n < a.topk) {
-        near |= close;
-        low |= !live;
-      } else {  // beyond the last place: as far as it is in doubt
-        open = close && (open || n == a.topk);
-        near |= open;
-        hard |= open && n == kRouteMaxTopk;
-        if (n == kRouteMaxTopk || !__any(open)) break;
-      }
-      before = m;
-      const uint64_t b = __ballot(value == m);
-      const uint32_t half = LPT == 64 || lane < 32 ? (uint32_t)b : (uint32_t)(b >> 32);
-      const int first = LPT == 64 ? __builtin_ctzll(b) : __builtin_ctz((half >> (lane & 16)) & 0xffffu);
-      const bool winner = l == first;
-      if (winner) picks[n] = live ? mine.from + (W - 1 - (lm & (W - 1))) : -1;
+      return (lm & -Q) | (LPT - 1 - l);
+    };
+    auto take = [&](int m, int key, int lm, int place) {
+      const bool winner = key == m;
+      picks[winner ? place : kRouteMaxTopk] = m >= kLow ? mine.from + Q - 1 - (lm & (Q - 1)) : -1;
       const int gone = winner ? lm : INT_MAX;
 #pragma unroll
       for (int i = 0; i < W; ++i) k[i] = k[i] == gone ? INT_MIN : k[i];
+    };
+    // How far two neighbours are apart, as far as it matters (m the lower one).
+    auto distance = [&](int before, int m) {
+      const uint32_t d = ORDER == kByScore ? (uint32_t)before - (uint32_t)m : (uint32_t)(before ^ m);
+      return m >= kLow ? d : UINT_MAX;
+    };
+    const uint32_t narrow = ORDER == kByScore ? unsure : Q;
+    int before = INT_MAX, most = 0, n = 0;
+    uint32_t gap = UINT_MAX;
+    for (; n < a.topk; ++n) {
+      int lm;
+      const int key = largest(lm), m = row_max<LPT>(key);
+      if (n == 0) most = m;
+      else gap = min(gap, distance(before, m));
+      take(m, key, lm, n);
+      before = m;
+    }
+    const bool low = before < kLow;
+    // bf16 logits that share a key are equal unless they are tiny
+    bool near = gap < narrow && (ORDER == kByScore || DT != kBF16 || (before < kTiny && most > -kTiny));
+    hard |= most >= (INT_MAX & -Q) || (ORDER == kByLogit && !softmax && most > kSaturated);
+    // beyond the last place: as far as it is in doubt
+    for (bool open = true;; ++n) {
+      int lm;
+      const int key = largest(lm), m = row_max<LPT>(key);
+      open &= distance(before, m) < narrow && (ORDER == kByScore || DT != kBF16 || abs(m) < kTiny + Q);
+      near |= open;
+      hard |= open && n == kRouteMaxTopk;
+      if (n == kRouteMaxTopk || !__any(open)) break;
+      take(m, key, lm, n);
+      before = m;
     }
     // below the keys' range: switched off, unless a live one is down there
     if (low) {
@@ -412,49 +474,71 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 2 : 4) void route_kernel
     if (ORDER == kByScore && softmax) hard |= near;  // (exact values need the row's exact sum)
     __threadfence_block();
     __builtin_amdgcn_wave_barrier();
-    if (__any(near && !hard)) {
-      // lane i: candidate i, ranked by its exact value, ties to the lower index
-      const int e = l < n ? picks[min(l, kRouteMaxTopk - 1)] : -1;
-      double v = e >= 0 ? (double)clean(ld1<DT>(row, e)) : -INFINITY;
-      if (ORDER == kByScore && e >= 0) v = 1.0 / (1.0 + exp(-v)) + (a.bias ? (double)a.bias[e] : 0.0);
-      int rank = 0;
-      for (int i = 0; i < n; ++i) {
-        const double o = __shfl(v, i, LPT);
-        const int oe = __shfl(e, i, LPT);
-        rank += o > v || (o == v && oe < e);
+    const int e = l < n ? picks[min(l, kRouteMaxTopk - 1)] : -1;
+    if (__any(near || hard)) {
+      // to the list, as far as there is room
+      const uint64_t want = __ballot(l == 0 && own && near && !hard);
+      const int at = listed + __builtin_popcountll(want & ((1ull << (lane & -LPT)) - 1));
+      const bool listing = own && near && !hard && at < kWaveList;
+      if (listing) {
+        Candidates& c = s_list[wave][at];
+        if (l < kRouteMaxTopk) c.e[l] = (int16_t)e;
+        if (l == 0) {
+          c.t = t;
+          c.n = n;
+          c.top = top;
+          c.inv = inv;
+        }
       }
-      if (near && e >= 0 && rank < kRouteMaxTopk) picks[rank] = e;
+      const bool later = own && (near || hard) && !listing;
+      if (later && l == 0) a.experts[t * a.topk] = kLater;
+      listed = min(listed + (int)__builtin_popcountll(want), kWaveList);
+      left |= __any(later);
     }
-    for (uint64_t todo = __ballot(hard); todo;) {
-      const int r = __builtin_ctzll(todo) / LPT;
-      todo &= LPT == 64 ? 0 : ~(0xffffull << (r * 16));
-      const int64_t tr = min(t0 + r, a.T - 1);
-      choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4), s_v[wave],
-                   s_pick[wave * TPW + r]);
+    emit<DT, LPT>(a, t, own && !near && !hard, l, e, top, inv, s_hist);
+    __builtin_amdgcn_wave_barrier();
+  }
+  __threadfence_block();
+  __builtin_amdgcn_wave_barrier();
+
+  // Candidates: lane i has candidate i, ranked by its exact value, ties to the lower index.
+  for (int i0 = 0; i0 < listed; i0 += TPW) {
+    const bool own = i0 + lane / LPT < listed;
+    const Candidates& c = s_list[wave][min(i0 + lane / LPT, listed - 1)];
+    const char* row = reinterpret_cast<const char*>(a.logits) + c.t * a.ld * (DT == kBF16 ? 2 : 4);
+    const int n = c.n, e = l < n ? c.e[min(l, kRouteMaxTopk - 1)] : -1;
+    double v = e >= 0 ? (double)clean(ld1<DT>(row, e)) : -INFINITY;
+    if (ORDER == kByScore && e >= 0) v = 1.0 / (1.0 + exp(-v)) + (a.bias ? (double)a.bias[e] : 0.0);
+    int rank = 0;
+    for (int i = 0; i < kRouteMaxTopk; ++i) {
+      const double o = __shfl(v, i, LPT);
+      const int oe = __shfl(e, i, LPT);
+      rank += i < n && (o > v || (o == v && oe < e));
     }
+    if (l < kRouteMaxTopk) picks[l] = -1;
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0 && rank < kRouteMaxTopk) picks[rank] = e;
     __threadfence_block();
     __builtin_amdgcn_wave_barrier();
-
-    // lane j: place j.  sigmoid(x) e^-c = e^(min(x, 0) - c) / (1 + e^-|x|); with
-    // renorm, c is the largest exponent, so that the sum cannot vanish
-    const bool place = l < a.topk;
-    const int e = place ? picks[l] : -1;
-    const float xe = e >= 0 ? clean(ld1<DT>(row, e)) : -INFINITY;
-    float up = softmax ? xe : fminf(xe, 0.0f);
-    float c = softmax ? top : 0.0f;
-    if (a.renorm) c = fmaxf(row_maxf<LPT>(up), -kMaxF);
-    float w = e >= 0 && (softmax || xe >= kVanished) ? expf(up - c) : 0.0f;
-    if (!softmax) w /= 1.0f + expf(-fabsf(xe));
-    if (a.renorm) {
-      const float sum = row_sum<LPT>(w);
-      inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    }
-    if (place && own) {
-      a.experts[t * a.topk + l] = e;
-      a.weights[t * a.topk + l] = e >= 0 ? w * inv * a.scale : 0.0f;
-      if (a.counts && e >= 0) atomicAdd(&s_hist[e], 1u);
-    }
+    emit<DT, LPT>(a, c.t, own, l, picks[min(l, kRouteMaxTopk - 1)], c.top, c.inv, s_hist);
     __builtin_amdgcn_wave_barrier();
+  }
+  if (left) {
+    wait_memory();  // the marks are there
+    for (int64_t t0 = begin; t0 < a.T; t0 += step) {
+      const int64_t t = min(t0 + lane / LPT, a.T - 1);
+      const int mark = __hip_atomic_load(&a.experts[t * a.topk], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (uint64_t todo = __ballot(l == 0 && t0 + lane / LPT < a.T && mark == kLater); todo; todo &= todo - 1) {
+        const int64_t tr = t0 + __builtin_ctzll(todo) / LPT;
+        float top = 0.0f, inv = 1.0f;
+        choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4),
+                                        s_v[wave], s_pick[wave * TPW], &top, &inv);
+        __threadfence_block();
+        __builtin_amdgcn_wave_barrier();
+        emit<DT, LPT>(a, tr, lane < LPT, l, s_pick[wave * TPW][min(l, kRouteMaxTopk - 1)], top, inv, s_hist);
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
   }
   if (a.counts) finish_counts(a, s_hist, &s_last);
 }
