@@ -480,7 +480,6 @@ class MoeRoute(_Moe):
             self.counts.fill_(-77)
 
 
-
 class MoeRouteBwd(_Moe):
     """hocf_moe_route_bwd: logits [T][E], the chosen experts [T][topk] and the gradients
     of their weights -> dlogits [T][E]."""
@@ -500,7 +499,6 @@ class MoeRouteBwd(_Moe):
         nan_fill(self.dlogits)
 
 
-
 class MoeSlots(_Moe):
     """hocf_moe_slots: experts [T][topk] -> index [T][topk], pair [bins * cap], counts [bins]."""
 
@@ -518,7 +516,6 @@ class MoeSlots(_Moe):
     def poison(self):
         for t in (self.index, self.pair, self.counts):
             t.fill_(-77)
-
 
 
 class MoeCombine(_Moe):
@@ -544,7 +541,6 @@ class MoeCombine(_Moe):
         nan_fill(self.out)
 
 
-
 class MoeCombineBwd(_Moe):
     """hocf_moe_combine_bwd: rows [R][N], weights [T][topk], dout [T][N], index [T][topk] and
     its inverse pair [R] (both None: pair order) -> drows [R][N], dweights [T][topk]."""
@@ -567,7 +563,6 @@ class MoeCombineBwd(_Moe):
     def poison(self):
         nan_fill(self.drows)
         nan_fill(self.dweights)
-
 
 
 def w4_layout(E, N, K, group):
