@@ -58,6 +58,25 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kVanished = -709.78f;    // a sigmoid below is 0 in 64 bits too
 constexpr float kMaxF = 3.402823466e38f;
 
+// A lane's keys in falling order: an odd-even merge sort, 63 exchanges of two
+// instructions for 16 keys.
+template <int W>
+__device__ __forceinline__ void sort_falling(int (&k)[W]) {
+#pragma unroll
+  for (int p = 1; p < W; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < W; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < W && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const int hi = max(k[i + j], k[i + j + q]);
+            k[i + j + q] = min(k[i + j], k[i + j + q]);
+            k[i + j] = hi;
+          }
+}
+
 // How a token's experts lie on its lanes.
 struct Spread {
   int lg;       // log2 of the lanes of one group
@@ -315,7 +334,12 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
   constexpr int TPW = 64 / LPT;  // tokens of one wave
   constexpr int Q = LPT > W ? LPT : W;    // units of a key that hold the slot or the lane
   constexpr int kLow = INT_MIN + Q;       // below: switched off (or far down)
-  __shared__ double s_v[kRouteWaves][LPT == 16 ? 256 : kRouteMaxE];
+  constexpr bool kListed = W > 4;  // the lanes' sorted keys are in LDS, but for the first two
+  // (one after the other: the keys, and the 64-bit values at the end)
+  __shared__ union {
+    double v[LPT == 16 ? 256 : kRouteMaxE];
+    int keys[kListed ? W + 1 : 1][64];
+  } s_wave[kRouteWaves];
   __shared__ int s_pick[kRouteWaves * TPW][kRouteMaxTopk + 1];  // (the last one: what nobody reads)
   __shared__ Candidates s_list[kRouteWaves][kWaveList];
   __shared__ float s_bias[ORDER == kByScore ? kRouteMaxE + W : 1];
@@ -366,28 +390,31 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
       sum = row_sum<LPT>(sum);
       inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    int k[W];
-    float bias[W];
-    if constexpr (ORDER == kByScore) __builtin_memcpy(bias, s_bias + mine.from, sizeof bias);
+    float v[W];
+    if constexpr (ORDER == kByScore) {
+      float bias[W];
+      __builtin_memcpy(bias, s_bias + mine.from, sizeof bias);
+      if (softmax) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      float v = x[i] * kLogitUnit;
-      if constexpr (ORDER == kByScore) {
-        const float s = softmax ? __builtin_amdgcn_exp2f((x[i] - top) * kLog2e) * inv
-                                : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[i] * kLog2e));
-        v = x[i] > -INFINITY ? (s + bias[i]) * kScoreUnit : -INFINITY;
+        for (int i = 0; i < W; ++i) v[i] = __builtin_amdgcn_exp2f((x[i] - top) * kLog2e) * inv;
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[i] * kLog2e));
       }
-      k[i] = (to_fixed(v) & -Q) | (Q - 1 - i);
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] = x[i] > -INFINITY ? (v[i] + bias[i]) * kScoreUnit : -INFINITY;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] = x[i] * kLogitUnit;
     }
+    int k[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) k[i] = (to_fixed(v[i]) & -Q) | (Q - 1 - i);
+    sort_falling<W>(k);
     // hard: to be chosen in 64 bits (the same in every lane of the token)
     bool hard = false, kept = true;
     if (a.n_group > 1) {
-      int m1 = INT_MIN, m2 = INT_MIN;
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        m2 = max(m2, min(m1, k[i]));
-        m1 = max(m1, k[i]);
-      }
+      int m1 = k[0], m2 = W > 1 ? k[W > 1] : INT_MIN;
       for (int d = 1; d < 1 << sp.lg; d *= 2) {
         const int o1 = __shfl_xor(m1, d, LPT), o2 = __shfl_xor(m2, d, LPT);
         m2 = max(min(m1, o1), max(m2, o2));
@@ -415,20 +442,37 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
         else hard |= in == out && (DT != kBF16 || abs(in) < kTiny);
       }
     }
-    // The next largest key, its place (losers write where nobody reads) and its removal.
-    auto largest = [&](int& lm) {
-      lm = k[0];
+    // The lanes' lists: the first key, the second, and where the third is.
+    if (!kept) {
 #pragma unroll
-      for (int i = 1; i < W; ++i) lm = max(lm, k[i]);
-      lm = kept ? lm : INT_MIN;
-      return (lm & -Q) | (LPT - 1 - l);
-    };
-    auto take = [&](int m, int key, int lm, int place) {
+      for (int i = 0; i < (kListed ? 2 : W); ++i) k[i] = INT_MIN;
+    }
+    int* const last = &s_wave[wave].keys[kListed ? W : 0][lane];  // (always INT_MIN)
+    const int* third = last;
+    if constexpr (kListed) {
+      __builtin_amdgcn_wave_barrier();  // (the wave is done with the last tokens' lists)
+#pragma unroll
+      for (int i = 2; i < W; ++i) s_wave[wave].keys[i][lane] = k[i];
+      *last = INT_MIN;
+      if (kept) third = &s_wave[wave].keys[2][lane];
+      __builtin_amdgcn_wave_barrier();
+    }
+    // The largest of the lanes' first keys (low bits: the lane), its place (losers
+    // write where nobody reads) and its removal.
+    auto largest = [&] { return (k[0] & -Q) | (LPT - 1 - l); };
+    auto take = [&](int m, int key, int place) {
       const bool winner = key == m;
-      picks[winner ? place : kRouteMaxTopk] = m >= kLow ? mine.from + Q - 1 - (lm & (Q - 1)) : -1;
-      const int gone = winner ? lm : INT_MAX;
+      picks[winner ? place : kRouteMaxTopk] = m >= kLow ? mine.from + Q - 1 - (k[0] & (Q - 1)) : -1;
+      if constexpr (kListed) {
+        const int after = *third;
+        k[0] = winner ? k[1] : k[0];
+        k[1] = winner ? after : k[1];
+        third += winner && third < last ? 64 : 0;
+      } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) k[i] = k[i] == gone ? INT_MIN : k[i];
+        for (int i = 0; i + 1 < W; ++i) k[i] = winner ? k[i + 1] : k[i];
+        k[W - 1] = winner ? INT_MIN : k[W - 1];
+      }
     };
     // How far two neighbours are apart, as far as it matters (m the lower one).
     auto distance = [&](int before, int m) {
@@ -439,11 +483,10 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
     int before = INT_MAX, most = 0, n = 0;
     uint32_t gap = UINT_MAX;
     for (; n < a.topk; ++n) {
-      int lm;
-      const int key = largest(lm), m = row_max<LPT>(key);
+      const int key = largest(), m = row_max<LPT>(key);
       if (n == 0) most = m;
       else gap = min(gap, distance(before, m));
-      take(m, key, lm, n);
+      take(m, key, n);
       before = m;
     }
     const bool low = before < kLow;
@@ -452,13 +495,12 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
     hard |= most >= (INT_MAX & -Q) || (ORDER == kByLogit && !softmax && most > kSaturated);
     // beyond the last place: as far as it is in doubt
     for (bool open = true;; ++n) {
-      int lm;
-      const int key = largest(lm), m = row_max<LPT>(key);
+      const int key = largest(), m = row_max<LPT>(key);
       open &= distance(before, m) < narrow && (ORDER == kByScore || DT != kBF16 || abs(m) < kTiny + Q);
       near |= open;
       hard |= open && n == kRouteMaxTopk;
       if (n == kRouteMaxTopk || !__any(open)) break;
-      take(m, key, lm, n);
+      take(m, key, n);
       before = m;
     }
     // below the keys' range: switched off, unless a live one is down there
@@ -532,7 +574,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
         const int64_t tr = t0 + __builtin_ctzll(todo) / LPT;
         float top = 0.0f, inv = 1.0f;
         choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4),
-                                        s_v[wave], s_pick[wave * TPW], &top, &inv);
+                                        s_wave[wave].v, s_pick[wave * TPW], &top, &inv);
         __threadfence_block();
         __builtin_amdgcn_wave_barrier();
         emit<DT, LPT>(a, tr, lane < LPT, l, s_pick[wave * TPW][min(l, kRouteMaxTopk - 1)], top, inv, s_hist);
