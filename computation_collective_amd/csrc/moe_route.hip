@@ -12,11 +12,9 @@
 // more than everything else here, so it is made on 32-bit integer keys and
 // kept only where they decide it:
 //
-//   key = v in fixed point, its low bits (four, six with 64 lanes) replaced by
-//         the slot within the lane (lower slot, larger key), so that a lane's
-//         keys differ and the largest names its slot; for the comparison of
-//         the lanes' largest keys those bits hold the lane (lower lane, larger
-//         key), so that the largest names its lane.
+//   key = v in fixed point, its low bits (Q units) replaced by the lane and the
+//         slot within the lane (lower index, larger key), so that a token's keys
+//         differ and the largest names its expert.
 //   Order = kByLogit: without a bias, v rises with x, and v = x * 2^26.
 //         Different keys (low bits aside) mean the same order of x, so only
 //         equal keys are in doubt; equal keys of bf16 logits that are not
@@ -26,6 +24,11 @@
 //         more, the conversion by one unit; a softmax by 35 * 2^-24 (the row's
 //         sum of up to 512 terms).  Neighbours nearer than that allows are in
 //         doubt.
+//
+// A lane sorts its keys once; a choice is then the largest of the lanes' first
+// keys, and its lane moves on by one.  The chosen keys go into a shift register
+// across the lanes of 16, newest in lane 0, where what is in doubt is seen for
+// all places at once.
 //
 // Neighbours in doubt are put in order by their exact values: a few more places
 // are chosen until the next one is clearly below, the lanes evaluate the
@@ -50,9 +53,8 @@ constexpr int kRouteWaves = kRouteThreads / 64;
 enum Order : int { kByLogit, kByScore };
 constexpr float kLogitUnit = 0x1p26f, kScoreUnit = 0x1p29f;
 // Twice the error of a score, in units of 2^-29 (and of a group's half sum of
-// two scores, in units of 2^-28), without the keys' slots.
+// two scores, in units of 2^-28); the keys' low bits come on top.
 constexpr int kDoubtSigmoid = 2 * 7 << 5, kDoubtSoftmax = 2 * 38 << 5;
-constexpr int kTiny = 1 << 13;           // logits below 2^-13: bf16 neighbours can share a key
 constexpr int kSaturated = 20 << 26;     // sigmoid(20) is 2e-9 from 1
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kVanished = -709.78f;    // a sigmoid below is 0 in 64 bits too
@@ -90,8 +92,6 @@ __device__ __forceinline__ int to_fixed(float f) {
   __asm__("v_cvt_i32_f32 %0, %1" : "=v"(r) : "v"(f));
   return r;
 }
-
-__device__ __forceinline__ uint32_t apart(int a, int b) { return (uint32_t)max(a, b) - (uint32_t)min(a, b); }
 
 // A logit as the operators take it: NaN as -inf, +inf as the largest number.
 __device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINITY), kMaxF); }
@@ -152,6 +152,14 @@ __device__ __forceinline__ double wave_maxd(double v) {
   v = fmax(v, dppd<0x140>(v));
   v = fmax(v, __shfl_xor(v, 16, 64));
   return fmax(v, __shfl_xor(v, 32, 64));
+}
+
+// Whether p holds in any lane of a token (16 or all 64).
+template <int LPT>
+__device__ __forceinline__ bool token_any(bool p) {
+  const uint64_t b = __ballot(p);
+  if (b == 0) return false;  // (the same in every lane)
+  return LPT == 64 || (b >> (threadIdx.x & 48) & 0xffffu) != 0;
 }
 
 // The choice of one token in 64 bits, by a whole wave (lane l: experts l, l +
@@ -291,14 +299,15 @@ __device__ __forceinline__ void finish_counts(const RouteArgs& a, const uint32_t
   }
 }
 
-// Lane l of a token's lanes has the expert of place l: its weight, and both to
-// the outputs.  sigmoid(x) e^-c = e^(min(x, 0) - c) / (1 + e^-|x|); with renorm, c is the
-// largest exponent, so that the sum cannot vanish.
+// A lane of a token has expert e (-1: none) of place `place` (outside [0, topk):
+// nothing): its weight, and both to the outputs.  sigmoid(x) e^-c = e^(min(x, 0) - c) / (1 + e^-|x|);
+// with renorm, c is the largest exponent, so that the sum cannot vanish.
 template <int DT, int LPT>
-__device__ __forceinline__ void emit(const RouteArgs& a, int64_t t, bool own, int l, int e, float top, float inv, uint32_t* hist) {
+__device__ __forceinline__ void emit(const RouteArgs& a, int64_t t, bool own, int place, int e, float top, float inv,
+                                     uint32_t* hist) {
   const char* row = reinterpret_cast<const char*>(a.logits) + t * a.ld * (DT == kBF16 ? 2 : 4);
-  const bool softmax = a.score == kSoftmax, place = l < a.topk;
-  if (!place) e = -1;
+  const bool softmax = a.score == kSoftmax, has = (uint32_t)place < (uint32_t)a.topk;
+  if (!has) e = -1;
   const float x = e >= 0 ? clean(ld1<DT>(row, e)) : -INFINITY;
   const float up = softmax ? x : fminf(x, 0.0f);
   float c = softmax ? top : 0.0f;
@@ -312,9 +321,9 @@ __device__ __forceinline__ void emit(const RouteArgs& a, int64_t t, bool own, in
     const float sum = row_sum<LPT>(w);
     inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   }
-  if (place && own) {
-    a.experts[t * a.topk + l] = e;
-    a.weights[t * a.topk + l] = e >= 0 ? w * inv * a.scale : 0.0f;
+  if (has && own) {
+    a.experts[t * a.topk + place] = e;
+    a.weights[t * a.topk + place] = e >= 0 ? w * inv * a.scale : 0.0f;
     if (a.counts && e >= 0) atomicAdd(&hist[e], 1u);
   }
 }
@@ -330,56 +339,71 @@ constexpr int kWaveList = 8;       // of them, a wave (any more: chosen in 64 bi
 constexpr int kLater = INT_MIN;    // stands in a token's first place until it is chosen in 64 bits
 
 template <int DT, int LPT, int W, Order ORDER>
-__global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel(RouteArgs a, Spread sp) {
-  constexpr int TPW = 64 / LPT;  // tokens of one wave
-  constexpr int Q = LPT > W ? LPT : W;    // units of a key that hold the slot or the lane
+__global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void route_kernel(RouteArgs a, Spread sp) {
+  constexpr int es = DT == kBF16 ? 2 : 4;
+  constexpr int TPW = 64 / LPT;           // tokens of one wave
+  constexpr int Q = LPT * W;              // units of a key that hold the lane and the slot
   constexpr int kLow = INT_MIN + Q;       // below: switched off (or far down)
-  constexpr bool kListed = W > 4;  // the lanes' sorted keys are in LDS, but for the first two
+  constexpr int kTop = INT_MAX & -Q;      // from here on: beyond the fixed-point range
+  constexpr int kTiny = 512 * Q;          // below: bf16 neighbours can share a key
+  constexpr bool kListed = W > 4;         // the lanes' sorted keys are in LDS, but for the first two
   // (one after the other: the keys, and the 64-bit values at the end)
   __shared__ union {
     double v[LPT == 16 ? 256 : kRouteMaxE];
     int keys[kListed ? W + 1 : 1][64];
   } s_wave[kRouteWaves];
-  __shared__ int s_pick[kRouteWaves * TPW][kRouteMaxTopk + 1];  // (the last one: what nobody reads)
+  __shared__ int s_pick[kRouteWaves][kRouteMaxTopk];
   __shared__ Candidates s_list[kRouteWaves][kWaveList];
-  __shared__ float s_bias[ORDER == kByScore ? kRouteMaxE + W : 1];
   __shared__ uint32_t s_hist[kRouteMaxE];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int l = lane & (LPT - 1);
-  int* picks = s_pick[wave * TPW + lane / LPT];
-  if (a.counts) {
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_hist[e] = 0;
-    __syncthreads();
-  }
+  const int l = lane & (LPT - 1), row_lane = lane & 15;
   // this lane's run of experts
   const int g = l >> sp.lg, in_group = (l & ((1 << sp.lg) - 1)) * sp.run;
   const int cnt = g < a.n_group ? min(max(sp.size - in_group, 0), sp.run) : 0;
   const Run mine = run_at<W>(cnt > 0 ? g * sp.size + in_group : 0, cnt, a.E);
   const bool softmax = a.score == kSoftmax;
-  if constexpr (ORDER == kByScore) {  // (a NaN is as good as no expert)
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_bias[e] = a.bias ? fmaxf(a.bias[e], -INFINITY) : 0.0f;
-    __syncthreads();
-  }
-  const uint32_t unsure = (softmax ? kDoubtSoftmax : kDoubtSigmoid) + 2 * Q;
+  const int low_bits = (LPT - 1 - l) * W;
 
   // The 64-bit work waits until the wave's other tokens are done: here, its
   // registers (the exponential's constants above all) would halve the waves.
   int listed = 0;
   bool left = false;
   const int64_t begin = ((int64_t)blockIdx.x * kRouteWaves + wave) * TPW, step = (int64_t)gridDim.x * kRouteWaves * TPW;
+  auto row_at = [&](int64_t t0) {  // (the wave's first row, and the lane's offset from it: up to 3 * 2^24 logits)
+    const uint32_t off = (uint32_t)(min(t0 + lane / LPT, a.T - 1) - t0) * (uint32_t)a.ld;
+    return reinterpret_cast<const char*>(a.logits) + t0 * a.ld * es + off * (uint32_t)es;
+  };
+  float x[W], bias[W];
+  if (begin < a.T) load_row<DT, W>(row_at(begin) + mine.from * es, x);
+  if constexpr (ORDER == kByScore) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) bias[i] = 0.0f;
+    if (a.bias) load_row<kF32, W>(a.bias + mine.from, bias);
+  }
+  if (a.counts) {
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_hist[e] = 0;
+    lds_barrier();
+  }
+  if constexpr (ORDER == kByScore) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) bias[i] = fmaxf(bias[i], -INFINITY) * kScoreUnit;  // (a NaN is as good as no expert)
+  }
   for (int64_t t0 = begin; t0 < a.T; t0 += step) {
-    const int64_t t = min(t0 + lane / LPT, a.T - 1);
-    const bool own = t0 + lane / LPT < a.T;
-    // (the wave's first row, and the lane's offset from it: up to 3 * 2^24 logits)
-    const char* row = reinterpret_cast<const char*>(a.logits) + t0 * a.ld * (DT == kBF16 ? 2 : 4) +
-                      (uint32_t)(t - t0) * (uint32_t)a.ld * (DT == kBF16 ? 2u : 4u);
-    float x[W];
-    load_logits<DT, W>(row, mine, x);
-
+    // switched-off logits, and other lanes' slots
+    bool live = mine.cnt == W;
+#pragma unroll
+    for (int i = 0; i < W; ++i) live &= x[i] > -INFINITY;
+    const bool gaps = !__all(live);
+    if (gaps) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = mine.has(i) && x[i] > -INFINITY ? x[i] : -INFINITY;
+    }
     // softmax: the row's largest logit and sum
     float top = 0.0f, inv = 1.0f;
     if (softmax && (ORDER == kByScore || !a.renorm)) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = fminf(x[i], kMaxF);
       top = x[0];
 #pragma unroll
       for (int i = 1; i < W; ++i) top = fmaxf(top, x[i]);
@@ -392,8 +416,6 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
     }
     float v[W];
     if constexpr (ORDER == kByScore) {
-      float bias[W];
-      __builtin_memcpy(bias, s_bias + mine.from, sizeof bias);
       if (softmax) {
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] = __builtin_amdgcn_exp2f((x[i] - top) * kLog2e) * inv;
@@ -402,51 +424,68 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
         for (int i = 0; i < W; ++i) v[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[i] * kLog2e));
       }
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = x[i] > -INFINITY ? (v[i] + bias[i]) * kScoreUnit : -INFINITY;
+      for (int i = 0; i < W; ++i) v[i] = fmaf(v[i], kScoreUnit, bias[i]);
+      if (gaps) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = x[i] > -INFINITY ? v[i] : -INFINITY;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < W; ++i) v[i] = x[i] * kLogitUnit;
     }
+    // the next tokens' logits are on their way during the choice
+    if (t0 + step < a.T) load_row<DT, W>(row_at(t0 + step) + mine.from * es, x);
     int k[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) k[i] = (to_fixed(v[i]) & -Q) | (Q - 1 - i);
+    for (int i = 0; i < W; ++i) k[i] = (to_fixed(v[i]) & -Q) | (low_bits + W - 1 - i);
     sort_falling<W>(k);
-    // hard: to be chosen in 64 bits (the same in every lane of the token)
-    bool hard = false, kept = true;
+    // to be chosen in 64 bits (the same in every lane of the token)
+    bool hard = false;
     if (a.n_group > 1) {
       int m1 = k[0], m2 = W > 1 ? k[W > 1] : INT_MIN;
-      for (int d = 1; d < 1 << sp.lg; d *= 2) {
-        const int o1 = __shfl_xor(m1, d, LPT), o2 = __shfl_xor(m2, d, LPT);
+      auto merge = [&](int o1, int o2) {
         m2 = max(min(m1, o1), max(m2, o2));
         m1 = max(m1, o1);
+      };
+      if (sp.lg > 0) merge(dpp<0xB1>(m1), dpp<0xB1>(m2));
+      if (sp.lg > 1) merge(dpp<0x4E>(m1), dpp<0x4E>(m2));
+      if (sp.lg > 2) merge(dpp<0x141>(m1), dpp<0x141>(m2));
+      if constexpr (LPT == 64) {
+        if (sp.lg > 3) merge(dpp<0x140>(m1), dpp<0x140>(m2));
+        if (sp.lg > 4) merge(__shfl_xor(m1, 16, 64), __shfl_xor(m2, 16, 64));
       }
       const bool group = g < a.n_group;
-      int of = m1 & -Q, low_of = kLow, unclear = m1 >= (INT_MAX & -Q);
+      int of = m1 & -Q, low_of = kLow;
+      bool unclear = m1 >= kTop;
       if constexpr (ORDER == kByScore) {
         const bool two = a.group_top == 2 && sp.size > 1;
-        of = (m1 >> 1) + (two && m2 >= kLow ? m2 >> 1 : 0);
+        of = (of >> 1) + (two && m2 >= kLow ? (m2 & -Q) >> 1 : 0);
         low_of = (kLow >> 1) + Q;
         unclear |= a.bias && (m1 < kLow || (two && m2 < kLow));
       }
-      int ahead = 0;
-      for (int o = 0; o < a.n_group; ++o) {
-        const int other = __shfl(of, o << sp.lg, LPT);
-        ahead += other > of || (other == of && o < g);
+      // one by one, the lower of equals first; the last that stays, and the first that does not
+      of = group ? (of & -LPT) | (LPT - 1 - (l >> sp.lg << sp.lg)) : INT_MIN;
+      bool kept = false;
+      int in = 0;
+      for (int j = 0; j < a.topk_group; ++j) {
+        in = row_max<LPT>(of);
+        const bool best = of == in;
+        kept |= best;
+        of = best ? INT_MIN : of;
       }
-      kept = ahead < a.topk_group;
-      // the last group that stays and the first that does not
-      const int in = ~row_max<LPT>(group && kept ? ~of : INT_MIN), out = row_max<LPT>(group && !kept ? of : INT_MIN);
-      hard = row_max<LPT>(group && unclear) != 0;
+      const int out = row_max<LPT>(of);
       if (out > low_of) {
-        if constexpr (ORDER == kByScore) hard |= apart(in, out) < unsure;
-        else hard |= in == out && (DT != kBF16 || abs(in) < kTiny);
+        if constexpr (ORDER == kByScore)
+          hard = (uint32_t)in - (uint32_t)out < (softmax ? kDoubtSoftmax : kDoubtSigmoid) + Q + 2 * LPT;
+        else hard = ((in ^ out) & -LPT) == 0 && (DT != kBF16 || abs(in) < kTiny);
+      }
+      hard |= token_any<LPT>(group && unclear);
+      if (!kept) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) k[i] = INT_MIN;
       }
     }
-    // The lanes' lists: the first key, the second, and where the third is.
-    if (!kept) {
-#pragma unroll
-      for (int i = 0; i < (kListed ? 2 : W); ++i) k[i] = INT_MIN;
-    }
+    // The lanes' lists: the first key and the second, and where the third is.
     int* const last = &s_wave[wave].keys[kListed ? W : 0][lane];  // (always INT_MIN)
     const int* third = last;
     if constexpr (kListed) {
@@ -454,69 +493,80 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
 #pragma unroll
       for (int i = 2; i < W; ++i) s_wave[wave].keys[i][lane] = k[i];
       *last = INT_MIN;
-      if (kept) third = &s_wave[wave].keys[2][lane];
+      third = &s_wave[wave].keys[2][lane];
+      __threadfence_block();
       __builtin_amdgcn_wave_barrier();
     }
-    // The largest of the lanes' first keys (low bits: the lane), its place (losers
-    // write where nobody reads) and its removal.
-    auto largest = [&] { return (k[0] & -Q) | (LPT - 1 - l); };
-    auto take = [&](int m, int key, int place) {
-      const bool winner = key == m;
-      picks[winner ? place : kRouteMaxTopk] = m >= kLow ? mine.from + Q - 1 - (k[0] & (Q - 1)) : -1;
+    // The next choice: the largest of the first keys; its lane moves on.
+    auto choose = [&] {
       if constexpr (kListed) {
-        const int after = *third;
+        int after = *third;
+        const int m = row_max<LPT>(k[0]);
+        __asm__ volatile("" : "+v"(after));  // (read in time, not when it is needed)
+        const bool winner = k[0] == m;
         k[0] = winner ? k[1] : k[0];
         k[1] = winner ? after : k[1];
         third += winner && third < last ? 64 : 0;
+        return m;
       } else {
+        const int m = row_max<LPT>(k[0]);
+        const bool winner = k[0] == m;
 #pragma unroll
         for (int i = 0; i + 1 < W; ++i) k[i] = winner ? k[i + 1] : k[i];
         k[W - 1] = winner ? INT_MIN : k[W - 1];
+        return m;
       }
     };
-    // How far two neighbours are apart, as far as it matters (m the lower one).
-    auto distance = [&](int before, int m) {
-      const uint32_t d = ORDER == kByScore ? (uint32_t)before - (uint32_t)m : (uint32_t)(before ^ m);
-      return m >= kLow ? d : UINT_MAX;
+    auto shift_in = [&](int m, int q) { return __builtin_amdgcn_update_dpp(m, q, 0x111, 0xf, 0xf, false); };
+    // Lane i of 16 has the choice of place n - 1 - i.
+    int q = INT_MIN, n = 0;
+    for (; n < a.topk; ++n) q = shift_in(choose(), q);
+    int next = row_max<LPT>(k[0]);
+    // whether two neighbours are in doubt (m the lower one)
+    auto close = [&](int before, int m) {
+      if (m < kLow) return false;
+      if constexpr (ORDER == kByScore)
+        return (uint32_t)(before & -Q) - (uint32_t)(m & -Q) < (softmax ? kDoubtSoftmax : kDoubtSigmoid) + (uint32_t)Q;
+      else return ((before ^ m) & -Q) == 0 && (DT != kBF16 || abs(m) < kTiny);
     };
-    const uint32_t narrow = ORDER == kByScore ? unsure : Q;
-    int before = INT_MAX, most = 0, n = 0;
-    uint32_t gap = UINT_MAX;
-    for (; n < a.topk; ++n) {
-      const int key = largest(), m = row_max<LPT>(key);
-      if (n == 0) most = m;
-      else gap = min(gap, distance(before, m));
-      take(m, key, n);
-      before = m;
-    }
-    const bool low = before < kLow;
-    // bf16 logits that share a key are equal unless they are tiny
-    bool near = gap < narrow && (ORDER == kByScore || DT != kBF16 || (before < kTiny && most > -kTiny));
-    hard |= most >= (INT_MAX & -Q) || (ORDER == kByLogit && !softmax && most > kSaturated);
-    // beyond the last place: as far as it is in doubt
-    for (bool open = true;; ++n) {
-      const int key = largest(), m = row_max<LPT>(key);
-      open &= distance(before, m) < narrow && (ORDER == kByScore || DT != kBF16 || abs(m) < kTiny + Q);
-      near |= open;
-      hard |= open && n == kRouteMaxTopk;
-      if (n == kRouteMaxTopk || !__any(open)) break;
-      take(m, key, n);
-      before = m;
-    }
-    // below the keys' range: switched off, unless a live one is down there
-    if (low) {
-      if (ORDER == kByScore) hard |= a.bias != nullptr;
-      else {
-        int down = 0;
+    bool doubt = row_lane < n && close(q, shift_in(next, q));
+    const bool below = row_lane < n && q < kLow;  // the key of no live expert, or of one that is far down
+    bool extreme = row_lane < n && (q >= kTop || (ORDER == kByLogit && !softmax && q > kSaturated));
+    bool near = false;
+    if (__any(doubt || below || extreme)) {
+      if (ORDER == kByScore) extreme |= below && a.bias;
+      else if (token_any<LPT>(below)) {
+        float y[W];
+        load_row<DT, W>(row_at(t0) + mine.from * es, y);
+        bool down = false;
 #pragma unroll
-        for (int i = 0; i < W; ++i) down |= x[i] > -INFINITY && x[i] <= -31.0f;
-        hard |= row_max<LPT>(down) != 0;
+        for (int i = 0; i < W; ++i) down |= mine.has(i) && y[i] > -INFINITY && y[i] <= -31.0f;
+        extreme |= token_any<LPT>(down);
       }
+      hard |= token_any<LPT>(extreme);
+      near = token_any<LPT>(doubt);
+      // beyond the last place: as far as it is in doubt
+      bool open = token_any<LPT>(doubt && row_lane == 0);
+      while (__any(open)) {
+        if (n == kRouteMaxTopk) {
+          hard |= open;
+          break;
+        }
+        const int m = choose();
+        q = shift_in(m, q);
+        ++n;
+        next = row_max<LPT>(k[0]);
+        open &= close(m, next);
+      }
+      if (ORDER == kByScore && softmax) hard |= near;  // (exact values need the row's exact sum)
     }
-    if (ORDER == kByScore && softmax) hard |= near;  // (exact values need the row's exact sum)
-    __threadfence_block();
-    __builtin_amdgcn_wave_barrier();
-    const int e = l < n ? picks[min(l, kRouteMaxTopk - 1)] : -1;
+    // the expert of a key: its lane and its slot
+    const int of_lane = LPT - 1 - (int)((uint32_t)q / W & (LPT - 1));
+    const int from = __shfl(mine.from, of_lane, LPT);
+    const int place = row_lane < n && l < 16 ? n - 1 - row_lane : -1;
+    const int e = place >= 0 && q >= kLow ? from + W - 1 - (q & (W - 1)) : -1;
+    const int64_t t = min(t0 + lane / LPT, a.T - 1);
+    const bool own = t0 + lane / LPT < a.T;
     if (__any(near || hard)) {
       // to the list, as far as there is room
       const uint64_t want = __ballot(l == 0 && own && near && !hard);
@@ -537,17 +587,16 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
       listed = min(listed + (int)__builtin_popcountll(want), kWaveList);
       left |= __any(later);
     }
-    emit<DT, LPT>(a, t, own && !near && !hard, l, e, top, inv, s_hist);
-    __builtin_amdgcn_wave_barrier();
+    emit<DT, LPT>(a, t, own && !near && !hard, place, e, top, inv, s_hist);
   }
   __threadfence_block();
   __builtin_amdgcn_wave_barrier();
 
-  // Candidates: lane i has candidate i, ranked by its exact value, ties to the lower index.
+  // Candidates: a lane each, ranked by their exact values, ties to the lower index.
   for (int i0 = 0; i0 < listed; i0 += TPW) {
     const bool own = i0 + lane / LPT < listed;
     const Candidates& c = s_list[wave][min(i0 + lane / LPT, listed - 1)];
-    const char* row = reinterpret_cast<const char*>(a.logits) + c.t * a.ld * (DT == kBF16 ? 2 : 4);
+    const char* row = reinterpret_cast<const char*>(a.logits) + c.t * a.ld * es;
     const int n = c.n, e = l < n ? c.e[min(l, kRouteMaxTopk - 1)] : -1;
     double v = e >= 0 ? (double)clean(ld1<DT>(row, e)) : -INFINITY;
     if (ORDER == kByScore && e >= 0) v = 1.0 / (1.0 + exp(-v)) + (a.bias ? (double)a.bias[e] : 0.0);
@@ -555,15 +604,9 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
     for (int i = 0; i < kRouteMaxTopk; ++i) {
       const double o = __shfl(v, i, LPT);
       const int oe = __shfl(e, i, LPT);
-      rank += i < n && (o > v || (o == v && oe < e));
+      rank += i < n && (o > v || (o == v && (oe < e || (oe == e && i < l))));
     }
-    if (l < kRouteMaxTopk) picks[l] = -1;
-    __builtin_amdgcn_wave_barrier();
-    if (e >= 0 && rank < kRouteMaxTopk) picks[rank] = e;
-    __threadfence_block();
-    __builtin_amdgcn_wave_barrier();
-    emit<DT, LPT>(a, c.t, own, l, picks[min(l, kRouteMaxTopk - 1)], c.top, c.inv, s_hist);
-    __builtin_amdgcn_wave_barrier();
+    emit<DT, LPT>(a, c.t, own, l < n ? rank : -1, e, c.top, c.inv, s_hist);
   }
   if (left) {
     wait_memory();  // the marks are there
@@ -573,11 +616,11 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : 6) void route_kernel
       for (uint64_t todo = __ballot(l == 0 && t0 + lane / LPT < a.T && mark == kLater); todo; todo &= todo - 1) {
         const int64_t tr = t0 + __builtin_ctzll(todo) / LPT;
         float top = 0.0f, inv = 1.0f;
-        choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * (DT == kBF16 ? 2 : 4),
-                                        s_wave[wave].v, s_pick[wave * TPW], &top, &inv);
+        choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * es, s_wave[wave].v,
+                                        s_pick[wave], &top, &inv);
         __threadfence_block();
         __builtin_amdgcn_wave_barrier();
-        emit<DT, LPT>(a, tr, lane < LPT, l, s_pick[wave * TPW][min(l, kRouteMaxTopk - 1)], top, inv, s_hist);
+        emit<DT, LPT>(a, tr, lane < LPT, l, s_pick[wave][min(l, kRouteMaxTopk - 1)], top, inv, s_hist);
         __builtin_amdgcn_wave_barrier();
       }
     }
