@@ -12,10 +12,10 @@ constexpr int kRouteMaxE = 512;     // experts of one router row
 constexpr int kRouteMaxTopk = 16;   // choices of one token
 constexpr int kRouteMaxGroups = 64;
 
-// With counts, the router's workspace: word 0 counts the workgroups that have
-// finished, then kCountCopies tables of the experts' counts; all left zeroed.
-constexpr int kCountWords = 32, kCountCopies = 8;
-__host__ __device__ constexpr int route_count_stride(int E) { return (E + 31) / 32 * 32; }
+// With counts, the router's workspace: a table of the experts' counts, then
+// kCountCopies tables that workgroups add to, 64 bits a word; all left zeroed.
+constexpr int kCountCopies = 8;
+__host__ __device__ constexpr int route_count_stride(int E) { return (E + 15) / 16 * 16; }
 
 enum Score : int { kSoftmax = 0, kSigmoid = 1 };
 
@@ -25,7 +25,7 @@ struct RouteArgs {
   int32_t* experts;    // [T][topk]
   float* weights;      // [T][topk]
   int32_t* counts;     // [E] or NULL
-  uint32_t* ws;        // with counts
+  uint64_t* ws;        // with counts
   int64_t T, ld;
   int E, topk, dt, score, n_group, topk_group, group_top, renorm;
   float scale;

@@ -38,7 +38,7 @@ extern "C" {
 /* ------------------------------------------------------------ routing */
 
 size_t hocf_moe_route_workspace_bytes(int E) {
-  return E < 1 || E > kRouteMaxE ? 0 : (size_t)(kCountWords + kCountCopies * route_count_stride(E)) * 4;
+  return E < 1 || E > kRouteMaxE ? 0 : (size_t)(1 + kCountCopies) * route_count_stride(E) * 8;
 }
 
 hocf_status hocf_moe_route(int64_t T, int E, int topk, hocf_dtype dt, const void* logits, int64_t ld,
@@ -72,7 +72,7 @@ hocf_status hocf_moe_route(int64_t T, int E, int topk, hocf_dtype dt, const void
   }
   RouteArgs a{};
   a.logits = logits; a.bias = bias; a.experts = experts; a.weights = weights; a.counts = counts;
-  a.ws = static_cast<uint32_t*>(sync->workspace);
+  a.ws = static_cast<uint64_t*>(sync->workspace);
   a.T = T; a.ld = ld; a.E = E; a.topk = topk; a.dt = dt; a.score = score;
   a.n_group = n_group; a.topk_group = topk_group; a.group_top = group_top;
   a.renorm = renorm; a.scale = scale;

@@ -145,13 +145,21 @@ __device__ __forceinline__ double dppd(double v) {
   const uint32_t lo = (uint32_t)dpp<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp<CTRL>((int)(uint32_t)(u >> 32));
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+template <int SWAP>
+__device__ __forceinline__ double swapd(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  uint32_t lo[2], hi[2];
+  across<SWAP>((uint32_t)u, lo[0], lo[1]);
+  across<SWAP>((uint32_t)(u >> 32), hi[0], hi[1]);
+  return fmax(__builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]), __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]));
+}
 __device__ __forceinline__ double wave_maxd(double v) {
   v = fmax(v, dppd<0xB1>(v));
   v = fmax(v, dppd<0x4E>(v));
   v = fmax(v, dppd<0x141>(v));
   v = fmax(v, dppd<0x140>(v));
-  v = fmax(v, __shfl_xor(v, 16, 64));
-  return fmax(v, __shfl_xor(v, 32, 64));
+  v = swapd<16>(v);
+  return swapd<32>(v);
 }
 
 // Whether p holds in any lane of a token (16 or all 64).
@@ -270,32 +278,29 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, do
   if (lane < a.topk) picks[lane] = mine;
 }
 
-// Counts of chosen experts leave a workgroup's LDS histogram through the
-// workspace; the last workgroup to finish copies them out and zeroes the
-// words again.  Additions to one cache line go one after another (some 40 ns
-// each, measured), so there are kCountCopies tables and few workgroups.
-__device__ __forceinline__ void finish_counts(const RouteArgs& a, const uint32_t* s_hist, int* s_last) {
-  const int stride = route_count_stride(a.E);
-  __syncthreads();
-  uint32_t* table = a.ws + kCountWords + (int)(blockIdx.x % kCountCopies) * stride;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-    if (s_hist[e]) __hip_atomic_fetch_add(&table[e], s_hist[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  wait_memory();  // this thread's additions are done
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const uint32_t prev = __hip_atomic_fetch_add(&a.ws[0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const int last = prev == gridDim.x - 1;
-    if (last) __hip_atomic_store(&a.ws[0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *s_last = last;
-  }
-  __syncthreads();
-  if (!uniform(*s_last)) return;
+// Counts of chosen experts leave a workgroup's LDS histogram through 64-bit
+// words of the workspace: the high half counts the workgroups that have added,
+// so that the last one to add an expert's word has its total, and no one waits
+// for an order of separate additions.  Additions to one cache line go one
+// after another (some 40 ns each, measured), so workgroups add to
+// kCountCopies tables, and each table's last ones to a table of sums.  Every
+// word is left zeroed by the last to add.
+__device__ __forceinline__ bool add_counts(uint64_t* at, uint32_t n, uint32_t of, uint32_t* total) {
+  const uint64_t was = __hip_atomic_fetch_add(at, (1ull << 32) + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  *total = (uint32_t)was + n;
+  const bool last = (uint32_t)(was >> 32) == of - 1;
+  if (last) __hip_atomic_store(at, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return last;
+}
+__device__ __forceinline__ void finish_counts(const RouteArgs& a, const uint32_t* s_hist) {
+  const uint32_t stride = route_count_stride(a.E), table = blockIdx.x % kCountCopies;
+  const uint32_t groups = gridDim.x, of = (groups - table + kCountCopies - 1) / kCountCopies;  // that add to this table
+  lds_barrier();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    uint32_t n = 0;
-#pragma unroll
-    for (int c = 0; c < kCountCopies; ++c)
-      n += __hip_atomic_exchange(&a.ws[kCountWords + c * stride + e], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    a.counts[e] = (int32_t)n;
+    uint32_t n;
+    if (add_counts(&a.ws[(table + 1) * stride + e], s_hist[e], of, &n) &&
+        add_counts(&a.ws[e], n, min(groups, (uint32_t)kCountCopies), &n))
+      a.counts[e] = (int32_t)n;
   }
 }
 
@@ -328,14 +333,15 @@ __device__ __forceinline__ void emit(const RouteArgs& a, int64_t t, bool own, in
   }
 }
 
-// A token whose candidates a wave has found but not ranked yet.
+// A token whose candidates a wave has found but not ranked yet (n = 0: it has
+// to be chosen in 64 bits).
 struct Candidates {
   int64_t t;
   int n;
   float top, inv;
   int16_t e[kRouteMaxTopk];
 };
-constexpr int kWaveList = 8;       // of them, a wave (any more: chosen in 64 bits)
+constexpr int kWaveList = 8;       // of them, a wave (any more are marked in the output, to be chosen in 64 bits)
 constexpr int kLater = INT_MIN;    // stands in a token's first place until it is chosen in 64 bits
 
 template <int DT, int LPT, int W, Order ORDER>
@@ -355,7 +361,6 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
   __shared__ int s_pick[kRouteWaves][kRouteMaxTopk];
   __shared__ Candidates s_list[kRouteWaves][kWaveList];
   __shared__ uint32_t s_hist[kRouteMaxE];
-  __shared__ int s_last;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int l = lane & (LPT - 1), row_lane = lane & 15;
   // this lane's run of experts
@@ -569,15 +574,15 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
     const bool own = t0 + lane / LPT < a.T;
     if (__any(near || hard)) {
       // to the list, as far as there is room
-      const uint64_t want = __ballot(l == 0 && own && near && !hard);
+      const uint64_t want = __ballot(l == 0 && own && (near || hard));
       const int at = listed + __builtin_popcountll(want & ((1ull << (lane & -LPT)) - 1));
-      const bool listing = own && near && !hard && at < kWaveList;
+      const bool listing = own && (near || hard) && at < kWaveList;
       if (listing) {
         Candidates& c = s_list[wave][at];
         if (l < kRouteMaxTopk) c.e[l] = (int16_t)e;
         if (l == 0) {
           c.t = t;
-          c.n = n;
+          c.n = hard ? 0 : n;
           c.top = top;
           c.inv = inv;
         }
@@ -593,11 +598,16 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
   __builtin_amdgcn_wave_barrier();
 
   // Candidates: a lane each, ranked by their exact values, ties to the lower index.
+  uint32_t whole = 0;
   for (int i0 = 0; i0 < listed; i0 += TPW) {
-    const bool own = i0 + lane / LPT < listed;
-    const Candidates& c = s_list[wave][min(i0 + lane / LPT, listed - 1)];
-    const char* row = reinterpret_cast<const char*>(a.logits) + c.t * a.ld * es;
+    const int at = i0 + lane / LPT;
+    const Candidates& c = s_list[wave][min(at, listed - 1)];
     const int n = c.n, e = l < n ? c.e[min(l, kRouteMaxTopk - 1)] : -1;
+    const bool own = at < listed && n > 0;
+    const uint64_t none = __ballot(l == 0 && at < listed && n == 0);
+    for (uint64_t u = none; u; u &= u - 1) whole |= 1u << (i0 + __builtin_ctzll(u) / LPT);
+    if (!__any(own)) continue;
+    const char* row = reinterpret_cast<const char*>(a.logits) + c.t * a.ld * es;
     double v = e >= 0 ? (double)clean(ld1<DT>(row, e)) : -INFINITY;
     if (ORDER == kByScore && e >= 0) v = 1.0 / (1.0 + exp(-v)) + (a.bias ? (double)a.bias[e] : 0.0);
     int rank = 0;
@@ -608,24 +618,38 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
     }
     emit<DT, LPT>(a, c.t, own, l < n ? rank : -1, e, c.top, c.inv, s_hist);
   }
-  if (left) {
-    wait_memory();  // the marks are there
-    for (int64_t t0 = begin; t0 < a.T; t0 += step) {
-      const int64_t t = min(t0 + lane / LPT, a.T - 1);
-      const int mark = __hip_atomic_load(&a.experts[t * a.topk], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      for (uint64_t todo = __ballot(l == 0 && t0 + lane / LPT < a.T && mark == kLater); todo; todo &= todo - 1) {
-        const int64_t tr = t0 + __builtin_ctzll(todo) / LPT;
-        float top = 0.0f, inv = 1.0f;
-        choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + tr * a.ld * es, s_wave[wave].v,
-                                        s_pick[wave], &top, &inv);
-        __threadfence_block();
-        __builtin_amdgcn_wave_barrier();
-        emit<DT, LPT>(a, tr, lane < LPT, l, s_pick[wave][min(l, kRouteMaxTopk - 1)], top, inv, s_hist);
-        __builtin_amdgcn_wave_barrier();
+  auto in_64_bits = [&](int64_t t) {
+    float top = 0.0f, inv = 1.0f;
+    choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + t * a.ld * es, s_wave[wave].v, s_pick[wave],
+                                    &top, &inv);
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    emit<DT, LPT>(a, t, lane < LPT, l, s_pick[wave][min(l, kRouteMaxTopk - 1)], top, inv, s_hist);
+    __builtin_amdgcn_wave_barrier();
+  };
+  int64_t t0 = begin;
+  if (left) wait_memory();  // the marks are there
+  for (;;) {
+    int64_t t;
+    if (whole) {
+      t = s_list[wave][__builtin_ctz(whole)].t;
+      whole &= whole - 1;
+    } else {
+      // the first marked token that is left
+      uint64_t todo = 0;
+      for (; left && t0 < a.T; t0 += step) {
+        const int mark = __hip_atomic_load(&a.experts[min(t0 + lane / LPT, a.T - 1) * a.topk], __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+        todo = __ballot(l == 0 && t0 + lane / LPT < a.T && mark == kLater);
+        if (todo) break;
       }
+      if (!todo) break;
+      t = t0 + __builtin_ctzll(todo) / LPT;
     }
+    in_64_bits(t);
+    if (left) wait_memory();  // (its mark is gone)
   }
-  if (a.counts) finish_counts(a, s_hist, &s_last);
+  if (a.counts) finish_counts(a, s_hist);
 }
 
 template <int DT, int LPT, int W>

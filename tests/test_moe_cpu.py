@@ -63,7 +63,7 @@ def test_route_rejects(kw, expect):
 
 
 def test_route_accepts():
-    assert hocf.hocf_moe_route_workspace_bytes(60) == (32 + 8 * 64) * 4 and hocf.hocf_moe_route_workspace_bytes(0) == 0
+    assert hocf.hocf_moe_route_workspace_bytes(60) == 9 * 64 * 8 and hocf.hocf_moe_route_workspace_bytes(0) == 0
     assert route(T=0, counts=None, logits=None, experts=None, weights=None) == OK
     valid(route())
     valid(route(counts=None, s=sync(ws=0, nbytes=0)))      # no counts: no workspace
