@@ -170,59 +170,72 @@ __device__ __forceinline__ bool token_any(bool p) {
   return LPT == 64 || (b >> (threadIdx.x & 48) & 0xffffu) != 0;
 }
 
+// A wave's room for a choice in 64 bits.
+template <int N>
+struct Room64 {
+  double v[N];
+  float bias[N];
+};
+
 // The choice of one token in 64 bits, by a whole wave (lane l: experts l, l +
 // 64, ...; V of them); picks to LDS, -1 where none is left, and a softmax's
 // largest logit and one over its sum.  Few tokens come here, but a wave that
 // has one is the last to finish: it is laid out for a short chain of dependent
-// steps (some 3 us), not for few instructions.
+// steps and for little code, most of whose lines are fetched for this one token.
 template <int DT, int V>
-__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, double* lds, int* picks, float* top_out,
-                                         float* inv_out) {
+__device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, double* lds, float* lds_bias, int* picks,
+                                         float* top_out, float* inv_out) {
   const int lane = threadIdx.x & 63, E = a.E;
   const double kOff = -INFINITY;
-  float x[V], bias[V];
-  double v[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = min(lane + 64 * i, E - 1);
-    x[i] = ld1<DT>(row, e);
-    bias[i] = a.bias ? a.bias[e] : 0.0f;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = lane + 64 * i < E ? clean(x[i]) : -INFINITY;
-  if (a.score == kSoftmax) {
-    double top = -(double)kMaxF, sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) top = fmax(top, (double)x[i]);
-    top = wave_maxd(top);
-    *top_out = (float)top;
+  const bool softmax = a.score == kSoftmax;
+  double top = -(double)kMaxF, sum = 0.0;
+  {
+    float x[V], bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      v[i] = exp((double)x[i] - top);
-      sum += v[i];
+      const int e = min(lane + 64 * i, E - 1);
+      x[i] = ld1<DT>(row, e);
+      bias[i] = a.bias ? a.bias[e] : 0.0f;
     }
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = v[i] / sum;  // (sum = 0: every logit is off)
-    *inv_out = sum > 0.0 ? (float)(1.0 / sum) : 0.0f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+    for (int i = 0; i < V; ++i) {
+      x[i] = lane + 64 * i < E ? clean(x[i]) : -INFINITY;
+      top = fmax(top, (double)x[i]);
+      lds[lane + 64 * i] = x[i];
+      lds_bias[lane + 64 * i] = bias[i];
+    }
   }
-#pragma unroll
+  if (softmax) {
+    top = wave_maxd(top);
+    *top_out = (float)top;
+  }
+  uint32_t on = 0;
+#pragma unroll 1
   for (int i = 0; i < V; ++i) {
-    const double w = v[i] + (double)bias[i];
-    v[i] = x[i] > -INFINITY && w > kOff ? w : kOff;
+    const double x = lds[lane + 64 * i], p = exp(softmax ? x - top : -x);
+    on |= (uint32_t)(x > kOff) << i;
+    lds[lane + 64 * i] = softmax ? p : 1.0 + p;
+    sum += p;
   }
+  if (softmax) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
+    *inv_out = sum > 0.0 ? (float)(1.0 / sum) : 0.0f;
+  }
+  double v[V];
+#pragma unroll 1
+  for (int i = 0; i < V; ++i) {
+    const double p = lds[lane + 64 * i];
+    const double w = (softmax ? p : 1.0) / (softmax ? sum : p) + (double)lds_bias[lane + 64 * i];  // (sum = 0: every logit is off)
+    lds[lane + 64 * i] = (on >> i & 1) && w > kOff ? w : kOff;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = lds[lane + 64 * i];
   if (a.n_group > 1) {
     // 1 << lg lanes on each group, strided through it
     const int size = E / a.n_group;
     int lg = 6;
     while ((64 >> lg) < a.n_group) --lg;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 64 * i < E) lds[lane + 64 * i] = v[i];
     __threadfence_block();
     __builtin_amdgcn_wave_barrier();
     const int g = lane >> lg, step = 1 << lg;
@@ -355,7 +368,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
   constexpr bool kListed = W > 4;         // the lanes' sorted keys are in LDS, but for the first two
   // (one after the other: the keys, and the 64-bit values at the end)
   __shared__ union {
-    double v[LPT == 16 ? 256 : kRouteMaxE];
+    Room64<LPT == 16 ? 256 : kRouteMaxE> exact;
     int keys[kListed ? W + 1 : 1][64];
   } s_wave[kRouteWaves];
   __shared__ int s_pick[kRouteWaves][kRouteMaxTopk];
@@ -618,36 +631,34 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
     }
     emit<DT, LPT>(a, c.t, own, l < n ? rank : -1, e, c.top, c.inv, s_hist);
   }
-  auto in_64_bits = [&](int64_t t) {
-    float top = 0.0f, inv = 1.0f;
-    choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + t * a.ld * es, s_wave[wave].v, s_pick[wave],
-                                    &top, &inv);
-    __threadfence_block();
-    __builtin_amdgcn_wave_barrier();
-    emit<DT, LPT>(a, t, lane < LPT, l, s_pick[wave][min(l, kRouteMaxTopk - 1)], top, inv, s_hist);
-    __builtin_amdgcn_wave_barrier();
-  };
-  int64_t t0 = begin;
-  if (left) wait_memory();  // the marks are there
-  for (;;) {
-    int64_t t;
-    if (whole) {
-      t = s_list[wave][__builtin_ctz(whole)].t;
-      whole &= whole - 1;
-    } else {
-      // the first marked token that is left
-      uint64_t todo = 0;
-      for (; left && t0 < a.T; t0 += step) {
-        const int mark = __hip_atomic_load(&a.experts[min(t0 + lane / LPT, a.T - 1) * a.topk], __ATOMIC_RELAXED,
-                                           __HIP_MEMORY_SCOPE_AGENT);
-        todo = __ballot(l == 0 && t0 + lane / LPT < a.T && mark == kLater);
-        if (todo) break;
+  if (whole || left) {
+    if (left) wait_memory();  // the marks are there
+    int64_t t0 = begin;
+    uint64_t todo = 0;  // marked tokens of the step before t0
+    for (;;) {
+      int64_t t;
+      if (whole) {
+        t = s_list[wave][__builtin_ctz(whole)].t;
+        whole &= whole - 1;
+      } else {
+        for (; left && !todo && t0 < a.T; t0 += step) {
+          const int mark = __hip_atomic_load(&a.experts[min(t0 + lane / LPT, a.T - 1) * a.topk], __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+          todo = __ballot(l == 0 && t0 + lane / LPT < a.T && mark == kLater);
+        }
+        if (!todo) break;
+        t = t0 - step + __builtin_ctzll(todo) / LPT;
+        todo &= todo - 1;
       }
-      if (!todo) break;
-      t = t0 + __builtin_ctzll(todo) / LPT;
+      float top = 0.0f, inv = 1.0f;
+      auto& room = s_wave[wave].exact;
+      choose64<DT, LPT == 16 ? 4 : 8>(a, reinterpret_cast<const char*>(a.logits) + t * a.ld * es, room.v, room.bias,
+                                      s_pick[wave], &top, &inv);
+      __threadfence_block();
+      __builtin_amdgcn_wave_barrier();
+      emit<DT, LPT>(a, t, lane < LPT, l, s_pick[wave][min(l, kRouteMaxTopk - 1)], top, inv, s_hist);
+      __builtin_amdgcn_wave_barrier();
     }
-    in_64_bits(t);
-    if (left) wait_memory();  // (its mark is gone)
   }
   if (a.counts) finish_counts(a, s_hist);
 }
