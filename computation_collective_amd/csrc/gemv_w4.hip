@@ -16,6 +16,10 @@
 // first -- x, then scales, then weights, each a straight run of loads, since
 // loads come back in order and a load under a condition is waited for at once
 // -- so that its products start with the first weights.
+//
+// Bound by the weights' bytes, and by the 2-3 us until the first of them
+// arrive: one token's 8 experts 4096 -> 1792 (30 MB) 8.8 us, 16 tokens x 2 of 32
+// experts 1792 -> 4096 (86 MB) 20-22 us.
 #include <algorithm>
 
 #include "moe.hpp"

