@@ -153,6 +153,54 @@ def test_route_near_ties():
     check_route(x, 8, bias=bias, score=SIGMOID, n_group=16, topk_group=3, group_top=2)
 
 
+@pytest.mark.parametrize("E,n_group,topk_group,topk", [
+    (16, 1, 1, 16), (30, 1, 1, 8), (64, 8, 3, 12), (100, 1, 1, 16), (128, 4, 2, 8), (256, 1, 1, 16), (256, 8, 4, 8),
+    (250, 2, 1, 7), (300, 1, 1, 16), (512, 1, 1, 16), (512, 32, 6, 16), (60, 60, 9, 9)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_crowded(E, n_group, topk_group, topk, dtype):
+    """Values that crowd around a few: most tokens are in doubt, more of them than a wave's list holds; the
+    largest all in one lane's run, in rising and falling order; runs of equal logits; tiny logits."""
+    say(f"route crowded E={E} of {n_group} topk={topk} {dtype}")
+    T, g = 160, gen(E + topk)
+    few = torch.tensor([0.5, 0.5001, -1.0, 2.0, 1e-3])
+    x = few[torch.randint(0, 5, (T, E), generator=g)]
+    x[:80] = torch.nextafter(x[:80], x[:80] + torch.randint(-2, 3, (80, E), generator=g))
+    e = torch.arange(E).float()
+    x[0], x[1], x[2], x[3] = e / 7, -e / 7, 3.0, 0.0
+    x[4] = torch.where(e < E // 2, e * 2.0 ** -23 + 1.0, 0.0)
+    x[5] = (e % 3) * 2.0 ** -20
+    x[6:9] = torch.randn(3, E, generator=g) * 2.0 ** -14
+    x[9] = -torch.inf
+    x[10, E // 3:] = -torch.inf
+    x[11, ::2] = torch.nan
+    x = x.to(dtype).cuda()
+    size = E // n_group
+    for score, top2, bias in ((SOFTMAX, False, None), (SIGMOID, True, None),
+                              (SIGMOID, True, torch.randint(-2, 3, (E,), generator=g) * 2.0 ** -10)):
+        check_route(x, topk, bias=bias, score=score, n_group=n_group, topk_group=topk_group,
+                    group_top=2 if top2 and size > 1 and n_group > 1 else 1, renorm=True)
+
+
+def test_route_odd_biases():
+    """Biases beyond the keys' range, and experts that a NaN or -inf bias rules out."""
+    say("route odd biases")
+    x = logits(40, 24, torch.float32, 3, masked=0.2)
+    for kind in range(4):
+        b = 0.1 * torch.randn(24, generator=gen(kind))
+        if kind == 0:
+            b[::3] += 100.0
+        elif kind == 1:
+            b -= 3.9
+        elif kind == 2:
+            b[::2] = -1e30
+        else:
+            b[5], b[6] = float("nan"), float("-inf")
+        e = ref.route(x.double().cpu().numpy(), 6, torch.nan_to_num(b, nan=-np.inf, neginf=-np.inf, posinf=np.inf).numpy(),
+                      score=SIGMOID, n_group=4, topk_group=3, group_top=2)[0]
+        h = run(bf.MoeRoute(40, 24, 6, x, bias=b.cuda(), score=SIGMOID, n_group=4, topk_group=3, group_top=2))
+        assert np.array_equal(h.experts.cpu().numpy(), e), kind
+
+
 def test_route_far_logits_by_value():
     """Softmax scores that underflow or saturate even in 64 bits tie: the lower index."""
     x = torch.tensor([[0.0, -800.0, -790.0, -900.0, -5.0], [60.0, 50.0, 55.0, 45.0, 70.0]]).cuda()
