@@ -181,6 +181,23 @@ def test_route_crowded(E, n_group, topk_group, topk, dtype):
                     group_top=2 if top2 and size > 1 and n_group > 1 else 1, renorm=True)
 
 
+@pytest.mark.parametrize("grid", [1, 3, 9])
+def test_route_few_workgroups(grid, monkeypatch):
+    """Many tokens a wave, in the last step a part of one; counts from a grid of any size."""
+    monkeypatch.setenv("HOCF_MAX_WORKGROUPS", str(grid))
+    say(f"route grid={grid}")
+    bias = 0.001 * torch.randint(-9, 10, (256,), generator=gen(1)).float()
+    check_route(logits(1001, 256, torch.float32, 2), 8, bias=bias, score=SIGMOID, n_group=8, topk_group=4, group_top=2)
+    check_route(logits(1003, 40, torch.bfloat16, 3, masked=0.3), 4)
+    x = logits(515, 320, torch.float32, 4)
+    check_route(x, 3, score=SIGMOID)
+    dw = torch.randn(515, 3, generator=gen(5))
+    e = ref.route(x.double().cpu().numpy(), 3)[0]
+    h = run(bf.MoeRouteBwd(515, 320, 3, x, torch.from_numpy(e).cuda(), dw.cuda()))
+    d, size = ref.route_bwd(x.double().cpu().numpy(), e, dw.numpy(), SOFTMAX, False, 1.0)
+    near(h.dlogits, d, size, torch.float32, 80)
+
+
 def test_route_odd_biases():
     """Biases beyond the keys' range, and experts that a NaN or -inf bias rules out."""
     say("route odd biases")
