@@ -21,9 +21,9 @@
 //         tiny are equal logits.
 //   Order = kByScore: v = (s + bias) * 2^29.  A sigmoid in 32 bits is off by at
 //         most 3.1 * 2^-24 (exponent, sum and reciprocal), a sum below 4 by 2
-//         more, the conversion by one unit; a softmax by 35 * 2^-24 (the row's
-//         sum of up to 512 terms).  Neighbours nearer than that allows are in
-//         doubt.
+//         more, the conversion by one unit; a softmax by 35 * 2^-24 of the row's
+//         largest score (a sum of up to 512 terms).  Neighbours nearer than that
+//         allows are in doubt.
 //
 // A lane sorts its keys once; a choice is then the largest of the lanes' first
 // keys, and its lane moves on by one.  The chosen keys go into a shift register
@@ -60,7 +60,8 @@ enum Order : int { kByLogit, kByScore };
 constexpr float kLogitUnit = 0x1p26f, kScoreUnit = 0x1p29f;
 // Twice the error of a score, in units of 2^-29 (and of a group's half sum of
 // two scores, in units of 2^-28); the keys' low bits come on top.
-constexpr int kDoubtSigmoid = 2 * 7 << 5, kDoubtSoftmax = 2 * 38 << 5;
+constexpr int kDoubtSigmoid = 2 * 7 << 5, kDoubtSum = 2 * 3 << 5;
+constexpr float kDoubtSoftmax = 2 * 36 << 5;  // times the largest score, and kDoubtSum
 constexpr int kSaturated = 20 << 26;     // sigmoid(20) is 2e-9 from 1
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kVanished = -709.78f;    // a sigmoid below is 0 in 64 bits too
@@ -168,6 +169,12 @@ __device__ __forceinline__ double wave_maxd(double v) {
   return swapd<32>(v);
 }
 
+__device__ __forceinline__ double read_lane(double v, int lane) {  // (the same lane for the whole wave)
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // Whether p holds in any lane of a token (16 or all 64).
 template <int LPT>
 __device__ __forceinline__ bool token_any(bool p) {
@@ -253,16 +260,20 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const void* row, do
         m2 = fmax(m2, fmin(m1, w));
         m1 = fmax(m1, w);
       }
-    for (int d = 1; d < step; d *= 2) {
-      const double o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
+    auto merge = [&](double o1, double o2) {
       m2 = fmax(fmin(m1, o1), fmax(m2, o2));
       m1 = fmax(m1, o1);
-    }
+    };
+    if (step > 1) merge(dppd<0xB1>(m1), dppd<0xB1>(m2));
+    if (step > 2) merge(dppd<0x4E>(m1), dppd<0x4E>(m2));
+    if (step > 4) merge(dppd<0x141>(m1), dppd<0x141>(m2));
+    if (step > 8) merge(dppd<0x140>(m1), dppd<0x140>(m2));
+    if (step > 16) merge(__shfl_xor(m1, 16, 64), __shfl_xor(m2, 16, 64));  // (two groups at least)
     const double of = a.group_top == 2 && m2 > kOff ? m1 + m2 : m1;
     int ahead = 0;
 #pragma unroll 4
     for (int o = 0; o < a.n_group; ++o) {
-      const double other = __shfl(of, o << lg, 64);
+      const double other = read_lane(of, o << lg);
       ahead += other > of || (other == of && o < g);
     }
     const uint64_t kept = __ballot(g < a.n_group && ahead < a.topk_group);
@@ -438,6 +449,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
       sum = row_sum<LPT>(sum);
       inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
+    const uint32_t unsure = softmax ? (uint32_t)(inv * kDoubtSoftmax) + kDoubtSum : kDoubtSigmoid;
     float v[W];
     if constexpr (ORDER == kByScore) {
       if (softmax) {
@@ -500,7 +512,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
       const int out = row_max<LPT>(of);
       if (out > low_of) {
         if constexpr (ORDER == kByScore)
-          hard = (uint32_t)in - (uint32_t)out < (softmax ? kDoubtSoftmax : kDoubtSigmoid) + Q + 2 * LPT;
+          hard = (uint32_t)in - (uint32_t)out < unsure + Q + 2 * LPT;
         else hard = ((in ^ out) & -LPT) == 0 && (DT != kBF16 || abs(in) < kTiny);
       }
       hard |= token_any<LPT>(group && unclear);
@@ -550,7 +562,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
     auto close = [&](int before, int m) {
       if (m < kLow) return false;
       if constexpr (ORDER == kByScore)
-        return (uint32_t)(before & -Q) - (uint32_t)(m & -Q) < (softmax ? kDoubtSoftmax : kDoubtSigmoid) + (uint32_t)Q;
+        return (uint32_t)(before & -Q) - (uint32_t)(m & -Q) < unsure + Q;
       else return ((before ^ m) & -Q) == 0 && (DT != kBF16 || abs(m) < kTiny);
     };
     bool doubt = row_lane < n && close(q, shift_in(next, q));
@@ -582,7 +594,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
         next = row_max<LPT>(k[0]);
         open &= close(m, next);
       }
-      if (ORDER == kByScore && softmax) hard |= near;  // (exact values need the row's exact sum)
+      if (ORDER == kByScore && softmax && a.bias) hard |= near;  // (exact values need the row's exact sum)
     }
     // the expert of a key: its lane and its slot
     const int of_lane = LPT - 1 - (int)((uint32_t)q / W & (LPT - 1));
@@ -628,7 +640,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
     if (!__any(own)) continue;
     const char* row = reinterpret_cast<const char*>(a.logits) + c.t * a.ld * es;
     double v = e >= 0 ? (double)clean(ld1<DT>(row, e)) : -INFINITY;
-    if (ORDER == kByScore && e >= 0) v = 1.0 / (1.0 + exp(-v)) + (a.bias ? (double)a.bias[e] : 0.0);
+    if (ORDER == kByScore && !softmax && e >= 0) v = 1.0 / (1.0 + exp(-v)) + (a.bias ? (double)a.bias[e] : 0.0);
     int rank = 0;
     for (int i = 0; i < kRouteMaxTopk; ++i) {
       const double o = __shfl(v, i, LPT);

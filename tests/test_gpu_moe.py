@@ -176,9 +176,25 @@ def test_route_crowded(E, n_group, topk_group, topk, dtype):
     x = x.to(dtype).cuda()
     size = E // n_group
     for score, top2, bias in ((SOFTMAX, False, None), (SIGMOID, True, None),
-                              (SIGMOID, True, torch.randint(-2, 3, (E,), generator=g) * 2.0 ** -10)):
+                              (SIGMOID, True, torch.randint(-2, 3, (E,), generator=g) * 2.0 ** -10), (SOFTMAX, True, None)):
         check_route(x, topk, bias=bias, score=score, n_group=n_group, topk_group=topk_group,
                     group_top=2 if top2 and size > 1 and n_group > 1 else 1, renorm=True)
+
+
+@pytest.mark.parametrize("E,n_group,topk_group,topk", [(64, 8, 3, 12), (256, 8, 4, 8), (512, 32, 6, 16), (100, 1, 1, 7)])
+@pytest.mark.parametrize("spread", [0.1, 1.0, 4.0])
+def test_route_softmax_by_score(E, n_group, topk_group, topk, spread):
+    """Softmax scores with biases (all different: sums that are equal but for their rounding have no order), flat rows
+    and peaked ones, half of the logits within a few steps of another one."""
+    say(f"route softmax by score E={E} of {n_group} spread={spread}")
+    T, g = 150, gen(E + topk)
+    x = spread * torch.randn(T, E, generator=g)
+    x[:, E // 2:] = torch.nextafter(x[:, :E - E // 2], x[:, :E - E // 2] + torch.randint(-1, 2, (T, E - E // 2), generator=g))
+    bias = 1e-3 * torch.randn(E, generator=g)
+    near_bias = 0.01 + 2.0 ** -30 * torch.randperm(E, generator=g).float()
+    for b in (bias, near_bias, None):
+        check_route(x.cuda(), topk, bias=b, score=SOFTMAX, n_group=n_group, topk_group=topk_group,
+                    group_top=2 if n_group > 1 else 1, renorm=True)
 
 
 @pytest.mark.parametrize("grid", [1, 3, 9])
