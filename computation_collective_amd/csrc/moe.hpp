@@ -72,6 +72,18 @@ struct CombineArgs {
   SyncArgs sync;
 };
 
+// How the weighted sum's backward pass gives a call's tokens to waves.
+enum BwdForm { kWide, kRows, kShifted };
+
+// Four waves on a token where tokens alone would not fill the device, and where
+// the rows hold nothing (the shifted form reads a piece of every row it is given).
+// Else a wave each, on pieces that start where the rows' cache lines do.
+constexpr int kLine = 128;  // bytes of a cache line
+constexpr BwdForm combine_bwd_form(int64_t T, int64_t R, int N, int dt, uintptr_t drows) {
+  if (T < 2048 || R == 0 || N == 0) return kWide;
+  return (int64_t)N * (dt == kBF16 ? 2 : 4) % kLine == 0 && drows % kLine == 0 ? kRows : kShifted;
+}
+
 constexpr int kW4MaxRows = 1024;
 
 struct GemvW4Args {

@@ -167,9 +167,6 @@ int launch_moe_combine(const CombineArgs& a, hipStream_t s) {
 // 4096 bytes take 134); dout is then read again at every row's pieces.  A dot product's partial sums fold in a
 // fixed order (a lane's pieces, the lanes by halves, the waves in order).
 constexpr int kZeroRows = 16;
-constexpr int kLine = 128;  // bytes of a cache line
-
-enum BwdForm { kWide, kRows, kShifted };
 
 template <int DT, int ODT, int K, BwdForm FORM>
 __global__ __launch_bounds__(kCombineThreads) void combine_bwd_kernel(CombineArgs a, int64_t zero_blocks,
@@ -289,12 +286,13 @@ static int launch_form(const CombineArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Four waves on a token where tokens alone would not fill the device.
 template <int DT, int ODT, int K>
 static int launch_bwd(const CombineArgs& a, hipStream_t s) {
-  if (a.T < 2048 || a.R == 0) return launch_form<DT, ODT, K, kWide>(a, s);
-  const bool lines = (int64_t)a.N * (DT == kBF16 ? 2 : 4) % kLine == 0 && reinterpret_cast<uintptr_t>(a.drows) % kLine == 0;
-  return lines ? launch_form<DT, ODT, K, kRows>(a, s) : launch_form<DT, ODT, K, kShifted>(a, s);
+  switch (combine_bwd_form(a.T, a.R, a.N, DT, reinterpret_cast<uintptr_t>(a.drows))) {
+    case kWide: return launch_form<DT, ODT, K, kWide>(a, s);
+    case kRows: return launch_form<DT, ODT, K, kRows>(a, s);
+    default: return launch_form<DT, ODT, K, kShifted>(a, s);
+  }
 }
 
 template <int DT, int ODT>

@@ -1,0 +1,48 @@
+"""The mixture-of-experts operators where calls are unusual but allowed: rows
+of no elements, scores that are equal in 64 bits, infinities, kernel forms
+that only large or odd shapes take, errors that have to end with their call."""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_ref as ref
+from computation_collective_amd import buffers as bf
+from computation_collective_amd import hocf
+from test_gpu_moe import dev, gen, host, near, run, say
+
+pytestmark = pytest.mark.gpu
+SOFTMAX, SIGMOID = hocf.HOCF_SCORE_SOFTMAX, hocf.HOCF_SCORE_SIGMOID
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+
+
+def entry(fn, *args):
+    """A C entry with a sync block of its own on the current stream."""
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hocf.check(fn(*args, hocf.sync(1, None, 0, status=status), torch.cuda.current_stream()))
+    torch.cuda.synchronize()
+    assert int(status) == 0
+
+
+# ------------------------------------------------------------------------------ weighted sum
+
+@pytest.mark.parametrize("T", [3, 2048, 2050])
+@pytest.mark.parametrize("dt", [hocf.HOCF_F32, hocf.HOCF_BF16])
+def test_combine_bwd_of_rows_without_elements(T, dt):
+    """N = 0, with rows that need not be there: the weights' gradients are empty sums, and nothing else is written."""
+    topk, R = 2, 2 * T
+    say(f"combine_bwd N=0 T={T} dt={dt}")
+    index = torch.arange(R, dtype=torch.int32).view(T, topk).cuda()
+    w, dw = torch.ones((T, topk)).cuda(), torch.full((T, topk), -7.0).cuda()
+    around = torch.full((256,), 3.0).cuda()
+    for rows, dout, drows in ((None, None, None), (None, None, around.data_ptr() + 16),
+                              (w, w, around.data_ptr() + 128)):
+        dw.fill_(-7.0)
+        entry(hocf.hocf_moe_combine_bwd, T, topk, 0, R, dt, dt, rows, w, dout, index, index.view(-1), drows, dw)
+        assert not dw.any() and (around == 3.0).all()
