@@ -447,12 +447,16 @@ class _Moe(_Common):
 
 
 def _rows_ld(logits, T, E):
-    """Row stride of the logits: [T][E], the experts of a row adjacent."""
+    """Row stride of the logits: [T][E], the experts of a row adjacent, the rows E or more
+    apart (the kernels read E logits from every row's start: rows that share memory, as an
+    expanded tensor's do, would be read beyond their end)."""
     if tuple(logits.shape) != (T, E):
         raise ValueError(f"logits have shape {tuple(logits.shape)}, not {(T, E)}")
     if E > 1 and logits.stride(1) != 1:
         raise ValueError("the logits of a row are not adjacent")
-    return max(logits.stride(0), E) if T > 1 else E
+    if T > 1 and logits.stride(0) < E:
+        raise ValueError(f"the logits' rows overlap: they are {logits.stride(0)} apart, of {E} experts")
+    return logits.stride(0) if T > 1 else E
 
 
 class MoeRoute(_Moe):

@@ -6,6 +6,9 @@ import shutil
 import subprocess
 
 import pytest
+import torch
+
+from computation_collective_amd import buffers as bf
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "computation_collective_amd", "csrc")
@@ -46,3 +49,30 @@ def test_combine_bwd_form(tmp_path):
                         "-I", CSRC, "-I", os.path.join(ROOT, "include"), str(src)], capture_output=True, text=True,
                        timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_logits_rows_may_not_overlap():
+    """The row stride is the tensor's own: rows less than E apart (a broadcast row, overlapping views) are refused."""
+    E = 8
+    one = torch.zeros((1, E))
+    store = torch.zeros(64)
+    for x in (one.expand(4, E), store.as_strided((4, E), (1, 1)), store.as_strided((2, E), (E - 1, 1)),
+              store[:1, None].expand(3, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            bf._rows_ld(x, *x.shape)
+    assert bf._rows_ld(torch.zeros((4, E)), 4, E) == E
+    assert bf._rows_ld(torch.zeros((4, 11))[:, :E], 4, E) == 11
+    assert bf._rows_ld(torch.zeros((9, E))[::3], 3, E) == 3 * E
+    assert bf._rows_ld(one.expand(1, E), 1, E) == E and bf._rows_ld(torch.zeros((0, E)), 0, E) == E
+    assert bf._rows_ld(torch.zeros((5, 1)), 5, 1) == 1
+    with pytest.raises(ValueError, match="not adjacent"):
+        bf._rows_ld(torch.zeros((E, 4)).t(), 4, E)
+
+
+def test_route_refuses_overlapping_logits():
+    """Both router handles ask before anything is bound."""
+    x = torch.zeros((1, 8)).expand(4, 8)
+    with pytest.raises(ValueError, match="overlap"):
+        bf.MoeRoute(4, 8, 2, x)
+    with pytest.raises(ValueError, match="overlap"):
+        bf.MoeRouteBwd(4, 8, 2, x, torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2)))
