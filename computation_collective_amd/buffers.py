@@ -409,6 +409,9 @@ def torch_dt(t: torch.Tensor) -> int:
 
 
 def _on(device, **tensors):
+    """Raises unless `device` is a GPU and every tensor given is on it."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}: the operators take a GPU's memory")
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, not on {device}")
@@ -509,6 +512,7 @@ class MoeSlots(_Moe):
     def __init__(self, T, topk, bins, per_bin, cap, experts):
         _dense(torch.int32, (T, topk), experts=experts)
         dev = experts.device
+        _on(dev)
         self.experts = experts
         self.index = torch.empty((T, topk), dtype=torch.int32, device=dev)
         self.pair = torch.empty(bins * cap, dtype=torch.int32, device=dev)

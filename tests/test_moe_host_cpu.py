@@ -76,3 +76,24 @@ def test_route_refuses_overlapping_logits():
         bf.MoeRoute(4, 8, 2, x)
     with pytest.raises(ValueError, match="overlap"):
         bf.MoeRouteBwd(4, 8, 2, x, torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2)))
+
+
+def test_handles_refuse_host_memory():
+    """Tensors in host memory are refused by every handle, before a kernel could be given their addresses."""
+    T, E, topk, N, K, group = 4, 8, 2, 16, 64, 32
+    i, b = torch.int32, torch.bfloat16
+    logits, w, x = torch.zeros((T, E)), torch.zeros((T, topk)), torch.zeros((T, K), dtype=b)
+    e, rows, index = torch.zeros((T, topk), dtype=i), torch.zeros((T * topk, N)), torch.zeros((T, topk), dtype=i)
+    codes, scales = torch.zeros((1, K, N), dtype=torch.uint8), torch.zeros((1, K // group, N), dtype=b)
+    words, small = bf.w4_layout(1, N, K, group)
+    for make in (lambda: bf.MoeRoute(T, E, topk, logits, counts=True),
+                 lambda: bf.MoeRouteBwd(T, E, topk, logits, e, w),
+                 lambda: bf.MoeSlots(T, topk, 4, 2, 8, e),
+                 lambda: bf.MoeCombine(T, topk, N, rows, w),
+                 lambda: bf.MoeCombineBwd(T, topk, N, rows, w, torch.zeros((T, N)), index=index,
+                                          pair=torch.zeros(T * topk, dtype=i)),
+                 lambda: bf.w4_pack(codes, scales, None, group, stream=0),
+                 lambda: bf.GemvW4(T, 1, 1, 0, N, K, group, x, None, torch.zeros(words, dtype=i),
+                                   torch.zeros(small, dtype=b))):
+        with pytest.raises(ValueError, match="on cpu"):
+            make()
