@@ -433,7 +433,9 @@ def _dense(dtype, shape, **tensors):
 class _Moe(_Common):
     """What the mixture-of-experts operators share: inputs are torch tensors, used
     where they are (no copy); a call goes to the current stream of their device
-    unless it is given one."""
+    unless it is given one.  A handle makes its outputs and workspace on the current
+    stream and reads and writes the same memory at every call: calls on another
+    stream are ordered behind that, and the handle is kept until they have ended."""
 
     def _bind(self, entry, args, device, ws_bytes=0):
         self._alloc_sync(ws_bytes, device)
@@ -581,7 +583,9 @@ def w4_layout(E, N, K, group):
 
 def w4_pack(codes, scales, zeros=None, group=128, stream=None):
     """hocf_w4_pack: codes [E][K][N] uint8, scales (and zeros) [E][ceil(K/group)][N] bf16 ->
-    (wq, scales, zeros or None) as hocf_gemv_w4 reads them."""
+    (wq, scales, zeros or None) as hocf_gemv_w4 reads them.  On another stream than the current
+    one, the packing is ordered behind the current one's work, and the memory of its tensors
+    is not used again before it has ended, whenever they are dropped."""
     E, K, N = codes.shape
     _dense(torch.uint8, (E, K, N), codes=codes)
     _dense(torch.bfloat16, (E, cdiv(K, group), N), scales=scales, zeros=zeros)
@@ -590,8 +594,17 @@ def w4_pack(codes, scales, zeros=None, group=128, stream=None):
     wq = torch.empty(words, dtype=torch.int32, device=codes.device)
     s = torch.empty(small, dtype=torch.bfloat16, device=codes.device)
     z = None if zeros is None else torch.empty(small, dtype=torch.bfloat16, device=codes.device)
-    stream = torch.cuda.current_stream(codes.device) if stream is None else stream
-    hocf.check(hocf.hocf_w4_pack(E, N, K, group, codes, scales, zeros, wq, s, z, stream))
+    now = torch.cuda.current_stream(codes.device)
+    on = now if stream is None else stream
+    if isinstance(on, int):
+        on = torch.cuda.ExternalStream(on, device=codes.device)
+    if on.cuda_stream != now.cuda_stream:
+        on.wait_stream(now)
+    hocf.check(hocf.hocf_w4_pack(E, N, K, group, codes, scales, zeros, wq, s, z, on))
+    if on.cuda_stream != now.cuda_stream:
+        for t in (codes, scales, zeros, wq, s, z):
+            if t is not None:
+                t.record_stream(on)
     return wq, s, z
 
 

@@ -46,3 +46,27 @@ def test_combine_bwd_of_rows_without_elements(T, dt):
         dw.fill_(-7.0)
         entry(hocf.hocf_moe_combine_bwd, T, topk, 0, R, dt, dt, rows, w, dout, index, index.view(-1), drows, dw)
         assert not dw.any() and (around == 3.0).all()
+
+
+# ------------------------------------------------------------------------------ 4-bit weights
+
+def test_w4_pack_on_another_stream_of_temporaries():
+    """Codes and scales made on the current stream and dropped at once; the packing's stream is busy meanwhile and
+    the current one fills the next tensors of the same sizes."""
+    E, N, K, group = 4, 512, 1024, 64
+    say("w4_pack on another stream")
+    g = gen(3)
+    codes = torch.randint(0, 16, (E, K, N), generator=g, dtype=torch.uint8).cuda()
+    scales, zeros = (torch.rand(2, E, K // group, N, generator=g) + 0.5).bfloat16().cuda()
+    want = bf.w4_pack(codes, scales, zeros, group)
+    torch.cuda.synchronize()
+    side, busy = torch.cuda.Stream(), torch.randn(2048, 2048, device="cuda")
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, None):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                busy = busy @ busy * 1e-3
+        got = bf.w4_pack(codes.clone(), scales.clone(), zeros.clone(), group, stream=stream)
+        other = [torch.full_like(t, 9) for t in (codes, scales, zeros)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(other) == 3
