@@ -15,10 +15,12 @@
 //   key = v in fixed point, its low bits (Q units) replaced by the lane and the
 //         slot within the lane (lower index, larger key), so that a token's keys
 //         differ and the largest names its expert.
-//   Order = kByLogit: without a bias, v rises with x, and v = x * 2^26.
-//         Different keys (low bits aside) mean the same order of x, so only
-//         equal keys are in doubt; equal keys of bf16 logits that are not
-//         tiny are equal logits.
+//   Order = kByLogit: without a bias, v rises with x, and v = x * 2^26 + 8.
+//         Different keys (low bits aside) mean the same order of the scores:
+//         the 8 puts the keys' borders where logits are 2^-47 apart or more,
+//         and a logit's distance to the row's largest, below 64, is held to
+//         2^-47.  So only equal keys are in doubt; equal keys of bf16 logits
+//         that are not tiny are equal logits.
 //   Order = kByScore: v = (s + bias) * 2^29.  A sigmoid in 32 bits is off by at
 //         most 3.1 * 2^-24 (exponent, sum and reciprocal), a sum below 4 by 2
 //         more, the conversion by one unit; a softmax by 35 * 2^-24 of the row's
@@ -32,7 +34,8 @@
 //
 // Neighbours in doubt are put in order by their exact values: a few more places
 // are chosen until the next one is clearly below, the lanes evaluate the
-// candidates in 64 bits and rank them.  What that cannot settle (a group's
+// candidates' scores in 64 bits (a softmax's up to its sum) and rank them, equal
+// ones by the lower index.  What that cannot settle (a group's
 // place in doubt, a key outside the fixed-point range, a sigmoid beyond 20
 // where 64 bits begin to saturate, a softmax with a bias) is chosen again in
 // 64 bits by the whole wave: about 1e-4 of the tokens with biased sigmoids in
@@ -57,7 +60,7 @@ constexpr int kRouteThreads = 512;
 constexpr int kRouteWaves = kRouteThreads / 64;
 
 enum Order : int { kByLogit, kByScore };
-constexpr float kLogitUnit = 0x1p26f, kScoreUnit = 0x1p29f;
+constexpr float kLogitUnit = 0x1p26f, kLogitShift = 8.0f, kScoreUnit = 0x1p29f;
 // Twice the error of a score, in units of 2^-29 (and of a group's half sum of
 // two scores, in units of 2^-28); the keys' low bits come on top.
 constexpr int kDoubtSigmoid = 2 * 7 << 5, kDoubtSum = 2 * 3 << 5;
@@ -467,7 +470,7 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = x[i] * kLogitUnit;
+      for (int i = 0; i < W; ++i) v[i] = fmaf(x[i], kLogitUnit, kLogitShift);
     }
     // the next tokens' logits are on their way during the choice
     if (t0 + step < a.T) load_row<DT, W>(row_at(t0 + step) + mine.from * es, x);
@@ -639,8 +642,13 @@ __global__ __launch_bounds__(kRouteThreads, LPT == 64 ? 3 : W > 4 ? 4 : 6) void 
     for (uint64_t u = none; u; u &= u - 1) whole |= 1u << (i0 + __builtin_ctzll(u) / LPT);
     if (!__any(own)) continue;
     const char* row = reinterpret_cast<const char*>(a.logits) + c.t * a.ld * es;
-    double v = e >= 0 ? (double)clean(ld1<DT>(row, e)) : -INFINITY;
-    if (ORDER == kByScore && !softmax && e >= 0) v = 1.0 / (1.0 + exp(-v)) + (a.bias ? (double)a.bias[e] : 0.0);
+    const float x = e >= 0 ? clean(ld1<DT>(row, e)) : -INFINITY;
+    // (the largest logit of a row is among the candidates where they are chosen by their logits)
+    const float top = !softmax ? 0.0f : ORDER == kByLogit ? row_maxf<LPT>(x) : c.top;
+    double v = exp(softmax ? (double)x - (double)top : -(double)x);
+    if (!softmax) v = 1.0 / (1.0 + v);
+    if (ORDER == kByScore && !softmax && a.bias && e >= 0) v += (double)a.bias[e];
+    if (e < 0) v = -INFINITY;
     int rank = 0;
     for (int i = 0; i < kRouteMaxTopk; ++i) {
       const double o = __shfl(v, i, LPT);

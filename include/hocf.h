@@ -558,9 +558,11 @@ hocf_status hocf_dma_put(int n, const void* const* src, void* const* dst, const 
  *   experts  [T][topk] int32      weights [T][topk] fp32
  *   counts   NULL or [E] int32: tokens that chose each expert
  *
- * The choice is the one that arithmetic in 64 bits makes (values that only
- * the last bits of a 64-bit exponential tell apart have no set order); softmax
- * scores without a bias rank by their logits.
+ * The choice is the one that arithmetic in 64 bits makes: scores that are
+ * equal in 64 bits rank by the lower index, also those of different logits
+ * (sigmoids of 1e-20 and 2e-20, softmax scores that underflow).  Values that
+ * only the last bits of a 64-bit exponential or quotient tell apart have no
+ * set order.
  * Supported: dt F32 or BF16; 1 <= E <= 512; 1 <= topk <= min(16, E); n_group
  * <= 64 dividing E; group_top 1 or 2.  0 <= T < 2^31.
  * ---------------------------------------------------------------------- */
