@@ -7,7 +7,9 @@
 // operand.  A rotation and one mask turn eight codes into the bf16 numbers
 // 16 + code; with sx = sum of x over a group (a product with ones),
 //   sum x (code - zero) = sum x (16 + code)  -  (16 + zero) sx
-// in fp32, then times the group's scale.
+// in fp32, then times the group's scale.  That form turns an infinity of x into
+// inf - inf, and leaves the range of fp32 from x = 1e37 on: a result that is not
+// finite is taken again by the definition, in 64 bits.
 //
 // A workgroup's four waves take C blocks of 16 columns of an expert together: a
 // wave takes every fourth block of rows, and the four fold through LDS in a
@@ -60,6 +62,26 @@ __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
   return e < (uint32_t)a.E ? (int)e : -1;
 }
 
+// One result by the definition (column c of column block `block`, counted over all
+// experts).  Slow, a few microseconds for every 64 rows of W, and hardly ever needed.
+template <int GROUP, bool ZEROS>
+__device__ __forceinline__ float by_definition(const GemvW4Args& a, int64_t block, int c, int xrow) {
+  const uint16_t* x = a.x + (int64_t)xrow * a.K;
+  double sum = 0.0;
+#pragma unroll 1
+  for (int k = 0; k < a.K; k += 8) {
+    const uint32_t w = a.wq[((block * a.kb + k / 128) * 64 + k % 32 / 8 * 16 + c) * 4 + k % 128 / 32];
+    const int64_t g = (block * a.groups + k / GROUP) * 16 + c;
+    const double s = bf16_to_f32(a.scales[g]), z = ZEROS ? bf16_to_f32(a.zeros[g]) : 8.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t code = __builtin_rotateright32(w, (3 + 16 * (i & 1) + 4 * (i >> 1)) & 31) & 15u;
+      sum += (double)bf16_to_f32(x[k + i]) * (s * ((double)code - z));
+    }
+  }
+  return (float)sum;
+}
+
 template <int ODT, int GROUP, bool ZEROS, int U, int C, int X>
 __global__ __launch_bounds__(256, X > kW4X ? 2 : 4) void gemv_w4_kernel(GemvW4Args a, bool by_row) {
   constexpr int kThreads = 256;
@@ -101,6 +123,7 @@ __global__ __launch_bounds__(256, X > kW4X ? 2 : 4) void gemv_w4_kernel(GemvW4Ar
   const int kq = wave;                         // this wave's quarter of K
   const int64_t at0 = (int64_t)want * a.nb;    // (blocks of columns past the last repeat it, unused)
   const Codes codes;
+  bool odd = false;  // whether a result of this lane's is not finite
   bf16x8 ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
@@ -124,7 +147,8 @@ __global__ __launch_bounds__(256, X > kW4X ? 2 : 4) void gemv_w4_kernel(GemvW4Ar
         if (p * kThreads >= rows << lp) break;
         const int i = threadIdx.x + p * kThreads, r = min(i >> lp, rows - 1), k = k0 + (i & ((1 << lp) - 1)) * 8;
         v[p] = *reinterpret_cast<const uint4*>(a.x + (int64_t)s_xrow[r0 + r] * a.K + min(k, a.K - 8));
-        if (k >= a.K) v[p] = make_uint4(0, 0, 0, 0);  // rows of W beyond K
+        // rows of W beyond K (in the large area at its store: 16 rows of 4096 x 4096 take 7.8 us with both here)
+        if (X == kW4X && k >= a.K) v[p] = make_uint4(0, 0, 0, 0);
       }
       uint4 wv[C][U];
       uint32_t sz[C][U];  // scale and zero
@@ -153,8 +177,9 @@ __global__ __launch_bounds__(256, X > kW4X ? 2 : 4) void gemv_w4_kernel(GemvW4Ar
 #pragma unroll
       for (int p = 0; p < XP; ++p) {
         if (p * kThreads >= rows << lp) break;
-        const int i = threadIdx.x + p * kThreads, r = i >> lp;
-        if (r < rows) *reinterpret_cast<uint4*>(&s_x[r * ldx + (i & ((1 << lp) - 1)) * 8]) = v[p];
+        const int i = threadIdx.x + p * kThreads, r = i >> lp, k = (i & ((1 << lp) - 1)) * 8;
+        if (X > kW4X && k0 + k >= a.K) v[p] = make_uint4(0, 0, 0, 0);  // (rows of W beyond K, see above)
+        if (r < rows) *reinterpret_cast<uint4*>(&s_x[r * ldx + k]) = v[p];
       }
       lds_barrier();
 #pragma unroll
@@ -205,10 +230,24 @@ __global__ __launch_bounds__(256, X > kW4X ? 2 : 4) void gemv_w4_kernel(GemvW4Ar
 #pragma unroll
         for (int k = 1; k < 4; ++k) v += s_part[n][k][tr][tc];
         if (column < a.N) st1<ODT>(a.out, out + column, v);
+        odd |= !(fabsf(v) < INFINITY);
       }
     }
     lds_barrier();
   }
+  if (!__any(odd)) return;
+  // This lane's results that are not finite (its own stores, read back).  The arguments
+  // are read anew: kept until here, they would cost the main loop its registers (5 %).
+  auto* args = __builtin_amdgcn_kernarg_segment_ptr();
+  __asm__ volatile("" : "+s"(args));
+  const GemvW4Args b = *(const GemvW4Args*)args;
+  for (int r = blockIdx.z * 16 + (threadIdx.x >> 4); r < n_rows; r += gridDim.z * 16)
+    for (int n = 0; n < C; ++n) {
+      const int column = (cb0 + n) * 16 + (threadIdx.x & 15);
+      const int64_t at = (int64_t)s_rows[r] * b.N + column;
+      if (column < b.N && !(fabsf(ld1<ODT>(b.out, at)) < INFINITY))
+        st1<ODT>(b.out, at, by_definition<GROUP, ZEROS>(b, at0 + cb0 + n, threadIdx.x & 15, s_xrow[r]));
+    }
 }
 
 template <int ODT, int GROUP, bool ZEROS, int U, int C, int X>

@@ -9,7 +9,7 @@ import torch
 import moe_ref as ref
 from computation_collective_amd import buffers as bf
 from computation_collective_amd import hocf
-from test_gpu_moe import dev, gen, host, near, run, say
+from test_gpu_moe import HALF, dev, gen, host, near, run, say, w4_case, w4_steps
 
 pytestmark = pytest.mark.gpu
 SOFTMAX, SIGMOID = hocf.HOCF_SCORE_SOFTMAX, hocf.HOCF_SCORE_SIGMOID
@@ -124,3 +124,48 @@ def test_route_equal_scores_across_keys():
     for renorm in (False, True):
         h = run(bf.MoeRoute(2, 8, 2, x, n_group=4, topk_group=2, renorm=renorm))
         assert h.experts.cpu().tolist() == e.tolist() == [[6, 1], [6, 1]]
+
+
+@pytest.mark.parametrize("R,E,N,K,group", [(1, 1, 24, 136, 32), (5, 1, 40, 1160, 64), (20, 1, 24, 264, 128),
+                                           (16, 4, 4104, 640, 64), (3, 40, 72, 4224, 128)])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("out_dt", [torch.float32, torch.bfloat16])
+def test_w4_values_that_are_not_finite(R, E, N, K, group, zeros, out_dt):
+    """Infinities and NaN in x, scales and zero points, and finite values whose sums leave the range of binary32 before
+    the zero points are taken off: what the definition gives in 64 bits."""
+    inf, nan = float("inf"), float("nan")
+    say(f"w4 not finite R={R} E={E} N={N} K={K} group={group} zeros={zeros}")
+    for kind in range(6):
+        codes, scales, z = w4_case(E, N, K, group, zeros, R + K + kind)
+        x = torch.randn(R, K, generator=gen(kind)).bfloat16()
+        if kind == 0:
+            x[0, K // 2] = inf
+        elif kind == 1:
+            x[-1, 0], x[-1, K - 1] = -inf, inf
+        elif kind == 2:
+            x[R // 2, K - 3] = nan
+        elif kind == 3:                          # finite, and so are the results: 3e38 * 1e-3 * 15 * K
+            x[0] = 3e38 * torch.randn(K, generator=gen(9)).sign()
+            x[-1, ::5] = 2e38
+            scales *= 2.0 ** -14
+        elif kind == 4:
+            scales[0, 0, N // 2], scales[-1, -1, 3], scales[0, 0, 0] = inf, nan, 0.0
+            x[:, 1] = 1e38
+        elif zeros:
+            z[0, 0, 5], z[-1, -1, N - 1] = inf, -inf
+            z[0, 0, 1] = 1e30
+        experts = torch.randint(-1, E + 1, (R,), generator=gen(R), dtype=torch.int32) if E > 1 else None
+        if E > 1:
+            experts[0], experts[-1] = 0, E - 1
+        wq, s, zz = bf.w4_pack(codes.cuda(), scales.cuda(), None if z is None else z.cuda(), group)
+        h = run(bf.GemvW4(R, 1, E, 0, N, K, group, x.cuda(), dev(experts), wq, s, zz,
+                          out_dt=hocf.HOCF_F32 if out_dt == torch.float32 else hocf.HOCF_BF16))
+        with np.errstate(invalid="ignore", over="ignore"):
+            want, size = ref.w4(x.float().numpy(), codes.numpy(), scales.float().numpy(),
+                                None if z is None else z.float().numpy(), None if experts is None else experts.numpy(),
+                                0, 1, group)
+        got, fin = host(h.out), np.isfinite(want)
+        assert fin.all() or kind != 3
+        assert np.array_equal(got[~fin], want[~fin], equal_nan=True), kind
+        room = HALF[out_dt] * np.abs(want[fin]) + ref.rel_steps(w4_steps(K, group)) * size[fin] + 2.0 ** -126
+        assert (np.abs(got[fin] - want[fin]) <= room).all(), kind
