@@ -61,6 +61,10 @@ class _Common:
     def status_value(self) -> int:
         return int(self.status.item())
 
+    def report_to(self, word: torch.Tensor) -> None:
+        """What later calls report asynchronously goes to this status word (int32 [1])."""
+        self.status = word
+
 
 class GemmRS(_Common):
     """hocf_gemm_rs: A [P][M][K], W [P][K][N] -> windows [P dst][P src][Mc][N], out [M][N]."""
@@ -442,6 +446,10 @@ class _Moe(_Common):
         self._sync = self.next_sync()
         self._fn = hocf.bind(entry, args, self._sync)
         self._index = torch.cuda.current_device() if device.index is None else device.index
+
+    def report_to(self, word):
+        super().report_to(word)
+        self._sync.status = word.data_ptr()
 
     def call(self, stream=None) -> int:
         self.epoch = self._sync.epoch = (self.epoch % 0xFFFFFFF0) + 1

@@ -42,10 +42,16 @@ class MoeLayer:
 
     forward(X [P][B][K] bf16) -> out [P][B][K] bf16 (the residual X included);
     backward(dout) -> (drows [P][P*cap][K], dlogits [P*B][P*E]): the gradients
-    that the experts' and the router's own products take.  Pairs beyond a
-    window's `cap` rows are dropped.  `recv_rows`: rows one rank receives at most
-    (its experts' groups padded to 256); rows beyond make forward() raise.  B *
-    topk is a multiple of 4 (every rank's choices start on 16 bytes)."""
+    that the experts' and the router's own products take (those products, and
+    the way of drows back to the experts' ranks, are not part of the layer).
+    `cap`: rows one rank sends to one source at most.  `recv_rows`: rows one rank
+    receives at most (its experts' groups padded to 256).  forward() raises where
+    a batch needs more of either, and computes the next one that does not.  B *
+    topk is a multiple of 4 (every rank's choices start on 16 bytes).
+
+    The operators' error words are read where forward() waits for the device
+    anyway, and by check(), which waits: an error of the last operators of a step
+    is raised by the next forward(), or by a check() after the step."""
 
     def __init__(self, P, E, B, topk, w_router, w_up, w_down, cap, recv_rows, score=hocf.HOCF_SCORE_SOFTMAX,
                  renorm=True):
@@ -68,7 +74,6 @@ class MoeLayer:
         self.win = [hocf.windows([(self.windows[s, p], self.flags[s, p]) for s in range(P)]) for p in range(P)]
         ws = hocf.hocf_gemm_a2a_workspace_bytes(P)
         self.ws = torch.zeros((ws + 3) // 4 + 4, dtype=torch.int32, device=w_up.device)
-        self.status = torch.zeros(1, dtype=torch.int32, device=w_up.device)
         self.epoch = 0
         self.slots = [bf.MoeSlots(B, topk, P, E, cap, experts[s]) for s in range(P)]
         rows = [self.windows[s].view(P * cap, self.K) for s in range(P)]
@@ -78,6 +83,23 @@ class MoeLayer:
                                              index=self.slots[s].index, pair=self.slots[s].pair) for s in range(P)]
         self.dweights = torch.empty((P * B, topk), dtype=torch.float32, device=w_up.device)
         self.route_bwd = bf.MoeRouteBwd(P * B, P * E, topk, self.logits, self.route.experts, self.dweights, **how)
+        # one error word for every operator that can report one
+        parts = [(f"rank {p}: dispatch", self.dispatch[p]) for p in range(P)]
+        parts += [(f"source {s}: weighted sum", self.combine[s]) for s in range(P)]
+        parts += [(f"source {s}: backward pass of the weighted sum", self.combine_bwd[s]) for s in range(P)]
+        parts += [("backward pass of the router", self.route_bwd)]
+        self.status = torch.zeros(len(parts) + P, dtype=torch.int32, device=w_up.device)
+        for i, (_, handle) in enumerate(parts):
+            handle.report_to(self.status[i:i + 1])
+        self.reporters = [name for name, _ in parts] + [f"rank {p}: down projection" for p in range(P)]
+
+    def check(self):
+        """Raises what an operator has reported since the last check; waits for the stream."""
+        words = self.status.tolist()
+        if any(words):
+            self.status.zero_()
+            raise RuntimeError("; ".join(f"{name}: {hocf.status_string(w)}"
+                                         for name, w in zip(self.reporters, words) if w))
 
     def forward(self, X):
         P, E = self.P, self.E
@@ -92,8 +114,7 @@ class MoeLayer:
         for p in range(P):
             d = self.dispatch[p]
             offsets, sent = d.offsets.cpu().numpy(), d.send_counts.cpu().numpy()
-            if d.status_value():
-                raise RuntimeError(f"rank {p}: {hocf.status_string(d.status_value())}")
+            self.check()
             if sent.max() > self.cap:
                 raise RuntimeError(f"rank {p} sends {sent.max()} rows to one source, its window holds {self.cap}")
             y = d.Y.view(torch.bfloat16)
@@ -102,7 +123,7 @@ class MoeLayer:
             hocf.check(hocf.hocf_gemm_a2a(
                 P, E, int(offsets[-1]), self.K, self.H, bf.BF16, bf.BF16, d.Y, self.w_down[p * E:(p + 1) * E], offsets,
                 d.dest, d.slot, sent, self.win[p], self.cap, 256, 256,
-                hocf.sync(self.epoch, self.ws, self.ws.numel() * 4 - 16, status=self.status),
+                hocf.sync(self.epoch, self.ws, self.ws.numel() * 4 - 16, status=self.status[p - P:].data_ptr()),
                 torch.cuda.current_stream(self.X.device)))
         for s in range(P):
             self.combine[s].run()
@@ -188,6 +209,8 @@ def main(argv=None):
     layer = MoeLayer(P, E, B, topk, normal(K, P * E, std=K ** -0.5), normal(P * E, K, H, std=0.02),
                      normal(P * E, H, K, std=0.02), cap=2 * pairs + 64, recv_rows=2 * P * pairs + E * 256)
     X, dout = normal(P, B, K), normal(P, B, K)
+    layer.backward(layer.forward(X))
+    layer.check()
     print(f"layer, {P} ranks x {B} tokens, top-{topk} of {P * E} experts {K} -> {H} -> {K}: "
           f"forward {_timed(lambda: layer.forward(X), a.steps):.3f} ms, "
           f"backward of combine and router {_timed(lambda: layer.backward(dout), a.steps):.3f} ms")

@@ -9,6 +9,7 @@ import torch
 import moe_ref as ref
 from computation_collective_amd import buffers as bf
 from computation_collective_amd import hocf
+from computation_collective_amd import moe_layer
 from test_gpu_moe import HALF, dev, gen, host, near, run, say, w4_case, w4_steps
 
 pytestmark = pytest.mark.gpu
@@ -169,3 +170,62 @@ def test_w4_values_that_are_not_finite(R, E, N, K, group, zeros, out_dt):
         assert np.array_equal(got[~fin], want[~fin], equal_nan=True), kind
         room = HALF[out_dt] * np.abs(want[fin]) + ref.rel_steps(w4_steps(K, group)) * size[fin] + 2.0 ** -126
         assert (np.abs(got[fin] - want[fin]) <= room).all(), kind
+
+
+# ------------------------------------------------------------------------------ the layer
+
+def two_way_layer(P, E, B, cap, recv_rows):
+    """P * E = 2 experts; a token goes to the first where its first element is positive, else to the second."""
+    K = H = 256
+    g = gen(11)
+    router = torch.zeros(K, 2)
+    router[0] = torch.tensor([1.0, -1.0])
+    up, down = (0.06 * torch.randn(2, K, H, generator=g)).bfloat16().cuda(), (0.06 * torch.randn(2, H, K, generator=g)).bfloat16().cuda()
+    return moe_layer.MoeLayer(P, E, B, 1, router.bfloat16().cuda(), up, down, cap=cap, recv_rows=recv_rows)
+
+
+def two_way_input(P, B, first):
+    """`first` tokens of every rank go to the first expert."""
+    x = 0.1 * torch.randn(P, B, 256, generator=gen(12))
+    x[:, :, 0] = torch.where(torch.arange(B) < first, 3.0, -3.0)
+    return x.bfloat16().cuda()
+
+
+@pytest.mark.parametrize("P,E,cap,recv_rows,fits,does_not,match", [
+    (1, 2, 8, 256, (8, 0), 3, "rank 0.*receive buffer"), (2, 1, 4, 512, (4,), 7, "its window holds 4")])
+def test_layer_after_an_input_it_refused(P, E, cap, recv_rows, fits, does_not, match):
+    """What a batch overflowed does not stay behind: the next one that fits is computed as by a new layer."""
+    B = 8
+    say(f"layer after a refused input P={P} cap={cap}")
+    layer = two_way_layer(P, E, B, cap, recv_rows)
+    for n in fits:
+        with pytest.raises(RuntimeError, match=match):
+            layer.forward(two_way_input(P, B, does_not))
+        x = two_way_input(P, B, n)
+        out = layer.forward(x)
+        assert torch.equal(out, two_way_layer(P, E, B, cap, recv_rows).forward(x))
+        drows, dlogits = layer.backward(x)
+        layer.check()
+        assert torch.isfinite(dlogits).all()
+
+
+def test_layer_reports_what_its_operators_found():
+    """An error word that an operator sets is raised once, by check() or by the next forward(), and cleared."""
+    P, E, B = 2, 1, 8
+    layer, x = two_way_layer(P, E, B, 8, 512), two_way_input(P, B, 4)
+    say("layer reports")
+    want = layer.forward(x)
+    layer.check()
+    for by_check in (True, False):
+        layer.forward(x)
+        layer.slots[1].index[3, 0] = 10 ** 6       # a row that no window has
+        layer.backward(x)
+        with pytest.raises(RuntimeError, match="source 1.*weighted sum.*index"):
+            layer.check() if by_check else layer.forward(x)
+        layer.check()
+        assert torch.equal(layer.forward(x), want)
+    layer.route.experts[5, 0] = -7                 # no expert of the row
+    layer.backward(x)
+    with pytest.raises(RuntimeError, match="router.*index"):
+        layer.check()
+    layer.check()
