@@ -10,7 +10,8 @@ import moe_ref as ref
 from computation_collective_amd import buffers as bf
 from computation_collective_amd import hocf
 from computation_collective_amd import moe_layer
-from test_gpu_moe import HALF, dev, gen, host, near, run, say, w4_case, w4_steps
+from test_gpu_moe import (HALF, TYPES, check_route, check_w4, combine_inputs, dev, gen, host, logits, near, run, say,
+                          w4_case, w4_steps)
 
 pytestmark = pytest.mark.gpu
 SOFTMAX, SIGMOID = hocf.HOCF_SCORE_SOFTMAX, hocf.HOCF_SCORE_SIGMOID
@@ -229,3 +230,62 @@ def test_layer_reports_what_its_operators_found():
     with pytest.raises(RuntimeError, match="router.*index"):
         layer.check()
     layer.check()
+
+
+# ------------------------------------------------------------------------------ forms of large and odd shapes
+
+@pytest.mark.parametrize("T,topk,N,bins,dt,out_dt", [
+    (2048, 2, 64, 0, torch.bfloat16, torch.bfloat16), (2051, 3, 128, 4, torch.bfloat16, torch.float32),
+    (2050, 2, 4096, 8, torch.bfloat16, torch.bfloat16), (2049, 8, 96, 8, torch.float32, torch.bfloat16),
+    (2053, 9, 192, 5, torch.bfloat16, torch.bfloat16), (2048, 16, 64, 0, torch.float32, torch.float32),
+    (2055, 12, 520, 3, torch.bfloat16, torch.bfloat16), (2050, 1, 32, 1, torch.float32, torch.float32)])
+def test_combine_of_many_tokens(T, topk, N, bins, dt, out_dt):
+    """A wave to a token: rows of whole cache lines (and one of parts of lines with more than eight places)."""
+    say(f"combine of many tokens T={T} topk={topk} N={N} bins={bins} {dt} {out_dt}")
+    rows, w, index, pair, dout = combine_inputs(T, topk, N, bins, dt, out_dt, T + N)
+    if index is not None:
+        gone = index[7].copy()
+        index[7] = -1                            # a token without rows: theirs have no pair either
+        pair[gone[gone >= 0]] = -1
+        rows[torch.from_numpy(gone[gone >= 0]).long()] = float("nan")
+    h = run(bf.MoeCombine(T, topk, N, dev(rows), dev(w), index=dev(index), out_dt=TYPES[out_dt]))
+    out, size = ref.combine(rows.float().numpy(), w.numpy(), index)
+    near(h.out, out, size, out_dt, topk + 1)
+    h = run(bf.MoeCombineBwd(T, topk, N, dev(rows), dev(w), dev(dout), index=dev(index), pair=dev(pair)))
+    dr, dw, size = ref.combine_bwd(rows.float().numpy(), w.numpy(), dout.float().numpy(), index)
+    near(h.drows, dr, np.abs(dr), dt, 1)
+    near(h.dweights, dw, size, torch.float32, N / 64 + 10)
+    first = h.dweights.clone(), h.drows.clone()
+    run(h)
+    assert torch.equal(first[0], h.dweights) and torch.equal(first[1], h.drows)
+
+
+@pytest.mark.parametrize("R,E,N,K,group,rows_of_one", [
+    (16, 16, 2056, 264, 64, 0),       # 129 blocks of columns x 16 experts: two blocks to a workgroup, the last one alone
+    (16, 32, 2056, 264, 128, 3),      # fewer rows than experts: a workgroup to the first row of each
+    (32, 32, 1064, 1160, 32, 12),     # 9 to 16 blocks of rows, and passes that hold 12 rows
+    (16, 16, 2072, 2184, 128, 9),     # more than 16 blocks of rows
+    (64, 16, 2056, 1032, 64, 20),     # more rows of one expert than a tile
+    (3, 1, 88, 1288, 128, 0), (4, 1, 264, 2048, 32, 0),   # one block to a workgroup, 9 to 16 blocks of rows, few rows
+    (3, 1, 32792, 136, 64, 0), (40, 1, 16648, 392, 64, 0)])   # one matrix of many columns, a few rows and three tiles
+@pytest.mark.parametrize("zeros", [False, True])
+def test_w4_of_many_blocks(R, E, N, K, group, rows_of_one, zeros):
+    say(f"w4 of many blocks R={R} E={E} N={N} K={K} group={group} zeros={zeros}")
+    experts = None
+    if E > 1:
+        experts = torch.randint(-1, E + 1, (R,), generator=gen(R + K), dtype=torch.int32)
+        experts[:rows_of_one] = E - 1
+    for out_dt in (torch.bfloat16, torch.float32):
+        check_w4(R, 1, E, 0, N, K, group, zeros, experts, out_dt, R + N)
+
+
+@pytest.mark.parametrize("E,n_group,topk_group,group_top,topk", [
+    (500, 5, 2, 2, 8), (500, 5, 3, 1, 16), (495, 33, 9, 2, 10), (507, 39, 20, 1, 5), (510, 17, 4, 2, 7), (432, 3, 1, 2, 8)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_long_runs_of_a_wave(E, n_group, topk_group, group_top, topk, dtype):
+    """A wave to a token whose lanes hold 9 to 16 experts each."""
+    say(f"route E={E} of {n_group} take {topk_group} top {group_top} {dtype}")
+    bias = 0.01 * torch.randint(-20, 21, (E,), generator=gen(E)).float()
+    for score, b, masked in ((SIGMOID, bias, 0.0), (SOFTMAX, None, 0.2), (SIGMOID, None, 0.5)):
+        check_route(logits(70, E, dtype, 5 * E, E + 1, masked), topk, bias=b, score=score, n_group=n_group,
+                    topk_group=topk_group, group_top=group_top, renorm=True)
