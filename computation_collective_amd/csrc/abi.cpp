@@ -108,7 +108,7 @@ const char* hocf_status_string(hocf_status s) {
     case HOCF_ERR_HIP: return "HIP runtime error";
     case HOCF_ERR_TIMEOUT: return "flag wait timed out";
     case HOCF_ERR_ABORTED: return "aborted";
-    case HOCF_ERR_BAD_INDEX: return "embedding index out of range";
+    case HOCF_ERR_BAD_INDEX: return "index out of range";
     case HOCF_ERR_PROTOCOL: return "partial consumed before its flag was set";
     case HOCF_ERR_CAPACITY: return "more rows routed here than the receive buffer holds";
   }

@@ -20,8 +20,10 @@
 // -- so that its products start with the first weights.
 //
 // Bound by the weights' bytes, and by the 2-3 us until the first of them
-// arrive: one token's 8 experts 4096 -> 1792 (30 MB) 8.8 us, 16 tokens x 2 of 32
-// experts 1792 -> 4096 (86 MB) 20-22 us.
+// arrive: one token's 8 experts 4096 -> 1792 (30 MB) 8.9 us, 16 tokens x 2 of 32
+// experts 1792 -> 4096 (86 MB) 20-22 us.  Beyond 16 rows of an expert, every tile of
+// 16 rows reads and decodes its weights again: 4096 x 4096, 16 rows 7.5 us, 32 rows
+// 8.8, 64 rows 16, 1024 rows 320.
 #include <algorithm>
 
 #include "moe.hpp"
@@ -63,7 +65,7 @@ __device__ __forceinline__ int local_expert(const GemvW4Args& a, int r) {
 }
 
 // One result by the definition (column c of column block `block`, counted over all
-// experts).  Slow, a few microseconds for every 64 rows of W, and hardly ever needed.
+// experts).  Slow (K = 4096: 120-140 us in all), and hardly ever needed.
 template <int GROUP, bool ZEROS>
 __device__ __forceinline__ float by_definition(const GemvW4Args& a, int64_t block, int c, int xrow) {
   const uint16_t* x = a.x + (int64_t)xrow * a.K;

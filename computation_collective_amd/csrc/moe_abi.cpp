@@ -7,8 +7,6 @@ using namespace hocf;
 
 namespace {
 
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 int64_t dt_bytes(hocf_dtype d) { return d == HOCF_BF16 ? 2 : 4; }
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;

@@ -11,8 +11,9 @@
 // Two forms.  For few pairs, one kernel: every workgroup counts all the pairs,
 // those before and after its own too, from one load of each.  Beyond, a kernel
 // counts every chunk, and a second one sums the chunks before and after its own
-// and places its pairs.  Both are bound by launches and latency (8192 pairs 5.3
-// us, 524288 pairs 8.1-8.7), so everything a wave reads is on its way at once.
+// and places its pairs.  Both are bound by launches and latency (8192 pairs of 8
+// bins 5.3 us, 524288 pairs of 16 bins 8.2 us), so everything a wave reads is on
+// its way at once.
 #include "lanes.hpp"
 #include "moe.hpp"
 #include "publish.hpp"
@@ -286,9 +287,10 @@ static int launch_direct(const SlotsArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// One kernel up to a workgroup's pairs, and with up to 8 bins up to eight
-// (8192 pairs: 6.1 us, where the two kernels take 6.5 and their launches 7.7;
-// with 16 bins 8.4 us).
+// One kernel up to a workgroup's pairs, and with up to 8 bins up to eight:
+// replayed from a graph, 8192 pairs take 5.2 us and the two kernels 5.6, 16384
+// pairs 6.5 and 5.7 (called one by one, two launches take 8-9.5 us whatever they
+// do).  With 16 bins the counts by ballots cost it more: 5.5 and 5.8 at 8192 pairs.
 template <int NB>
 static int launch_bits(const SlotsArgs& a, hipStream_t s) {
   if (a.pairs <= kSlotsThreads) return launch_direct<NB, 1>(a, s);

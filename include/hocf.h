@@ -61,7 +61,8 @@
  * is a device pointer on the current HIP device, 16-byte aligned, except
  * sync->abort_flag (device or host-pinned memory) and the hocf_window arrays
  * themselves (host memory, read during the call).  All tensors are dense
- * row-major.  bf16 tensors hold bfloat16 bit patterns (uint16).
+ * row-major, but for a router's logits, whose rows may be apart.  bf16
+ * tensors hold bfloat16 bit patterns (uint16).
  *
  * Streams.  A call validates its arguments, enqueues its kernel (the
  * unfused baselines: its two kernels) on `stream`
@@ -80,7 +81,7 @@
  * returns HOCF_ERR_HIP.
  *
  * Asynchronous errors.  A wait that exceeds its time limit, an abort request
- * or an out-of-range embedding index is recorded in *sync->status (if
+ * or an out-of-range index (an embedding's, a row's or an expert's) is recorded in *sync->status (if
  * non-NULL) by the first workgroup that meets it (compare-and-swap from 0);
  * every workgroup still exits, and the outputs are then unspecified.  The
  * caller zeroes *status before the call and reads it after.  Every wait of
@@ -103,11 +104,15 @@
  * environment variable HOCF_MAX_WORKGROUPS (a positive integer, read at each
  * call) caps it further, e.g. to leave CUs to other work or to have each
  * workgroup take many items; every operator completes with any grid of one
- * or more workgroups.
+ * or more workgroups.  hocf_moe_slots (one or two kernels), hocf_moe_combine
+ * and its backward pass, hocf_gemv_w4 and hocf_w4_pack launch ordinary grids,
+ * which the variable does not cap.
  *
  * Workspace.  Scheduler counters.  The caller allocates at least the size
  * the matching *_workspace_bytes() query returns, zeroes it ONCE, and may
- * then reuse it for any number of calls: every call leaves it zeroed again.
+ * then reuse it for any number of calls: every call leaves it zeroed again,
+ * except those of hocf_a2a_gemm* and hocf_moe_slots, which need no zeroing and
+ * do not leave it zeroed (zero it before another operator takes it).
  * Calls that may run concurrently need separate workspaces.
  */
 #ifndef HOCF_H
@@ -140,7 +145,7 @@ typedef enum hocf_status HOCF_ENUM_INT {
     HOCF_ERR_HIP = 3,         /* a HIP runtime call failed (launch, attribute query) */
     HOCF_ERR_TIMEOUT = 4,     /* (async) a flag wait exceeded sync->spin_timeout_ns */
     HOCF_ERR_ABORTED = 5,     /* (async) *sync->abort_flag became nonzero during a wait */
-    HOCF_ERR_BAD_INDEX = 6,   /* (async) an embedding index outside [0, R) was skipped */
+    HOCF_ERR_BAD_INDEX = 6,   /* (async) an index outside its range was skipped */
     HOCF_ERR_PROTOCOL = 7,    /* (async) a reducer found a partial's flag not set */
     HOCF_ERR_CAPACITY = 8     /* (async) more rows routed here than the receive buffer holds */
 } hocf_status;
@@ -609,7 +614,7 @@ hocf_status hocf_moe_route_bwd(int64_t T, int E, int topk, hocf_dtype dt, const 
  *
  * The results do not depend on the grid.  Supported: 1 <= bins <= 64,
  * per_bin >= 1, cap >= 0, topk >= 1; T * topk, bins * per_bin and bins * cap
- * below 2^31.  The workspace needs no zeroing.
+ * below 2^31.  The workspace needs no zeroing, and is not left zeroed.
  * ---------------------------------------------------------------------- */
 hocf_status hocf_moe_slots(int64_t T, int topk, int bins, int per_bin, int64_t cap, const int32_t* experts,
                            int32_t* index, int32_t* pair, int64_t* counts, const hocf_sync* sync, void* stream);
@@ -667,7 +672,8 @@ hocf_status hocf_moe_combine_bwd(int64_t T, int topk, int N, int64_t R, hocf_dty
  * projection (the pairs of a token share its row), 1 for the down projection.
  * Every weight that some row needs is read once for up to 16 of its rows.
  * A row whose expert is not one of this rank's e0 .. e0+E-1 gets zeros, so
- * that the ranks' outputs add up.
+ * that the ranks' outputs add up.  Infinities and NaN in x, scales or zeros
+ * give what the sums above give (such a call is slow).
  *
  *   x        [R / rows_per_x][K] bf16
  *   experts  [R] int32, or NULL: one matrix for every row (E = 1)
