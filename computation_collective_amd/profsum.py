@@ -17,7 +17,7 @@ GRBM_GUI_ACTIVE` -- and writes one summary per operator,
     reads and writes 1 GiB), the factors known/measured they give, and the
     scaled bytes per launch between the L2s and the memory fabric (which the
     Infinity Cache may partly serve);
-  * the hash of the library sources the counters were taken with, and the
+  * the hash of the sources the profiled kernels were compiled from, and the
     variant (slot dtype, tile) that was profiled;
   * with the MFMA run: matrix-core busy cycles summed over all SIMDs,
     GRBM_GUI_ACTIVE (reported summed over the 8 XCDs, so divided by 8 for
@@ -33,7 +33,7 @@ bench.py's put operators: the kernels that ran (the runtime's copy kernels
 among them) and the copies the copy engines ran.
 
 `traffic(op, variant)` returns the scaled bytes, or None when there is no
-summary, it was taken for another variant, or the sources have changed.
+summary, it was taken for another variant, or the kernels' sources have changed.
 """
 
 from __future__ import annotations
@@ -42,6 +42,7 @@ import csv
 import glob
 import hashlib
 import os
+import re
 import statistics
 import sys
 from collections import defaultdict
@@ -50,6 +51,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 PROFILES = os.path.join(ROOT, "profiles")
 COPY_BYTES = 1 << 30  # the calibration pass reads and writes 1 GiB
+# the units that the profiled kernels are in
+UNITS = ("a2a_gemm.hip", "ag_gemm.hip", "embbag_a2a.hip", "gemm_a2a.hip", "gemm_rs.hip", "gemv_ar.hip")
 
 # kernel-name fragment -> operator name used by bench.py
 KERNELS = [("gemm_rs_kernel<hocf::TileF32", "gemm_rs_tiny"), ("gemm_rs_kernel", "gemm_rs"), ("gemm_ar_kernel", "gemm_ar"), ("gemm_a2a_kernel", "gemm_a2a"),
@@ -90,14 +93,20 @@ def workloads():
 
 
 def source_hash() -> str:
-    """sha256 over the library's HIP/C++ sources and the ABI header."""
+    """sha256 over the sources that the profiled kernels are compiled from: their units and
+    the headers that these include, and no other operator's (whose changes leave the
+    summaries valid)."""
+    found, todo = {}, list(UNITS)
+    while todo:
+        name = todo.pop()
+        if name not in found:
+            with open(os.path.join(HERE, "csrc", name), "rb") as fh:
+                found[name] = fh.read()
+            todo += re.findall(r'^#include "(\w+\.hpp)"', found[name].decode(), re.M)
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(HERE, "csrc", "*"))) + [os.path.join(ROOT, "include", "hocf.h")]
-    for f in files:
-        if os.path.isfile(f):
-            h.update(os.path.basename(f).encode())
-            with open(f, "rb") as fh:
-                h.update(fh.read())
+    for name in sorted(found):
+        h.update(name.encode())
+        h.update(found[name])
     return h.hexdigest()[:16]
 
 

@@ -1,5 +1,6 @@
 """Host logic around the mixture-of-experts operators (CPU only): the rules by
-which a call's kernel form is chosen, and what the Python handles refuse."""
+which a call's kernel form is chosen, what the Python handles refuse, and that
+the other operators' profile summaries stay valid beside them."""
 
 import os
 import shutil
@@ -9,6 +10,7 @@ import pytest
 import torch
 
 from computation_collective_amd import buffers as bf
+from computation_collective_amd import profsum
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "computation_collective_amd", "csrc")
@@ -97,3 +99,35 @@ def test_handles_refuse_host_memory():
                                    torch.zeros(small, dtype=b))):
         with pytest.raises(ValueError, match="on cpu"):
             make()
+
+
+# ------------------------------------------------------------------ the bench's memory traffic
+
+def test_committed_summaries_are_current():
+    """Every profiled operator's traffic is known from the committed summaries, as bench.py prints it."""
+    for op in list(profsum.workloads()) + list(profsum.COMPOSITE):
+        if op in profsum.COMPOSITE or os.path.isfile(os.path.join(profsum.PROFILES, profsum.workloads()[op][0] + ".txt")):
+            assert profsum.traffic(op), op
+
+
+def test_summaries_outlive_other_operators_changes(tmp_path, monkeypatch):
+    """The hash in a summary covers the profiled kernels' units and the headers they include, and nothing else."""
+    src = profsum.source_hash()
+    shutil.copytree(os.path.join(ROOT, "computation_collective_amd", "csrc"), tmp_path / "csrc")
+    monkeypatch.setattr(profsum, "HERE", str(tmp_path))
+    assert profsum.source_hash() == src
+
+    def after(name, text):
+        with open(tmp_path / "csrc" / name, "a") as fh:
+            fh.write(text)
+        return profsum.source_hash()
+
+    for name in ("moe_route.hip", "gemv_w4.hip", "moe.hpp", "abi.cpp", "another.hip"):
+        assert after(name, "// more\n") == src
+    for name in ("embbag_a2a.hip", "mfma_tile.hpp", "common.hpp"):     # a unit, its header, that header's
+        assert after(name, "// more\n") != src
+        src = profsum.source_hash()
+    with open(tmp_path / "csrc" / "new.hpp", "w") as fh:
+        fh.write("// new\n")
+    src = after("gemm_rs.hip", '#include "new.hpp"\n')
+    assert after("new.hpp", "// more\n") != src
