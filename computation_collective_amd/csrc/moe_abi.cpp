@@ -1,5 +1,7 @@
 // C entry points of the mixture-of-experts operators: argument validation
 // and launch-argument packing, as abi.cpp does for the fused operators.
+#include <algorithm>
+
 #include "abi_util.hpp"
 #include "moe.hpp"
 
@@ -239,6 +241,9 @@ static hocf_status check_w4(const char* op, int E, int N, int K, int group) {
   if (group != 32 && group != 64 && group != 128)
     return fail(HOCF_ERR_UNSUPPORTED, "%s: group=%d is none of 32, 64, 128", op, group);
   if (N > (1 << 20) || K > (1 << 20)) return fail(HOCF_ERR_UNSUPPORTED, "%s: N=%d or K=%d > 2^20", op, N, K);
+  // (no memory holds these; their sizes in bytes would not fit 64 bits)
+  if (E > (int64_t(1) << 60) / std::max<int64_t>(cdiv(N, 16) * 16 * cdiv(K, 128) * 128, 1))
+    return fail(HOCF_ERR_UNSUPPORTED, "%s: E=%d experts of %d x %d are more than 2^60 weights", op, E, K, N);
   return HOCF_OK;
 }
 
