@@ -66,8 +66,9 @@ def draw(rng):
     K, N = 16 * _log(rng, 4, 256), 8 * _log(rng, 8, 512)
     if op == "save":
         dt = rng.choice(["bf16", "bf16", "f32"])
-        return dict(op=op, T=_log(rng, 1, min(32768, 58_000_000 // K)), K=K, ld=K + rng.choice([0, 0, 8]), dt=dt,
-                    act=rng.choice(["none", "silu"]) if dt == "bf16" else "none", keep=rng.random() < 0.5)
+        act = rng.choice(["none", "silu"]) if dt == "bf16" else "none"
+        return dict(op=op, T=_log(rng, 1, min(32768, 58_000_000 // K)), K=K, ld=K + rng.choice([0, 0, 8]), dt=dt, act=act,
+                    keep=act == "silu" and rng.random() < 0.5)
     if op == "weights":
         return dict(op=op, E=rng.randint(1, max(1, min(8, 29_000_000 // (K * N)))), K=K, N=N, dt=rng.choice(["bf16", "f32"]))
     if op == "decode":
