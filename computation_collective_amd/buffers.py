@@ -635,3 +635,164 @@ class GemvW4(_Moe):
 
     def poison(self):
         nan_fill(self.out)
+
+
+# ------------------------------------------------------------ 8-bit integers
+
+def _rows_apart(x, T, K):
+    """Row stride of x [T][K]: the numbers of a row adjacent, the rows K or more apart."""
+    if tuple(x.shape) != (T, K):
+        raise ValueError(f"x has shape {tuple(x.shape)}, not {(T, K)}")
+    if K > 1 and x.stride(1) != 1:
+        raise ValueError("the numbers of a row of x are not adjacent")
+    if T > 1 and x.stride(0) < K:
+        raise ValueError(f"x's rows overlap: they are {x.stride(0)} apart, of {K} numbers")
+    return x.stride(0) if T > 1 else K  # (the stride of a single row says nothing)
+
+
+def _bf16(dy):
+    if dy.dtype not in (torch.bfloat16, torch.int16):
+        raise TypeError(f"dy is {dy.dtype}, not bfloat16")
+
+
+class QuantI8(_Moe):
+    """hocf_quant_i8: x [T][K] (rows may be apart) -> codes [T][K] int8, scales [T] of act(x);
+    with keep=True (and an activation) pre_codes and pre_scales of x itself too."""
+
+    def __init__(self, T, K, x, act=hocf.HOCF_ACT_NONE, keep=False):
+        ld, dev = _rows_apart(x, T, K), x.device
+        _on(dev)
+        self.x = x
+        self.codes = torch.empty((T, K), dtype=torch.int8, device=dev)
+        self.scales = torch.empty(T, dtype=torch.float32, device=dev)
+        self.pre_codes = torch.empty_like(self.codes) if keep else None
+        self.pre_scales = torch.empty_like(self.scales) if keep else None
+        args = (T, K, torch_dt(x), x.data_ptr(), ld, act, self.codes.data_ptr(), self.scales.data_ptr(),
+                hocf.ptr(self.pre_codes), hocf.ptr(self.pre_scales))
+        self._bind("hocf_quant_i8", args, dev)
+
+    def poison(self):
+        for q, s in ((self.codes, self.scales), (self.pre_codes, self.pre_scales)):
+            if q is not None:
+                q.fill_(-128)
+                nan_fill(s)
+
+
+class DequantI8(_Moe):
+    """hocf_dequant_i8: codes [T][K] int8, scales [T] -> out [T][K]."""
+
+    def __init__(self, T, K, codes, scales, out_dt=BF16):
+        _dense(torch.int8, (T, K), codes=codes)
+        _dense(torch.float32, (T,), scales=scales)
+        _on(codes.device, scales=scales)
+        self.codes, self.scales = codes, scales
+        self.out = torch.empty((T, K), dtype=tdtype(out_dt), device=codes.device)
+        args = (T, K, out_dt, codes.data_ptr(), scales.data_ptr(), self.out.data_ptr())
+        self._bind("hocf_dequant_i8", args, codes.device)
+
+    def poison(self):
+        nan_fill(self.out)
+
+
+class WeightsI8(_Moe):
+    """hocf_weights_i8: w [E][K][N] -> wq [E][N][K] int8, scales [E][N]."""
+
+    def __init__(self, E, N, K, w):
+        _dense(None, (E, K, N), w=w)
+        _on(w.device)
+        self.w = w
+        self.wq = torch.empty((E, N, K), dtype=torch.int8, device=w.device)
+        self.scales = torch.empty((E, N), dtype=torch.float32, device=w.device)
+        args = (E, N, K, torch_dt(w), w.data_ptr(), self.wq.data_ptr(), self.scales.data_ptr())
+        self._bind("hocf_weights_i8", args, w.device, hocf.hocf_weights_i8_workspace_bytes(E, N, K))
+
+    def poison(self):
+        self.wq.fill_(-128)
+        nan_fill(self.scales)
+
+
+class GemmI8(_Moe):
+    """hocf_gemm_i8: xq [T][K], xs [T], wq [E][N][K], ws [E][N] and the groups' offsets [E + 1]
+    int64 (None: one matrix for every row) -> out [T][N].  Rows of no group keep what
+    out held."""
+
+    def __init__(self, E, T, N, K, xq, xs, wq, ws, offsets=None, out_dt=BF16):
+        _dense(torch.int8, (T, K), xq=xq)
+        _dense(torch.float32, (T,), xs=xs)
+        _dense(torch.int8, (E, N, K), wq=wq)
+        _dense(torch.float32, (E, N), ws=ws)
+        _dense(torch.int64, (E + 1,), offsets=offsets)
+        _on(xq.device, xs=xs, wq=wq, ws=ws, offsets=offsets)
+        self.xq, self.xs, self.wq, self.ws_, self.offsets = xq, xs, wq, ws, offsets
+        self.out = torch.empty((T, N), dtype=tdtype(out_dt), device=xq.device)
+        args = (E, T, N, K, out_dt, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), hocf.ptr(offsets),
+                self.out.data_ptr())
+        self._bind("hocf_gemm_i8", args, xq.device)
+
+    def poison(self):
+        nan_fill(self.out)
+
+
+class GemvI8(_Moe):
+    """hocf_gemv_i8: xq [R / rows_per_x][K], xs [R / rows_per_x], experts [R] (None: one matrix),
+    wq [E][N][K], ws [E][N] -> out [R][N]."""
+
+    def __init__(self, R, rows_per_x, E, e0, N, K, xq, xs, experts, wq, ws, out_dt=BF16):
+        _dense(torch.int8, (R // rows_per_x, K), xq=xq)
+        _dense(torch.float32, (R // rows_per_x,), xs=xs)
+        _dense(torch.int32, (R,), experts=experts)
+        _dense(torch.int8, (E, N, K), wq=wq)
+        _dense(torch.float32, (E, N), ws=ws)
+        _on(xq.device, xs=xs, experts=experts, wq=wq, ws=ws)
+        self.xq, self.xs, self.experts, self.wq, self.ws_ = xq, xs, experts, wq, ws
+        self.out = torch.empty((R, N), dtype=tdtype(out_dt), device=xq.device)
+        args = (R, rows_per_x, E, e0, N, K, out_dt, xq.data_ptr(), xs.data_ptr(), hocf.ptr(experts), wq.data_ptr(),
+                ws.data_ptr(), self.out.data_ptr())
+        self._bind("hocf_gemv_i8", args, xq.device)
+
+    def poison(self):
+        nan_fill(self.out)
+
+
+class GemmI8Dx(_Moe):
+    """hocf_gemm_i8_dx: dy [T][N] bf16, wq [E][N][K], ws [E][N], offsets as GemmI8 and, for the
+    gradient of what SiLU was given, pre_codes [T][K] and pre_scales [T] -> out [T][K].  Rows
+    of no group keep what out held."""
+
+    def __init__(self, E, T, N, K, dy, wq, ws, offsets=None, pre_codes=None, pre_scales=None, out_dt=BF16):
+        _dense(None, (T, N), dy=dy)
+        _bf16(dy)
+        _dense(torch.int8, (E, N, K), wq=wq)
+        _dense(torch.float32, (E, N), ws=ws)
+        _dense(torch.int64, (E + 1,), offsets=offsets)
+        _dense(torch.int8, (T, K), pre_codes=pre_codes)
+        _dense(torch.float32, (T,), pre_scales=pre_scales)
+        _on(dy.device, wq=wq, ws=ws, offsets=offsets, pre_codes=pre_codes, pre_scales=pre_scales)
+        self.dy, self.wq, self.ws_, self.offsets = dy, wq, ws, offsets
+        self.pre_codes, self.pre_scales = pre_codes, pre_scales
+        self.out = torch.empty((T, K), dtype=tdtype(out_dt), device=dy.device)
+        args = (E, T, N, K, out_dt, dy.data_ptr(), wq.data_ptr(), ws.data_ptr(), hocf.ptr(offsets),
+                hocf.ptr(pre_codes), hocf.ptr(pre_scales), self.out.data_ptr())
+        self._bind("hocf_gemm_i8_dx", args, dy.device)
+
+    def poison(self):
+        nan_fill(self.out)
+
+
+class GemmI8Dw(_Moe):
+    """hocf_gemm_i8_dw: xq [T][K], xs [T], dy [T][N] bf16, offsets as GemmI8 -> out [E][K][N]."""
+
+    def __init__(self, E, T, N, K, xq, xs, dy, offsets=None, out_dt=F32):
+        _dense(torch.int8, (T, K), xq=xq)
+        _dense(torch.float32, (T,), xs=xs)
+        _dense(None, (T, N), dy=dy)
+        _bf16(dy)
+        _dense(torch.int64, (E + 1,), offsets=offsets)
+        _on(xq.device, xs=xs, dy=dy, offsets=offsets)
+        self.xq, self.xs, self.dy, self.offsets = xq, xs, dy, offsets
+        self.out = torch.empty((E, K, N), dtype=tdtype(out_dt), device=xq.device)
+        args = (E, T, N, K, out_dt, xq.data_ptr(), xs.data_ptr(), dy.data_ptr(), hocf.ptr(offsets), self.out.data_ptr())
+        self._bind("hocf_gemm_i8_dw", args, xq.device)
+
+    def poison(self):
+        nan_fill(self.out)

@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libhocf.so")
 TRACE_LIB = os.path.join(HERE, "libhocf_trace.so")
 SOURCES = ["abi.cpp", "gemm_rs.hip", "gemv_ar.hip", "ag_gemm.hip", "embbag_a2a.hip", "gemm_a2a.hip",
            "a2a_gemm.hip", "moe_abi.cpp", "moe_route.hip", "moe_slots.hip",
-           "moe_combine.hip", "gemv_w4.hip"]
+           "moe_combine.hip", "gemv_w4.hip", "i8_abi.cpp", "i8_quant.hip", "i8_gemm.hip", "i8_grad.hip"]
 TRACE_SOURCES = ["abi.cpp", "gemm_rs.hip"]   # the sources HOCF_TRACE changes
 ARCH = "gfx950"
 

@@ -1,0 +1,358 @@
+// Rows and weights to 8-bit codes, and back.
+//
+//   s = max(largest |x| / 127 (rounded to fp32), 2^-126),  q = x / s to the
+//   nearest whole number, halves to the even one
+// of the real quotient: bf16 rows meet halves often (x = m / 254 of the largest
+// number), and a product with 1 / s would take them either way.  The product
+// gives a candidate t; x - t s is a whole number of half steps of s's last bit
+// and at most a little over s / 2, so an fma has it without error, and its size
+// against s / 2 tells whether t stands.  (s is never subnormal, for its
+// reciprocal and so that |q| stays below 128.)  A row with an infinity or a NaN
+// gets the scale NaN and codes 0: what is computed from it is NaN.
+//
+// All of it is bound by memory.  A row stays in registers between its largest
+// number and its codes: read once.
+#include <algorithm>
+
+#include "i8.hpp"
+#include "lanes.hpp"
+#include "sync.hpp"
+
+namespace hocf {
+
+constexpr int kQThreads = 256;
+
+// Workgroups in two dimensions (one dimension holds fewer than 2^32 threads), and a
+// workgroup's number among them; those past the last have nothing to do.
+static dim3 flat_grid(int64_t n) {
+  const int64_t x = std::min<int64_t>(n, 1 << 20);
+  return dim3((uint32_t)x, (uint32_t)((n + x - 1) / x));
+}
+__device__ __forceinline__ int64_t flat_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
+// Eight consecutive numbers of a row, as loaded.
+template <int DT>
+struct Eight;
+template <>
+struct Eight<kBF16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* row, int k) {
+    u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(row) + k);
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+};
+template <>
+struct Eight<kF32> {
+  float4 lo, hi;
+  __device__ __forceinline__ void load(const void* row, int k) {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(row) + k);
+    lo = p[0];
+    hi = p[1];
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    const float4& q = i < 4 ? lo : hi;
+    return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    lo = make_float4(v[0], v[1], v[2], v[3]);
+    hi = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+
+// The larger of the running magnitude (its bits: NaN > infinity > numbers) and eight more.
+template <int DT>
+__device__ __forceinline__ uint32_t largest(const Eight<DT>& e, uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(e[i]) & 0x7fffffffu);
+  return m;
+}
+
+struct Scale {
+  float s, inv;
+  bool bad;
+};
+__device__ __forceinline__ Scale scale_of(uint32_t m) {
+  Scale r;
+  r.bad = m >= 0x7f800000u;
+  r.s = fmaxf(__fdiv_rn(__uint_as_float(m), 127.0f), kI8TinyScale);
+  r.inv = __frcp_rn(r.s);
+  if (r.bad) r.s = __builtin_nanf("");
+  return r;
+}
+
+// Eight codes.  1.5 * 2^23 + t has the byte t at its low end.
+template <int DT>
+__device__ __forceinline__ uint2 codes_of(const Eight<DT>& e, const Scale& sc) {
+  constexpr float kMagic = 12582912.0f;
+  float y[8], worst = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[i] = fmaf(e[i], sc.inv, kMagic);
+    worst = fmaxf(worst, fabsf(fmaf(kMagic - y[i], sc.s, e[i])));
+  }
+  if (worst + worst >= sc.s) {  // (a half, or a candidate on the wrong side of one)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = fmaf(kMagic - y[i], sc.s, e[i]), d2 = fabsf(d) + fabsf(d);
+      if (d2 > sc.s || (d2 == sc.s && (__float_as_uint(y[i]) & 1u))) y[i] += copysignf(1.0f, d);
+    }
+  }
+  auto four = [&](int i) {
+    const uint32_t ab = __builtin_amdgcn_perm(__float_as_uint(y[i + 1]), __float_as_uint(y[i]), 0x0c0c0400u);
+    const uint32_t cd = __builtin_amdgcn_perm(__float_as_uint(y[i + 3]), __float_as_uint(y[i + 2]), 0x04000c0cu);
+    return ab | cd;
+  };
+  return sc.bad ? make_uint2(0, 0) : make_uint2(four(0), four(4));
+}
+
+// x / (1 + exp(-x)).  In fp32 for a result that is rounded to bf16 (off by less than
+// 2^-20 of itself for |x| < 16), where exp(-|x|) would leave fp32's range through a scaled
+// exponent; in 64 bits for an fp32 result, whose last bit decides codes.
+template <int DT>
+__device__ __forceinline__ float silu(float x) {
+  if constexpr (DT == kBF16) {
+    const float t = fabsf(x) * -1.44269504f;
+    const bool far = t < -100.0f;
+    const float p = __builtin_amdgcn_exp2f(far ? t + 64.0f : t);  // exp(-|x|)
+    const float q = x < 0.0f ? x * p : x;
+    return far ? (x < 0.0f ? q * 0x1p-64f : q) : q * __builtin_amdgcn_rcpf(1.0f + p);
+  } else {
+    return (float)((double)x / (1.0 + exp(-(double)x)));
+  }
+}
+template <int DT>
+__device__ __forceinline__ Eight<DT> silu8(const Eight<DT>& e) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = silu<DT>(e[i]);
+  Eight<DT> r;
+  r.set(v);
+  return r;
+}
+
+template <int W>
+__device__ __forceinline__ uint32_t row_largest(uint32_t m, uint32_t* s_max, int wave) {
+  m = (uint32_t)row_max<64>((int)m);  // (magnitudes: the sign bit is clear)
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) s_max[wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = max(m, s_max[w]);
+  }
+  return m;
+}
+
+// W waves a row (1 or 4), up to C pieces of eight numbers a lane; LOOP: rows of any
+// length, read twice.
+// (KEEP only with an activation: the codes of x and of act(x).)
+template <int DT, int ACT, bool KEEP, int W, int C, bool LOOP>
+__global__ __launch_bounds__(kQThreads) void quant_kernel(QuantI8Args a) {
+  __shared__ uint32_t s_max[2][4];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t row = W == 1 ? flat_block() * 4 + wave : flat_block();
+  if (row >= a.T) return;  // (W = 4: the workgroup's row)
+  const char* x = reinterpret_cast<const char*>(a.x) + row * a.ld * (DT == kBF16 ? 2 : 4);
+  const int k0 = (W == 1 ? lane : (int)threadIdx.x) * 8;
+  constexpr int kStep = W * 512;
+  static_assert(ACT == kSilu || !KEEP, "one side only");
+  Eight<DT> v[LOOP ? 1 : C], p[KEEP && !LOOP ? C : 1];
+  uint32_t m = 0, mp = 0;
+  if constexpr (LOOP) {
+    for (int k = k0; k < a.K; k += kStep) {
+      Eight<DT> e;
+      e.load(x, k);
+      if constexpr (KEEP) mp = largest(e, mp);
+      if constexpr (ACT == kSilu) e = silu8(e);
+      m = largest(e, m);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (k0 + c * kStep < a.K) (KEEP ? p[KEEP ? c : 0] : v[c]).load(x, k0 + c * kStep);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (k0 + c * kStep < a.K) {
+        if constexpr (KEEP) {
+          mp = largest(p[c], mp);
+          v[c] = silu8(p[c]);
+        } else if constexpr (ACT == kSilu) {
+          v[c] = silu8(v[c]);
+        }
+        m = largest(v[c], m);
+      }
+  }
+  const Scale s = scale_of(row_largest<W>(m, s_max[0], wave));
+  Scale sp = s;
+  if constexpr (KEEP) sp = scale_of(row_largest<W>(mp, s_max[1], wave));
+  int8_t* q = a.codes + row * a.K;
+  int8_t* qp = KEEP ? a.pre_codes + row * a.K : nullptr;
+  auto put = [&](int k, const Eight<DT>& pre, const Eight<DT>& act) {
+    *reinterpret_cast<uint2*>(q + k) = codes_of(act, s);
+    if constexpr (KEEP) *reinterpret_cast<uint2*>(qp + k) = codes_of(pre, sp);
+  };
+  if constexpr (LOOP) {
+    for (int k = k0; k < a.K; k += kStep) {
+      Eight<DT> e;
+      e.load(x, k);
+      put(k, e, ACT == kSilu ? silu8(e) : e);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (k0 + c * kStep < a.K) put(k0 + c * kStep, p[KEEP ? c : 0], v[c]);
+  }
+  if (lane == 0 && (W == 1 || wave == 0)) {
+    a.scales[row] = s.s;
+    if constexpr (KEEP) a.pre_scales[row] = sp.s;
+  }
+}
+
+template <int DT, int ACT, bool KEEP, int W, int C, bool LOOP>
+static int launch_q(const QuantI8Args& a, hipStream_t s) {
+  const int64_t grid = W == 1 ? (a.T + 3) / 4 : a.T;
+  hipLaunchKernelGGL((quant_kernel<DT, ACT, KEEP, W, C, LOOP>), flat_grid(grid), dim3(kQThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+// A wave a row where rows alone fill the device and fit a wave's registers, four
+// waves a row else.
+template <int DT, int ACT, bool KEEP>
+static int launch_act(const QuantI8Args& a, hipStream_t s) {
+  if (a.T >= 2048 && a.K <= 4096) {
+    if (a.K <= 1024) return launch_q<DT, ACT, KEEP, 1, 2, false>(a, s);
+    if (a.K <= 2048) return launch_q<DT, ACT, KEEP, 1, 4, false>(a, s);
+    return launch_q<DT, ACT, KEEP, 1, 8, false>(a, s);
+  }
+  if (a.K <= 2048) return launch_q<DT, ACT, KEEP, 4, 1, false>(a, s);
+  if (a.K <= 4096) return launch_q<DT, ACT, KEEP, 4, 2, false>(a, s);
+  if (a.K <= 8192) return launch_q<DT, ACT, KEEP, 4, 4, false>(a, s);
+  return launch_q<DT, ACT, KEEP, 4, 1, true>(a, s);
+}
+template <int DT>
+static int launch_qdt(const QuantI8Args& a, hipStream_t s) {
+  if (a.act == kSilu) return a.pre_codes ? launch_act<DT, kSilu, true>(a, s) : launch_act<DT, kSilu, false>(a, s);
+  return launch_act<DT, kNone, false>(a, s);
+}
+
+int launch_quant_i8(const QuantI8Args& a, hipStream_t s) {
+  return a.dt == kBF16 ? launch_qdt<kBF16>(a, s) : launch_qdt<kF32>(a, s);
+}
+
+// Reading back: lanes of a wave take pieces of eight codes of 1 to 8 rows.
+template <int DT>
+__global__ __launch_bounds__(kQThreads) void dequant_kernel(DequantI8Args a, int lg) {  // 2^lg lanes a row
+  const int64_t i = flat_block() * kQThreads + threadIdx.x, row = i >> lg;
+  if (row >= a.T) return;
+  const float s = a.scales[row];
+  for (int k = ((int)i & ((1 << lg) - 1)) * 8; k < a.K; k += 8 << lg) {
+    const uint2 w = *reinterpret_cast<const uint2*>(a.codes + row * a.K + k);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * s;
+    st4<DT>(a.out, row * a.K + k, floatx4{v[0], v[1], v[2], v[3]});
+    st4<DT>(a.out, row * a.K + k + 4, floatx4{v[4], v[5], v[6], v[7]});
+  }
+}
+
+int launch_dequant_i8(const DequantI8Args& a, hipStream_t s) {
+  int lg = 3;
+  while (lg < 6 && (8 << lg) < a.K) ++lg;
+  const int64_t grid = ((a.T << lg) + kQThreads - 1) / kQThreads;
+  if (a.dt == kBF16) hipLaunchKernelGGL(dequant_kernel<kBF16>, flat_grid(grid), dim3(kQThreads), 0, s, a, lg);
+  else hipLaunchKernelGGL(dequant_kernel<kF32>, flat_grid(grid), dim3(kQThreads), 0, s, a, lg);
+  return hipGetLastError();
+}
+
+// Weights, first step: the largest magnitude of every column of a slab of rows.
+// 64 columns x 256 rows a workgroup, eight lanes a row.
+template <int DT>
+__global__ __launch_bounds__(256) void w8_largest_kernel(WeightsI8Args a) {
+  __shared__ uint32_t s_max[32][65];
+  const int c8 = (threadIdx.x & 7) * 8, r0 = threadIdx.x >> 3;
+  const int n = blockIdx.x * 64 + c8, e = blockIdx.z;
+  uint32_t m[8] = {};
+  if (n < a.N) {
+    const int end = min(a.K, (int)(blockIdx.y + 1) * kW8SlabRows);
+    for (int k = blockIdx.y * kW8SlabRows + r0; k < end; k += 32) {
+      Eight<DT> v;
+      v.load(reinterpret_cast<const char*>(a.W) + (((int64_t)e * a.K + k) * a.N + n) * (DT == kBF16 ? 2 : 4), 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i] = max(m[i], __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s_max[r0][c8 + i] = m[i];
+  __syncthreads();
+  if (threadIdx.x < 64 && (int)(blockIdx.x * 64 + threadIdx.x) < a.N) {
+    uint32_t t = 0;
+    for (int r = 0; r < 32; ++r) t = max(t, s_max[r][threadIdx.x]);
+    a.part[((int64_t)e * a.slabs + blockIdx.y) * a.N + blockIdx.x * 64 + threadIdx.x] = t;
+  }
+}
+
+// Second step: 128 rows x 64 columns to codes, turned through LDS into 64 runs of 128 bytes.
+template <int DT>
+__global__ __launch_bounds__(256) void w8_codes_kernel(WeightsI8Args a) {
+  __shared__ Scale s_scale[64];
+  __shared__ __attribute__((aligned(16))) uint32_t s_q[64][36];  // [column][row / 4]: 144-byte rows
+  const int e = blockIdx.z, n0 = blockIdx.x * 64, kb = blockIdx.y * 128;
+  if (threadIdx.x < 64) {
+    const int n = min(n0 + (int)threadIdx.x, a.N - 1);
+    uint32_t m = 0;
+    for (int j = 0; j < a.slabs; ++j) m = max(m, a.part[((int64_t)e * a.slabs + j) * a.N + n]);
+    s_scale[threadIdx.x] = scale_of(m);
+    if (blockIdx.y == 0 && n0 + (int)threadIdx.x < a.N) a.scales[(int64_t)e * a.N + n] = s_scale[threadIdx.x].s;
+  }
+  // four rows x eight columns a thread
+  const int c8 = (threadIdx.x & 7) * 8, r4 = threadIdx.x >> 3;
+  const int n = n0 + c8, k = kb + r4 * 4;
+  Eight<DT> v[4];
+  const bool mine = n < a.N && k < a.K;
+  if (mine)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      v[r].load(reinterpret_cast<const char*>(a.W) + (((int64_t)e * a.K + k + r) * a.N + n) * (DT == kBF16 ? 2 : 4), 0);
+  __syncthreads();
+  if (mine) {
+    // codes_of takes eight numbers with one scale: two columns' four rows share none, so a column at a time
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const Scale sc = s_scale[c8 + i];
+      Eight<kF32> col;
+      const float f[8] = {v[0][i], v[1][i], v[2][i], v[3][i], 0.f, 0.f, 0.f, 0.f};
+      col.set(f);
+      s_q[c8 + i][r4] = codes_of(col, sc).x;
+    }
+  }
+  __syncthreads();
+  // 16 bytes a thread and pass: eight threads a column's 128 rows
+#pragma unroll
+  for (int t = threadIdx.x; t < 64 * 8; t += 256) {
+    const int c = t >> 3, k16 = kb + (t & 7) * 16;
+    if (n0 + c < a.N && k16 < a.K)
+      *reinterpret_cast<uint4*>(a.wq + ((int64_t)e * a.N + n0 + c) * a.K + k16) =
+          *reinterpret_cast<const uint4*>(&s_q[c][(t & 7) * 4]);
+  }
+}
+
+template <int DT>
+static int launch_w8(const WeightsI8Args& a, hipStream_t s) {
+  const int nb = (a.N + 63) / 64;
+  hipLaunchKernelGGL(w8_largest_kernel<DT>, dim3(nb, a.slabs, a.E), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(w8_codes_kernel<DT>, dim3(nb, (a.K + 127) / 128, a.E), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+int launch_weights_i8(const WeightsI8Args& a, hipStream_t s) {
+  return a.dt == kBF16 ? launch_w8<kBF16>(a, s) : launch_w8<kF32>(a, s);
+}
+
+}  // namespace hocf

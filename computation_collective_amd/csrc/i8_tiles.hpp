@@ -1,0 +1,198 @@
+// What the 8-bit products and their gradients share: the tiles of grouped rows,
+// LDS layouts of tile stages, and loads straight into them.
+#pragma once
+
+#include <algorithm>
+
+#include "i8.hpp"
+#include "mfma_tile.hpp"
+#include "publish.hpp"
+#include "sync.hpp"
+
+namespace hocf {
+
+#if defined(__HIP_DEVICE_COMPILE__)
+#define HOCF_LDS __attribute__((address_space(3)))
+#else
+#define HOCF_LDS
+#endif
+
+// A buffer resource over [base, base + bytes): loads past its end give zeros and
+// touch no memory (base and bytes wave-uniform, bytes < 2^31).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t ranged_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kRawBufferWord3);
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past the end of every resource
+
+// 16 bytes a lane from voff (per lane) + soff (wave-uniform) to 1 KB of LDS.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voff, uint32_t soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (HOCF_LDS void*)lds, 16, (int)voff, uniform((int)soff), 0, 0);
+#endif
+}
+
+// The memory operations before it are issued before those after it: a count of
+// operations still on their way says which they are.
+__device__ __forceinline__ void in_order() { __asm__ volatile("" ::: "memory"); }
+
+// vmcnt(N) and lgkmcnt(0), then the workgroup's barrier.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  static_assert(N <= 63, "vmcnt range");
+  in_order();
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+}
+
+// The bounds of group e within [0, T], whatever the offsets hold.
+__device__ __forceinline__ void group_bounds(const int64_t* offsets, int e, int64_t T, int64_t* lo, int64_t* hi) {
+  const int64_t a = offsets[e], b = offsets[e + 1];
+  *lo = a < 0 ? 0 : a > T ? T : a;
+  *hi = b < *lo ? *lo : b > T ? T : b;
+}
+
+struct RowTile {
+  int64_t row, end;  // first row, and the end of its group
+  int e, nt;         // expert and column tile; e = -1: none
+};
+
+// Workgroup b's tile of TM rows x one of `ntiles` columns.  The groups' row tiles stand one
+// after another; each XCD (workgroups are dealt to them in turn) takes one run of all tiles, in blocks of
+// up to 8 column tiles, row tile by row tile, so that what it reads together shares its L2.
+// Every wave finds the same.  Offsets that fall or leave [0, T] are reported by workgroup 0.
+template <int TM>
+__device__ __forceinline__ RowTile row_tile(const int64_t* offsets, int E, int64_t T, int ntiles, const SyncArgs& sync) {
+  const int lane = threadIdx.x & 63;
+  RowTile t{0, T, 0, 0};
+  int64_t total, skip = 0;
+  if (!offsets) {
+    total = (T + TM - 1) / TM;
+  } else {
+    total = 0;
+    bool bad = false;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      int n = 0;
+      if (e0 + lane < E) {
+        int64_t lo, hi;
+        group_bounds(offsets, e0 + lane, T, &lo, &hi);
+        bad |= lo != offsets[e0 + lane] || hi != offsets[e0 + lane + 1];
+        n = (int)((hi - lo + TM - 1) / TM);
+      }
+      for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d, 64);
+      total += n;
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && bad) report_status(sync, kErrBadIndex);
+  }
+  total = uniform64(total) * ntiles;
+  const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;  // (a row of the grid is whole turns of the XCDs)
+  const int q = (int)(b % kNumQueues);
+  const int64_t at = total * q / kNumQueues + b / kNumQueues;
+  if (at >= total * (q + 1) / kNumQueues) {
+    t.e = -1;
+    return t;
+  }
+  int64_t mtiles = total / ntiles;
+  if (offsets) {
+    // the group that holds tile `at`: tiles before it are skip * ntiles
+    bool found = false;
+    for (int e0 = 0; e0 < E && !found; e0 += 64) {
+      int64_t lo = 0, hi = 0;
+      if (e0 + lane < E) group_bounds(offsets, e0 + lane, T, &lo, &hi);
+      const int n = (int)((hi - lo + TM - 1) / TM);
+      int upto = n;
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(upto, d, 64);
+        if (lane >= d) upto += o;
+      }
+      const uint64_t m = __ballot((skip + upto) * (int64_t)ntiles > at);
+      if (m) {
+        const int l = __builtin_ctzll(m);
+        t.e = uniform(e0 + l);
+        skip = uniform64(skip + __shfl(upto, l, 64) - __shfl(n, l, 64));
+        mtiles = uniform(__shfl(n, l, 64));
+        t.row = uniform64(__shfl(lo, l, 64));
+        t.end = uniform64(__shfl(hi, l, 64));
+        found = true;
+      } else {
+        skip = uniform64(skip + __shfl(upto, 63, 64));
+      }
+    }
+  }
+  const int64_t j = at - skip * ntiles;
+  constexpr int kColBlock = 8;
+  const int64_t block = mtiles * kColBlock;
+  const int nb = (int)(j / block), width = min(kColBlock, ntiles - nb * kColBlock);
+  const int64_t in = j - nb * block;
+  t.row += in / width * TM;
+  t.nt = nb * kColBlock + (int)(in % width);
+  t.e = uniform(t.e);
+  t.nt = uniform(t.nt);
+  t.row = uniform64(t.row);
+  if (t.row >= t.end) t.e = -1;  // (offsets that overlap)
+  return t;
+}
+
+// Workgroups that cover the tiles of any offsets.
+inline dim3 row_tile_grid(int64_t T, int E, bool grouped, int TM, int ntiles) {
+  int64_t rows = (T + TM - 1) / TM;
+  if (grouped) rows = std::min(T, T / TM + E);  // (a group ends at most one tile that is not full)
+  const int64_t total = rows * ntiles;
+  const int64_t n = (total + kNumQueues - 1) / kNumQueues * kNumQueues, x = std::min<int64_t>(n, 1 << 20);
+  return dim3((uint32_t)x, (uint32_t)((n + x - 1) / x));
+}
+
+// A tile's results to memory, row by row: value(i, j, g) gives the four results of group g of
+// block (i, j) (row 32 i + lane mod 32, columns 32 j + 8 g + 4 (lane / 32) .. of the wave's
+// part) and finish(row, column, v) what becomes of four results of one row before they are
+// rounded.  A wave stages 32 rows in LDS (FIN: in fp32, else as they are stored) and stores
+// whole lines.  Rows < rows and columns < cols only (cols a multiple of 8).
+template <class Tile, int ODT, bool FIN, class V, class F>
+__device__ __forceinline__ void store_rows(char* dst, int64_t ld, int rows, int cols, char* const (&stages)[4], V value,
+                                           F finish) {
+  constexpr int SDT = FIN ? kF32 : ODT;
+  using L = PublishLayout<Tile, SDT>;
+  constexpr int OES = ODT == kBF16 ? 2 : 4, CE = 16 / L::ES;  // elements of a staged piece
+  constexpr int RPI = 64 / L::NCH, NIT = L::NCH / 2;
+  constexpr int BATCH = NIT < 8 ? NIT : 8;
+  const int wave = uniform(threadIdx.x >> 6), lane = opaque_lane();
+  const int wm = wave / Tile::WN, wn = wave % Tile::WN;
+  const int lr = lane & 31, half = lane >> 5, sr = lane / L::NCH, sc = lane % L::NCH;
+  const int tcol = wn * Tile::WTN + sc * CE;
+  __syncthreads();
+  char* area = L::area(stages, wave);
+#pragma unroll
+  for (int i = 0; i < Tile::FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < Tile::FN; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int byte = (32 * j + 8 * g + 4 * half) * L::ES;
+        char* p = area + L::at(lr, byte >> 4) + (byte & 15);
+        const floatx4 v = value(i, j, g);
+        if constexpr (SDT == kBF16) *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        else *reinterpret_cast<floatx4*>(p) = v;
+      }
+    // (LDS operations of one wave complete in order; the compiler must not reuse an earlier block's)
+    __asm__ volatile("" ::: "memory");
+#pragma unroll
+    for (int it0 = 0; it0 < NIT; it0 += BATCH) {
+      u32x4 v[BATCH];
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) v[b] = *reinterpret_cast<const u32x4*>(area + L::at((it0 + b) * RPI + sr, sc));
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int trow = wm * Tile::WTM + 32 * i + (it0 + b) * RPI + sr;
+        if (trow < rows && tcol < cols) {
+          char* p = dst + ((int64_t)trow * ld + tcol) * OES;
+          if constexpr (FIN) st4<ODT>(p, 0, finish(trow, tcol, __builtin_bit_cast(floatx4, v[b])));
+          else *reinterpret_cast<u32x4*>(p) = v[b];
+        }
+      }
+    }
+    __asm__ volatile("" ::: "memory");
+  }
+}
+
+}  // namespace hocf

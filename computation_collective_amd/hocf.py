@@ -42,6 +42,8 @@ EXPORTED = [
     "hocf_moe_route", "hocf_moe_route_workspace_bytes", "hocf_moe_route_bwd",
     "hocf_moe_slots", "hocf_moe_slots_workspace_bytes", "hocf_moe_combine", "hocf_moe_combine_bwd",
     "hocf_gemv_w4", "hocf_w4_pack",
+    "hocf_quant_i8", "hocf_dequant_i8", "hocf_weights_i8", "hocf_weights_i8_workspace_bytes",
+    "hocf_gemm_i8", "hocf_gemv_i8", "hocf_gemm_i8_dx", "hocf_gemm_i8_dw",
     "hocf_status_string", "hocf_last_error", "hocf_abi_version",
 ]
 
@@ -129,8 +131,18 @@ def lib():
         L.hocf_moe_combine_bwd.argtypes = [i64, i, i, i64, i, i, vp, vp, vp, vp, vp, vp, vp, S, vp]
         L.hocf_gemv_w4.argtypes = [i] * 8 + [vp] * 6 + [S, vp]
         L.hocf_w4_pack.argtypes = [i] * 4 + [vp] * 7
+        L.hocf_quant_i8.argtypes = [i64, i, i, vp, i64, i, vp, vp, vp, vp, S, vp]
+        L.hocf_dequant_i8.argtypes = [i64, i, i, vp, vp, vp, S, vp]
+        L.hocf_weights_i8.argtypes = [i, i, i, i, vp, vp, vp, S, vp]
+        L.hocf_weights_i8_workspace_bytes.argtypes = [i, i, i]
+        L.hocf_weights_i8_workspace_bytes.restype = sz
+        L.hocf_gemm_i8.argtypes = [i, i64, i, i, i] + [vp] * 6 + [S, vp]
+        L.hocf_gemv_i8.argtypes = [i] * 7 + [vp] * 6 + [S, vp]
+        L.hocf_gemm_i8_dx.argtypes = [i, i64, i, i, i] + [vp] * 7 + [S, vp]
+        L.hocf_gemm_i8_dw.argtypes = [i, i64, i, i, i] + [vp] * 5 + [S, vp]
         for f in ("hocf_moe_route", "hocf_moe_route_bwd", "hocf_moe_slots", "hocf_moe_combine", "hocf_moe_combine_bwd",
-                  "hocf_gemv_w4", "hocf_w4_pack"):
+                  "hocf_gemv_w4", "hocf_w4_pack", "hocf_quant_i8", "hocf_dequant_i8", "hocf_weights_i8", "hocf_gemm_i8",
+                  "hocf_gemv_i8", "hocf_gemm_i8_dx", "hocf_gemm_i8_dw"):
             getattr(L, f).restype = i
         for f in ("hocf_moe_route_workspace_bytes", "hocf_moe_slots_workspace_bytes"):
             getattr(L, f).restype = sz
@@ -370,6 +382,53 @@ def hocf_w4_pack(E, N, K, group, codes, scales, zeros, wq, scales_out, zeros_out
     """4-bit codes, scales and zero points in the layout hocf_gemv_w4 reads."""
     return lib().hocf_w4_pack(E, N, K, group, ptr(codes), ptr(scales), ptr(zeros), ptr(wq), ptr(scales_out),
                               ptr(zeros_out), _stream(stream))
+
+
+HOCF_ACT_NONE, HOCF_ACT_SILU = 0, 1
+
+
+def hocf_quant_i8(T, K, dt, x, ld, act, codes, scales, pre_codes, pre_scales, sync_, stream=None) -> int:
+    """Rows to 8-bit codes, one scale a row; every array a device buffer."""
+    return lib().hocf_quant_i8(T, K, dt, ptr(x), ld, act, ptr(codes), ptr(scales), ptr(pre_codes), ptr(pre_scales),
+                               ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_dequant_i8(T, K, out_dt, codes, scales, out, sync_, stream=None) -> int:
+    """What rows of codes stand for."""
+    return lib().hocf_dequant_i8(T, K, out_dt, ptr(codes), ptr(scales), ptr(out), ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_weights_i8_workspace_bytes(E, N, K) -> int:
+    return lib().hocf_weights_i8_workspace_bytes(E, N, K)
+
+
+def hocf_weights_i8(E, N, K, dt, W, wq, scales, sync_, stream=None) -> int:
+    """W [E][K][N] to 8-bit codes [E][N][K], one scale an output channel."""
+    return lib().hocf_weights_i8(E, N, K, dt, ptr(W), ptr(wq), ptr(scales), ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_gemm_i8(E, T, N, K, out_dt, xq, xs, wq, ws, offsets, out, sync_, stream=None) -> int:
+    """The experts' products in 8-bit integers, rows grouped by expert."""
+    return lib().hocf_gemm_i8(E, T, N, K, out_dt, ptr(xq), ptr(xs), ptr(wq), ptr(ws), ptr(offsets), ptr(out),
+                              ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_gemv_i8(R, rows_per_x, E, e0, N, K, out_dt, xq, xs, experts, wq, ws, out, sync_, stream=None) -> int:
+    """Products of a few token rows with their experts' 8-bit weights."""
+    return lib().hocf_gemv_i8(R, rows_per_x, E, e0, N, K, out_dt, ptr(xq), ptr(xs), ptr(experts), ptr(wq), ptr(ws),
+                              ptr(out), ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_gemm_i8_dx(E, T, N, K, out_dt, dy, wq, ws, offsets, pre_codes, pre_scales, dx, sync_, stream=None) -> int:
+    """The gradient of the product's rows (with pre_codes: of what SiLU was given)."""
+    return lib().hocf_gemm_i8_dx(E, T, N, K, out_dt, ptr(dy), ptr(wq), ptr(ws), ptr(offsets), ptr(pre_codes),
+                                 ptr(pre_scales), ptr(dx), ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_gemm_i8_dw(E, T, N, K, out_dt, xq, xs, dy, offsets, dw, sync_, stream=None) -> int:
+    """The gradient of the product's weights, from the rows' codes."""
+    return lib().hocf_gemm_i8_dw(E, T, N, K, out_dt, ptr(xq), ptr(xs), ptr(dy), ptr(offsets), ptr(dw),
+                                 ctypes.byref(sync_), _stream(stream))
 
 
 def bind(name, args, sync_):

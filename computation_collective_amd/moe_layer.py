@@ -1,6 +1,6 @@
 """A mixture-of-experts layer from the library's operators.
 
-Two forms, both on one GPU:
+Three parts, all on one GPU:
 
 * ``MoeLayer``, for training and prompts: P logical ranks of B tokens, E experts
   each.  route -> dispatch + up projection (hocf_a2a_gemm) -> SiLU -> down
@@ -10,7 +10,14 @@ Two forms, both on one GPU:
   the experts' rows, the weights (hocf_moe_combine_bwd) and the router's logits
   (hocf_moe_route_bwd).
 * ``MoeDecode``, for a decode step of a few tokens: route -> up and down
-  projections with 4-bit weights (hocf_gemv_w4) -> weighted sum.
+  projections with 4-bit weights (hocf_gemv_w4), or in 8-bit integers
+  (hocf_quant_i8, hocf_gemv_i8) -> weighted sum.
+* ``ExpertsI8``, one rank's experts on the rows that were dispatched to them, in
+  8-bit integers, with their backward pass: rows to codes (hocf_quant_i8) -> up
+  projection (hocf_gemm_i8) -> SiLU and codes again -> down projection; and from
+  the gradient of the results those of the rows (hocf_gemm_i8_dx) and of both
+  projections' weights (hocf_gemm_i8_dw).  What the backward pass keeps of the
+  activations is their codes, one byte a number.
 
 Buffers are allocated once; a step launches on the current stream.  The library
 is called through its Python binding; matrix products with the router and the
@@ -18,7 +25,7 @@ activation are plain torch operations.
 
     python -m computation_collective_amd.moe_layer
 
-runs both at the sizes of the dispatch and combine workloads and prints the
+runs them at the sizes of the dispatch and combine workloads and prints the
 time of a step.
 """
 
@@ -140,21 +147,106 @@ class MoeLayer:
                 self.route_bwd.dlogits.view(torch.bfloat16))
 
 
+class ExpertsI8:
+    """E experts of one rank on `rows` dispatched rows, w_up [E][K][H] and w_down [E][H][K] bf16:
+    y = silu(x w_up) w_down for the rows of each group, in 8-bit integers.
+
+    forward(x [rows][K] bf16, offsets [E + 1] int64 on the GPU) -> y [rows][K] bf16; group e is
+    rows [offsets[e], offsets[e + 1]), as the dispatch leaves them.  backward(dy) -> (dx
+    [rows][K] bf16, dw_up [E][K][H] fp32, dw_down [E][H][K] fp32), from the codes of the last
+    forward().  Rows of no group hold nothing in y and dx.  requantise() takes the weights'
+    codes anew, after an optimiser's step on w_up and w_down.  The results are the layer's own
+    buffers: the next step writes them again.  check() raises what an operator has reported
+    (offsets that fall or leave the rows); it waits for the stream."""
+
+    def __init__(self, E, rows, w_up, w_down):
+        K, H = w_up.shape[1], w_up.shape[2]
+        dev = w_up.device
+        self.x = torch.empty((rows, K), dtype=torch.bfloat16, device=dev)
+        self.dy = torch.empty_like(self.x)
+        self.offsets = torch.zeros(E + 1, dtype=torch.int64, device=dev)
+        self.w_up, self.w_down = bf.WeightsI8(E, H, K, w_up), bf.WeightsI8(E, K, H, w_down)
+        up, down = (self.w_up.wq, self.w_up.scales), (self.w_down.wq, self.w_down.scales)
+        self.x_codes = bf.QuantI8(rows, K, self.x)
+        x = (self.x_codes.codes, self.x_codes.scales)
+        self.up = bf.GemmI8(E, rows, H, K, *x, *up, offsets=self.offsets)
+        self.h_codes = bf.QuantI8(rows, H, self.up.out.view(torch.bfloat16), act=hocf.HOCF_ACT_SILU, keep=True)
+        h = (self.h_codes.codes, self.h_codes.scales)
+        self.down = bf.GemmI8(E, rows, K, H, *h, *down, offsets=self.offsets)
+        self.dw_down = bf.GemmI8Dw(E, rows, K, H, *h, self.dy, offsets=self.offsets)
+        self.dh = bf.GemmI8Dx(E, rows, K, H, self.dy, *down, offsets=self.offsets, pre_codes=self.h_codes.pre_codes,
+                              pre_scales=self.h_codes.pre_scales)
+        dh = self.dh.out.view(torch.bfloat16)
+        self.dw_up = bf.GemmI8Dw(E, rows, H, K, *x, dh, offsets=self.offsets)
+        self.dx = bf.GemmI8Dx(E, rows, H, K, dh, *up, offsets=self.offsets)
+        # rows of no group are not written: they hold zeros, never what the memory held before
+        for handle in (self.up, self.down, self.dh, self.dx):
+            handle.out.zero_()
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        for handle in (self.up, self.down, self.dw_down, self.dh, self.dw_up, self.dx):
+            handle.report_to(self.status)
+        self.requantise()
+
+    def requantise(self):
+        self.w_up.run()
+        self.w_down.run()
+
+    def forward(self, x, offsets):
+        self.x.copy_(x)
+        self.offsets.copy_(offsets)
+        return self.experts()
+
+    def experts(self):
+        """The forward pass of what self.x and self.offsets hold: can be captured into a graph."""
+        self.x_codes.run()
+        self.up.run()
+        self.h_codes.run()
+        self.down.run()
+        return self.down.out.view(torch.bfloat16)
+
+    def backward(self, dy):
+        self.dy.copy_(dy)
+        self.dw_down.run()
+        self.dh.run()
+        self.dw_up.run()
+        self.dx.run()
+        return self.dx.out.view(torch.bfloat16), self.dw_up.out, self.dw_down.out
+
+    def check(self):
+        word = int(self.status.item())
+        if word:
+            self.status.zero_()
+            raise RuntimeError(f"experts: {hocf.status_string(word)}")
+
+
 class MoeDecode:
     """A decode step of T tokens over E experts with 4-bit weights: `up` (K -> H) and
-    `down` (H -> K) as bf.w4_pack gives them, w_router [K][E] bf16.  step(x [T][K]
-    bf16) -> [T][K] bf16, the residual x included."""
+    `down` (H -> K) as bf.w4_pack gives them, w_router [K][E] bf16.  Or, with bits=8, in 8-bit
+    integers: `up` and `down` are (wq, scales) as bf.WeightsI8 makes them, and rows become
+    codes before each projection.  step(x [T][K] bf16) -> [T][K] bf16, the residual x
+    included."""
 
-    def __init__(self, T, E, topk, w_router, up, down, K, H, group, score=hocf.HOCF_SCORE_SOFTMAX, renorm=True):
+    def __init__(self, T, E, topk, w_router, up, down, K, H, group=128, score=hocf.HOCF_SCORE_SOFTMAX, renorm=True,
+                 bits=4):
+        if bits not in (4, 8):
+            raise ValueError(f"{bits}-bit weights: 4 or 8")
         dev = w_router.device
         self.w_router = w_router
         self.x = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
         self.logits = torch.empty((T, E), dtype=torch.bfloat16, device=dev)
         self.route = bf.MoeRoute(T, E, topk, self.logits, score=score, renorm=renorm)
         experts = self.route.experts.view(-1)
-        self.up = bf.GemvW4(T * topk, topk, E, 0, H, K, group, self.x, experts, *up)
-        self.hidden = self.up.out.view(torch.bfloat16)
-        self.down = bf.GemvW4(T * topk, 1, E, 0, K, H, group, self.hidden, experts, *down)
+        self.x_codes = self.h_codes = None
+        if bits == 8:
+            self.x_codes = bf.QuantI8(T, K, self.x)
+            self.up = bf.GemvI8(T * topk, topk, E, 0, H, K, self.x_codes.codes, self.x_codes.scales, experts, *up)
+            self.hidden = self.up.out.view(torch.bfloat16)
+            self.h_codes = bf.QuantI8(T * topk, H, self.hidden, act=hocf.HOCF_ACT_SILU)
+            self.down = bf.GemvI8(T * topk, 1, E, 0, K, H, self.h_codes.codes, self.h_codes.scales, experts, *down)
+        else:
+            self.up = bf.GemvW4(T * topk, topk, E, 0, H, K, group, self.x, experts, *up)
+            self.hidden = self.up.out.view(torch.bfloat16)
+            self.down = bf.GemvW4(T * topk, 1, E, 0, K, H, group, self.hidden, experts, *down)
         self.combine = bf.MoeCombine(T, topk, K, self.down.out, self.route.weights, add=self.x)
 
     def step(self, x):
@@ -165,8 +257,13 @@ class MoeDecode:
     def experts(self):
         """What follows the router's logits (self.logits, self.x): can be captured into a graph."""
         self.route.run()
+        if self.x_codes is not None:
+            self.x_codes.run()
         self.up.run()
-        silu_(self.hidden)
+        if self.h_codes is not None:
+            self.h_codes.run()
+        else:
+            silu_(self.hidden)
         self.down.run()
         self.combine.run()
         return self.combine.out.view(torch.bfloat16)
@@ -214,11 +311,29 @@ def main(argv=None):
     print(f"layer, {P} ranks x {B} tokens, top-{topk} of {P * E} experts {K} -> {H} -> {K}: "
           f"forward {_timed(lambda: layer.forward(X), a.steps):.3f} ms, "
           f"backward of combine and router {_timed(lambda: layer.backward(dout), a.steps):.3f} ms")
+    rows, w_up, w_down = 2 * pairs * P + E * 256, normal(E, K, H, std=0.02), normal(E, H, K, std=0.02)
+    experts = ExpertsI8(E, rows, w_up, w_down)
+    off = torch.linspace(0, pairs * P, E + 1, device=dev).long()
+    x, dy = normal(rows, K), normal(rows, K)
+    experts.backward(experts.forward(x, off))
+    experts.check()
+    print(f"one rank's {E} experts in 8-bit integers, {pairs * P} rows {K} -> {H} -> {K}: "
+          f"forward {_timed(lambda: experts.forward(x, off), a.steps):.3f} ms, "
+          f"backward {_timed(lambda: experts.backward(dy), a.steps):.3f} ms, "
+          f"weights to codes {_timed(experts.requantise, a.steps):.3f} ms")
     T, E, group = a.decode_tokens, P * E, 128
     decode = MoeDecode(T, E, topk, normal(K, E, std=K ** -0.5), random_w4(E, K, H, group, gen, dev),
                        random_w4(E, H, K, group, gen, dev), K, H, group)
     x = normal(T, K)
     print(f"decode, {T} tokens, top-{topk} of {E} experts, 4-bit weights: "
+          f"step {1e3 * _timed(lambda: decode.step(x), 20 * a.steps):.1f} us")
+    codes = []
+    for w in (normal(E, K, H, std=0.02), normal(E, H, K, std=0.02)):
+        handle = bf.WeightsI8(E, w.shape[2], w.shape[1], w)
+        handle.run()
+        codes.append((handle.wq, handle.scales))
+    decode = MoeDecode(T, E, topk, normal(K, E, std=K ** -0.5), *codes, K, H, bits=8)
+    print(f"decode, {T} tokens, top-{topk} of {E} experts, 8-bit integers: "
           f"step {1e3 * _timed(lambda: decode.step(x), 20 * a.steps):.1f} us")
 
 

@@ -47,6 +47,14 @@
  *                    products of a few token rows with their experts' 4-bit
  *                    weights (the decode form of the experts' GEMM), and the
  *                    weights' layout for it
+ *   hocf_quant_i8, hocf_dequant_i8, hocf_weights_i8
+ *                    activations and weights to 8-bit codes, and back
+ *   hocf_gemm_i8, hocf_gemv_i8
+ *                    the experts' products in 8-bit integers: for rows
+ *                    grouped by expert, and for a few rows of a decode step
+ *   hocf_gemm_i8_dx, hocf_gemm_i8_dw
+ *                    their gradients, from the codes that the forward pass
+ *                    kept
  *
  * The method (SC24 abstract; mKernel, section on persistent kernels and
  * tile/chunk overlap): the workgroups of one kernel each finish an output
@@ -105,14 +113,15 @@
  * call) caps it further, e.g. to leave CUs to other work or to have each
  * workgroup take many items; every operator completes with any grid of one
  * or more workgroups.  hocf_moe_slots (one or two kernels), hocf_moe_combine
- * and its backward pass, hocf_gemv_w4 and hocf_w4_pack launch ordinary grids,
- * which the variable does not cap.
+ * and its backward pass, hocf_gemv_w4, hocf_w4_pack and the 8-bit operators
+ * (hocf_weights_i8: two kernels, the others: one) launch ordinary grids, which
+ * the variable does not cap.
  *
  * Workspace.  Scheduler counters.  The caller allocates at least the size
  * the matching *_workspace_bytes() query returns, zeroes it ONCE, and may
  * then reuse it for any number of calls: every call leaves it zeroed again,
- * except those of hocf_a2a_gemm* and hocf_moe_slots, which need no zeroing and
- * do not leave it zeroed (zero it before another operator takes it).
+ * except those of hocf_a2a_gemm*, hocf_moe_slots and hocf_weights_i8, which need
+ * no zeroing and do not leave it zeroed (zero it before another operator takes it).
  * Calls that may run concurrently need separate workspaces.
  */
 #ifndef HOCF_H
@@ -702,6 +711,125 @@ hocf_status hocf_gemv_w4(int R, int rows_per_x, int E, int e0, int N, int K, int
  * ---------------------------------------------------------------------- */
 hocf_status hocf_w4_pack(int E, int N, int K, int group, const uint8_t* codes, const void* scales, const void* zeros,
                          uint32_t* wq, void* scales_out, void* zeros_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rows of activations to 8-bit codes, one scale a row.
+ *
+ *   a = act(x)
+ *   scales[t]   = max(largest |a[t]| / 127, 2^-126)   (the quotient rounded to fp32)
+ *   codes[t][k] = a[t][k] / scales[t], to the nearest whole number, halves to the even one
+ * of the real quotient, so |codes| <= 127.  What a code stands for is
+ * codes * scales.  A row with an infinity or a NaN gets the scale NaN and
+ * codes 0: everything computed from it is NaN.
+ * The codes serve the forward product (hocf_gemm_i8, hocf_gemv_i8) and, kept,
+ * the backward pass in place of the activations (hocf_gemm_i8_dw; with
+ * pre_codes, the activation function's part of hocf_gemm_i8_dx).
+ *
+ *   x        [T][ld] dt, the first K of each row (K <= ld <= 2^24; rows start on 16 bytes)
+ *   act      HOCF_ACT_NONE, or HOCF_ACT_SILU: a = x / (1 + exp(-x)) rounded to dt
+ *            (dt F32: computed in 64 bits; BF16: in 32, its rounding may go the other
+ *            way within 2^-20 of a border)
+ *   codes    [T][K] int8          scales  [T] fp32
+ *   pre_codes, pre_scales   NULL, or (with an activation) the same for x itself
+ * Supported: dt F32 or BF16; K a multiple of 16 up to 65536; 0 <= T < 2^31.
+ * ---------------------------------------------------------------------- */
+typedef enum hocf_act HOCF_ENUM_INT { HOCF_ACT_NONE = 0, HOCF_ACT_SILU = 1 } hocf_act;
+hocf_status hocf_quant_i8(int64_t T, int K, hocf_dtype dt, const void* x, int64_t ld, hocf_act act, int8_t* codes,
+                          float* scales, int8_t* pre_codes, float* pre_scales, const hocf_sync* sync, void* stream);
+
+/* Reading back: out[t][k] = codes[t][k] * scales[t], rounded to fp32 and to out_dt. */
+hocf_status hocf_dequant_i8(int64_t T, int K, hocf_dtype out_dt, const int8_t* codes, const float* scales, void* out,
+                            const hocf_sync* sync, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Weights to 8-bit codes, one scale for each output channel (when they are
+ * loaded, or after an optimiser's step).
+ *
+ *   W [E][K][N] dt  ->  wq [E][N][K] int8, scales [E][N] fp32
+ * Column n of W_e becomes row n of wq_e, by the rule of hocf_quant_i8 (a
+ * column with an infinity or a NaN gets the scale NaN).  So
+ * hocf_dequant_i8(E * N, K, ...) reads the transposed weights back.  The workspace
+ * needs no zeroing, and is not left zeroed.
+ * Supported: dt F32 or BF16; 1 <= E <= 1024; N a multiple of 8 and K of 16, up
+ * to 65536.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_weights_i8(int E, int N, int K, hocf_dtype dt, const void* W, int8_t* wq, float* scales,
+                            const hocf_sync* sync, void* stream);
+size_t hocf_weights_i8_workspace_bytes(int E, int N, int K);
+
+/* ------------------------------------------------------------------------
+ * The experts' products in 8-bit integers, rows grouped by expert.
+ *
+ *   out[r][n] = xs[r] * ws[e][n] * sum_k xq[r][k] * wq[e][n][k]
+ * for the rows r of expert e's group, [offsets[e], offsets[e + 1]).  The sum is
+ * exact (32-bit integers); it and the two factors are rounded to fp32, the
+ * result to out_dt.  Groups may have any number of rows, also none; rows
+ * before the first group and behind the last are not read, and their rows of
+ * out are left as they were.
+ *
+ *   xq  [T][K] int8   xs [T] fp32      wq [E][N][K] int8   ws [E][N] fp32
+ *   offsets  [E + 1] int64 (device), rising from 0 or more to T or less; or NULL
+ *            (E = 1): every row.  As hocf_a2a_gemm writes them.
+ *   out [T][N] out_dt
+ * Offsets that fall, or leave [0, T], are taken as the nearest that do not, and
+ * HOCF_ERR_BAD_INDEX goes to the status word.
+ * Supported: out_dt F32 or BF16; 1 <= E <= 1024; N a multiple of 8 and K of 16,
+ * up to 65536; 0 <= T < 2^31.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_gemm_i8(int E, int64_t T, int N, int K, hocf_dtype out_dt, const int8_t* xq, const float* xs,
+                         const int8_t* wq, const float* ws, const int64_t* offsets, void* out, const hocf_sync* sync,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products of a few token rows with their experts' 8-bit weights.
+ *
+ *   out[r] = the product above of row r / rows_per_x and expert experts[r] - e0,  r = 0 .. R-1
+ * as hocf_gemv_w4 takes its rows: R = T * topk pairs of a decode step, rows_per_x =
+ * topk for the up projection, 1 for the down projection; a row whose expert is
+ * not one of this rank's e0 .. e0+E-1 gets zeros.  The same bits as hocf_gemm_i8 gives.
+ *
+ *   xq       [R / rows_per_x][K] int8     xs [R / rows_per_x] fp32
+ *   experts  [R] int32, or NULL: one matrix for every row (E = 1)
+ *   wq       [E][N][K] int8               ws [E][N] fp32
+ *   out      [R][N] out_dt
+ * Supported: 0 <= R <= 1024 a multiple of rows_per_x; else as hocf_gemm_i8.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_gemv_i8(int R, int rows_per_x, int E, int e0, int N, int K, hocf_dtype out_dt, const int8_t* xq,
+                         const float* xs, const int32_t* experts, const int8_t* wq, const float* ws, void* out,
+                         const hocf_sync* sync, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' products in 8-bit integers, backward: the rows' gradient.
+ *
+ *   dx[r][k] = sum_n dy[r][n] * bf16(wq[e][n][k] * ws[e][n])
+ * in fp32, for the rows of expert e's group (the codes' rounding counts as the
+ * identity).  With pre_codes, the rows came through SiLU from h, which
+ * was kept in codes, and the result is h's gradient:
+ *   dx[r][k] *= p (1 + h (1 - p)),  p = 1 / (1 + exp(-h)),  h = bf16(pre_codes[r][k] * pre_scales[r])
+ *
+ *   dy  [T][N] bf16    wq, ws, offsets  as hocf_gemm_i8 takes them
+ *   pre_codes, pre_scales  NULL, or [T][K] int8 and [T] fp32 as hocf_quant_i8 keeps them
+ *   dx  [T][K] out_dt (rows of no group: left as they were)
+ * Other arguments, offsets and support as for hocf_gemm_i8.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_gemm_i8_dx(int E, int64_t T, int N, int K, hocf_dtype out_dt, const void* dy, const int8_t* wq,
+                            const float* ws, const int64_t* offsets, const int8_t* pre_codes, const float* pre_scales,
+                            void* dx, const hocf_sync* sync, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' products in 8-bit integers, backward: the weights' gradient,
+ * from the rows as they were kept.
+ *
+ *   dw[e][k][n] = sum over the rows r of expert e's group of bf16(xq[r][k] * xs[r]) * dy[r][n]
+ * in fp32, in a fixed order.  A group without rows has the gradient zero.  (The
+ * gradient is of W as hocf_weights_i8 takes it.)
+ *
+ *   xq [T][K] int8   xs [T] fp32   dy [T][N] bf16   offsets  as for hocf_gemm_i8
+ *   dw [E][K][N] out_dt
+ * Other arguments, offsets and support as for hocf_gemm_i8.
+ * ---------------------------------------------------------------------- */
+hocf_status hocf_gemm_i8_dw(int E, int64_t T, int N, int K, hocf_dtype out_dt, const int8_t* xq, const float* xs,
+                            const void* dy, const int64_t* offsets, void* dw, const hocf_sync* sync, void* stream);
 
 /* ---------------------------------------------------------------------- */
 const char* hocf_status_string(hocf_status s); /* static string, never NULL */
