@@ -792,7 +792,7 @@ class GemmI8Dw(_Moe):
         self.xq, self.xs, self.dy, self.offsets = xq, xs, dy, offsets
         self.out = torch.empty((E, K, N), dtype=tdtype(out_dt), device=xq.device)
         args = (E, T, N, K, out_dt, xq.data_ptr(), xs.data_ptr(), dy.data_ptr(), hocf.ptr(offsets), self.out.data_ptr())
-        self._bind("hocf_gemm_i8_dw", args, xq.device)
+        self._bind("hocf_gemm_i8_dw", args, xq.device, hocf.hocf_gemm_i8_dw_workspace_bytes(E, T, N, K))
 
     def poison(self):
         nan_fill(self.out)

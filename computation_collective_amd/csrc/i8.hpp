@@ -2,6 +2,8 @@
 // the arguments, the i8_*.hip units launch).
 #pragma once
 
+#include <algorithm>
+
 #include "internal.hpp"
 
 namespace hocf {
@@ -73,10 +75,19 @@ struct GradI8Args {
   const int8_t* pre;       // dx: [T][K] or NULL
   const float* pre_s;      // dx: [T] or NULL
   void* out;               // dx: [T][K]; dw: [E][K][N], out_dt
+  float* part;             // dw: workspace, [splits][E][K][N] where there are more than one
   int64_t T;
   int E, N, K, out_dt;
   SyncArgs sync;
 };
+
+// Parts that dw's sums over rows are taken in: as many as give each of 256 CUs a 256 x 256
+// tile, where the tiles alone would leave half of them idle and each part is long enough to be worth its
+// sums' way through memory.
+inline int dw_splits(int E, int64_t T, int N, int K) {
+  const int64_t tiles = (int64_t)E * ((K + 255) / 256) * ((N + 255) / 256);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, T / E / 1024));
+}
 
 int launch_quant_i8(const QuantI8Args& a, hipStream_t s);
 int launch_dequant_i8(const DequantI8Args& a, hipStream_t s);

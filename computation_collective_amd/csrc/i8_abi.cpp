@@ -234,11 +234,19 @@ hocf_status hocf_gemm_i8_dx(int E, int64_t T, int N, int K, hocf_dtype out_dt, c
   return launched(launch_gemm_i8_dx(a, static_cast<hipStream_t>(stream)), op);
 }
 
+size_t hocf_gemm_i8_dw_workspace_bytes(int E, int64_t T, int N, int K) {
+  if (E < 1 || T < 1 || N < 1 || K < 1 || E > kI8MaxExperts || T > kMaxRows || N > kI8MaxDim || K > kI8MaxDim) return 0;
+  const int splits = dw_splits(E, T, N, K);
+  return splits > 1 ? (size_t)splits * E * K * N * 4 : 0;
+}
+
 hocf_status hocf_gemm_i8_dw(int E, int64_t T, int N, int K, hocf_dtype out_dt, const int8_t* xq, const float* xs,
                             const void* dy, const int64_t* offsets, void* dw, const hocf_sync* sync, void* stream) {
   const char* op = "gemm_i8_dw";
   hocf_status st = check_grouped(op, E, T, N, K, out_dt, offsets, sync);
   if (st != HOCF_OK) return st;
+  const size_t need = hocf_gemm_i8_dw_workspace_bytes(E, T, N, K);
+  if ((st = check_sync(sync, need)) != HOCF_OK) return st;
   if ((T && (!xq || !xs || !dy)) || !dw) return null_tensor(op);
   if ((st = check_aligned(op, xq, xs, dy, offsets, dw)) != HOCF_OK) return st;
   {
@@ -248,13 +256,14 @@ hocf_status hocf_gemm_i8_dw(int E, int64_t T, int N, int K, hocf_dtype out_dt, c
     rg.in("dy", 0, dy, T * N * 2);
     rg.in("offsets", 0, offsets, (int64_t)(E + 1) * 8);
     rg.out("dw", 0, dw, (int64_t)E * K * N * dt_bytes(out_dt));
-    add_sync(rg, sync, 0);
+    add_sync(rg, sync, need);
     if ((st = rg.check(op)) != HOCF_OK) return st;
   }
   GradI8Args a{};
   if ((st = to_sync_args(sync, &a.sync)) != HOCF_OK) return st;
   a.dy = static_cast<const uint16_t*>(dy);
   a.q = xq; a.s = xs; a.offsets = offsets; a.out = dw;
+  a.part = static_cast<float*>(sync->workspace);
   a.T = T; a.E = E; a.N = N; a.K = K; a.out_dt = out_dt;
   return launched(launch_gemm_i8_dw(a, static_cast<hipStream_t>(stream)), op);
 }

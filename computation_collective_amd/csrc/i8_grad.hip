@@ -16,30 +16,51 @@ namespace hocf {
 
 // x / (1 + exp(-x)), its derivative.
 __device__ __forceinline__ float silu_slope(float h) {
-  const float p = 1.0f / (1.0f + __expf(-h));  // (h = -inf: 0, and its slope below NaN, as the formula's)
+  const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(h * -1.44269504f));
   return p * fmaf(h, 1.0f - p, 1.0f);
 }
 
+// Order within a quarter of a step: NM matrix instructions, ND LDS reads soon behind the
+// first of them, NV vector instructions and NW LDS writes spread over all.
+template <int NM, int ND, int NV, int NW, int X = 0>
+__device__ __forceinline__ void mix() {
+  if constexpr (X < NM) {
+    constexpr int dpm = (ND + NM - 1) / NM, d = ND - X * dpm < dpm ? (ND - X * dpm > 0 ? ND - X * dpm : 0) : dpm;
+    constexpr int v = NV * (X + 1) / NM - NV * X / NM, w = NW * (X + 1) / NM - NW * X / NM;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
+    if constexpr (w > 0) __builtin_amdgcn_sched_group_barrier(0x200, w, 0);
+    mix<NM, ND, NV, NW, X + 1>();
+  } else {
+    __builtin_amdgcn_sched_barrier(0);  // (conversions stay in their quarter)
+  }
+}
+
 // A TR x TC tile (rows x columns of the result) of four waves, summed over steps of 64.
-// DW: rows are codes, columns dy, both with the summed index outermost.
-// Else: rows are dy with the summed index innermost, columns codes with it outermost.
+// DW: rows are codes, columns dy.  Else: rows are dy, columns codes.
 //
-// LDS of an operand with the summed index c outermost: rows of its W numbers, 16-byte pieces
-// at piece ^ 4 (c mod 4) (W = 64: ^ 4 (c / 2 mod 2)), so that the transposing read's four rows
-// x 64 bytes touch every bank once; innermost: as rows of 128 bytes, piece ^ (row / 2 mod 8).
+// LDS: a row is one row or column of the tile, 128 bytes of the summed index c in eight
+// 16-byte pieces.  dx's dy comes like that, piece p at p ^ (row / 2 mod 8).  Codes have c
+// outermost in memory: a thread takes a block of 8 c x 8 columns, whose numbers
+// it turns on their way (piece p of column n at p ^ (n / 2 mod 8) ^ (n / 8 mod 8): the writes
+// of eight columns apart and the reads of neighbours both touch every bank once).  dw's dy
+// has c outermost too and goes straight to LDS as it is, rows of c, pieces at p ^ 4 (c mod 4)
+// (64 columns: ^ 4 (c / 2 mod 2)); the transposing read turns it, four rows x 64 bytes at a time.
 template <bool DW, int TR, int TC>
 struct TileGrad {
   static constexpr int TM = TR, TN = TC, WM = 2, WN = 2, NW = 4, NT = 256;
   static constexpr int WTM = TM / WM, WTN = TN / WN, FM = WTM / 32, FN = WTN / 32;
-  static constexpr int BK = 64, NST = 2;
-  static constexpr int SMEM_BYTES = (TM + TN) * BK * 2;          // one stage: rows, then columns
+  // Two stages of two arrays, 2 S for dy and 2 S + 1 for codes: with one array for both, the
+  // compiler would wait for dy's loads before it lets the codes' writes go (dx 177 us, not 130).
+  static constexpr int BK = 64, NST = 4;
   static constexpr int QW = DW ? TR : TC, PW = DW ? TC : TR;     // codes and dy of a step
-  static constexpr int Q_AT = DW ? 0 : TM * BK * 2, P_AT = DW ? TM * BK * 2 : 0;
+  static constexpr int SMEM_BYTES = TM * BK * 2;
+  static_assert(TM == TN, "arrays of one size");
   static constexpr int P_LD = PW * BK * 2 / 1024 / NW;           // 1 KB loads of a wave and step
-  static constexpr int QR = 512 / QW, Q_LD = 16 / QR;            // rows of codes of one load; loads of a wave and step
-  static_assert(Q_LD >= 1 && P_LD >= 1, "four waves");
-
-  __device__ static __forceinline__ int turn(int W, int c) { return W >= 128 ? 4 * (c & 3) : 4 * ((c >> 1) & 1); }
+  static constexpr int QR = QW == 64 ? 4 : 8, QC = QW * BK / NT / QR;  // a thread's block of codes
+  static constexpr int Q_LD = QR + QR / 4;                       // its loads: rows of codes, and their scales
+  static_assert((QC == 8 || QC == 4) && P_LD >= 1, "four waves");
 
   struct Operands {
     const uint16_t* dy;  // dx: the tile's first row; dw: the group's first row
@@ -62,13 +83,14 @@ struct TileGrad {
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
     // dy: this lane's part of a 1 KB load
+    constexpr int RP = 512 / PW, PC = PW / 8;  // dw: rows of one load; pieces of a row
+    auto turn = [](int c) { return PW >= 128 ? 4 * (c & 3) : 4 * ((c >> 1) & 1); };
     uint32_t poff;
     int ppiece = 0;
     if constexpr (DW) {
-      constexpr int RP = 512 / PW, PC = PW / 8;  // rows of one load; pieces of a row
-      const int c = wave * RP + lane / PC;       // (loads are 4 RP rows apart, which does not move the pieces)
+      const int c = wave * RP + lane / PC;     // (loads are 4 RP rows apart, which does not move the pieces)
       static_assert((NW * RP) % 4 == 0, "pieces stay");
-      poff = (uint32_t)c * (uint32_t)o.N * 2u + (uint32_t)(o.p0 * 2) + (((lane % PC) ^ turn(PW, c)) << 4);
+      poff = (uint32_t)c * (uint32_t)o.N * 2u + (uint32_t)(o.p0 * 2) + (((lane % PC) ^ turn(c)) << 4);
     } else {
       const int row = wave * 8 + (lane >> 3);
       ppiece = ((lane & 7) ^ ((row >> 1) & 7)) << 4;
@@ -77,74 +99,91 @@ struct TileGrad {
     const __amdgpu_buffer_rsrc_t rp0 = ranged_rsrc(o.dy, DW ? 0 : (uint32_t)o.rows * (uint32_t)o.N * 2u);
     auto load_p = [&](char* st, int ks) {
       if constexpr (DW) {
-        constexpr int RP = 512 / PW;
-        const int64_t c0 = (int64_t)ks * BK, left = min((int64_t)BK, max(o.C - c0, (int64_t)0));
-        const __amdgpu_buffer_rsrc_t r = ranged_rsrc(o.dy + min(c0, o.C) * o.N, (uint32_t)left * (uint32_t)o.N * 2u);
+        const int64_t c0 = min((int64_t)ks * BK, o.C);
+        const uint32_t left = (uint32_t)min((int64_t)BK, o.C - c0);
+        const __amdgpu_buffer_rsrc_t r = ranged_rsrc(o.dy + c0 * o.N, left * (uint32_t)o.N * 2u);
 #pragma unroll
         for (int t = 0; t < P_LD; ++t)
-          load_lds16(r, st + P_AT + (t * NW + wave) * 1024, poff, (uint32_t)(t * NW * RP) * (uint32_t)o.N * 2u);
+          load_lds16(r, st + (t * NW + wave) * 1024, poff, (uint32_t)(t * NW * RP) * (uint32_t)o.N * 2u);
       } else {
         const uint32_t voff = (int64_t)ks * BK * 2 + ppiece < (int64_t)o.N * 2 ? poff : kNowhere;
 #pragma unroll
         for (int t = 0; t < P_LD; ++t)
-          load_lds16(rp0, st + P_AT + (t * NW + wave) * 1024, voff,
+          load_lds16(rp0, st + (t * NW + wave) * 1024, voff,
                      (uint32_t)ks * (BK * 2) + (uint32_t)(t * 32) * (uint32_t)o.N * 2u);
       }
     };
-    // codes: wave w's rows 16 w .. of a step, QR of them a load, eight codes a lane; and the rows' scales, lane i's row 16 w + i
-    const int qrow = lane / (QW / 8), qpiece = lane % (QW / 8);
-    const uint32_t qoff = (uint32_t)(wave * 16 + qrow) * (uint32_t)o.K + o.q0 + qpiece * 8;
+    // codes: QR rows x QC columns a thread, and the rows' scales
+    const int tid = wave * 64 + lane, qcol = tid % (QW / QC) * QC, qrow = tid / (QW / QC) * QR;
+    const uint32_t qoff = (uint32_t)qrow * (uint32_t)o.K + (uint32_t)(o.q0 + qcol);
     struct Codes {
-      u32x2 w[Q_LD];
-      float s;
+      uint32_t w[QR][QC / 4];
+      floatx4 s[QR / 4];
     };
     auto load_q = [&](Codes& r, int ks) {
       const int64_t c0 = min((int64_t)ks * BK, o.C);
       const uint32_t left = (uint32_t)min((int64_t)BK, o.C - c0);
-      const __amdgpu_buffer_rsrc_t rq = ranged_rsrc(o.q + c0 * o.K, left * (uint32_t)o.K);
+      const __amdgpu_buffer_rsrc_t rq = ranged_rsrc(o.q + c0 * o.K, left * (uint32_t)o.K), rs = ranged_rsrc(o.s + c0, left * 4u);
 #pragma unroll
-      for (int t = 0; t < Q_LD; ++t)
-        r.w[t] = __builtin_amdgcn_raw_buffer_load_b64(rq, (int)qoff, uniform((int)(t * QR * (uint32_t)o.K)), 0);
-      r.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ranged_rsrc(o.s + c0, left * 4u),
-                                                                           (wave * 16 + (lane & 15)) * 4, 0, 0));
+      for (int t = 0; t < QR / 4; ++t)
+        r.s[t] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, qrow * 4 + t * 16, 0, 0));
+#pragma unroll
+      for (int t = 0; t < QR; ++t) {
+        const int soff = uniform((int)(t * (uint32_t)o.K));
+        if constexpr (QC == 8) {
+          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rq, (int)qoff, soff, 0);
+          r.w[t][0] = v[0];
+          r.w[t][QC / 4 - 1] = v[1];
+        } else {
+          r.w[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rq, (int)qoff, soff, 0);
+        }
+      }
     };
-    auto put_q = [&](const Codes& r, char* st, int t) {
-      const int c = wave * 16 + t * QR + qrow;
-      const float s = __shfl(r.s, t * QR + qrow, 64);
-      float v[8];
+    // column i of the block
+    const int qpiece = qrow >> 3, qhalf = (qrow & 4) * 2;
+    auto put_q = [&](const Codes& r, char* st, int i) {
+      const int n = qcol + i;
+      float v[QR];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)(r.w[t][i / 4] >> (8 * (i & 3))) * s;
-      *reinterpret_cast<u32x4*>(st + Q_AT + c * (QW * 2) + ((qpiece ^ turn(QW, c)) << 4)) =
-          u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      for (int t = 0; t < QR; ++t) v[t] = (float)(int8_t)(r.w[t][i / 4] >> (8 * (i & 3))) * r.s[t / 4][t & 3];
+      char* p = st + n * (BK * 2) + ((qpiece ^ ((n >> 1) & 7) ^ ((n >> 3) & 7)) << 4) + qhalf;
+      if constexpr (QR == 8)
+        *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[QR - 4], v[QR - 3]),
+                                             pack_bf16x2(v[QR - 2], v[QR - 1])};
+      else
+        *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     };
 
     typedef short short4v __attribute__((ext_vector_type(4)));
     typedef short short8v __attribute__((ext_vector_type(8)));
-    // fragments of quarter kk of a step: summed index innermost
-    const int m = lane & 31, inner = (wm * WTM + m) * (BK * 2) + (((lane >> 5) ^ ((m >> 1) & 7)) << 4);
-    auto frag_inner = [&](const char* st, int kk, int i) {
-      return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(st + (inner ^ (kk << 5)) + i * 32 * BK * 2));
+    // fragments of quarter kk of a step: pieces 2 kk + lane / 32 of rows lane mod 32 of each block
+    const int m = lane & 31, half = lane >> 5;
+    const int p_at = (wm * WTM + m) * (BK * 2) + ((half ^ ((m >> 1) & 7)) << 4);                // (dx)
+    const int qw0 = (DW ? wm * WTM : wn * WTN) + m;
+    const int q_at = qw0 * (BK * 2) + ((half ^ ((qw0 >> 1) & 7) ^ ((qw0 >> 3) & 7)) << 4);
+    auto frag_p = [&](const char* st, int kk, int i) {
+      return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(st + (p_at ^ (kk << 5)) + i * 32 * BK * 2));
     };
-    // outermost: 16 lanes read four rows c x 16 numbers, and lane l gets number l of the four rows
-    const int G = lane >> 4, s16 = lane & 15, crow = (G >> 1) * 8 + (s16 >> 2);
-    auto outer_at = [&](int W, int w0) {
-      const int n = w0 + (G & 1) * 16 + 4 * (s16 & 3);
-      return crow * (W * 2) + (((n >> 3) ^ turn(W, crow)) << 4) + (n & 7) * 2;
+    auto frag_q = [&](const char* st, int kk, int i) {  // (32 columns on: n / 8 mod 8 changes by 4)
+      return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(st + (q_at ^ (kk << 5) ^ ((i & 1) << 6)) + i * 32 * BK * 2));
     };
-    auto frag_outer = [&](const char* st, int at, int W, int kk, int j) {
+    // dw's dy: 16 lanes read four rows c x 16 numbers, and lane l gets number l of the four rows
+    const int G = lane >> 4, s16 = lane & 15, crow = (G >> 1) * 8 + (s16 >> 2), pn = wn * WTN + (G & 1) * 16 + 4 * (s16 & 3);
+    const int t_at = crow * (PW * 2) + (((pn >> 3) ^ turn(crow)) << 4) + (pn & 7) * 2;
+    auto frag_t = [&](const char* st, int kk, int j) {
       short4v h[2];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
         h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (HOCF_LDS short4v*)(st + (at ^ (j << 6)) + (kk * 16 + 4 * hh) * (W * 2)));
+            (HOCF_LDS short4v*)(st + (t_at ^ (j << 6)) + (kk * 16 + 4 * hh) * (PW * 2)));
       return __builtin_bit_cast(bf16x8, short8v{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]});
     };
-    const int rat = outer_at(TM, wm * WTM), cat = outer_at(TN, wn * WTN);
-    auto frags = [&](const char* st, int kk, bf16x8 (&a)[FM], bf16x8 (&b)[FN]) {
+    auto frags = [&](int S, int kk, bf16x8 (&a)[FM], bf16x8 (&b)[FN]) {
+      const char *p = stages[2 * S], *q = stages[2 * S + 1];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) a[i] = DW ? frag_outer(st, rat, TM, kk, i) : frag_inner(st, kk, i);
+      for (int i = 0; i < FM; ++i) a[i] = DW ? frag_q(q, kk, i) : frag_p(p, kk, i);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) b[j] = frag_outer(st + TM * BK * 2, cat, TN, kk, j);
+      for (int j = 0; j < FN; ++j) b[j] = DW ? frag_t(p, kk, j) : frag_q(q, kk, j);
     };
     auto mfmas = [&](const bf16x8 (&a)[FM], const bf16x8 (&b)[FN]) {
 #pragma unroll
@@ -153,7 +192,7 @@ struct TileGrad {
         for (int j = 0; j < FN; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
     };
-    constexpr int NM = FM * FN, ND = (DW ? 2 : 1) * FM + 2 * FN;
+    constexpr int NM = FM * FN, ND = FM + (DW ? 2 : 1) * FN;
     bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
     Codes qa, qb;
 
@@ -165,37 +204,42 @@ struct TileGrad {
     in_order();
     load_p(stages[0], 0);
 #pragma unroll
-    for (int t = 0; t < Q_LD; ++t) put_q(qa, stages[0], t);
+    for (int i = 0; i < QC; ++i) put_q(qa, stages[1], i);
     wait_barrier<0>();
-    load_p(stages[1], 1);
+    load_p(stages[2], 1);
     in_order();
     load_q(qa, 2);
-    frags(stages[0], 0, a0, b0);
+    frags(0, 0, a0, b0);
     // Stage S holds step ks, whose quarters are multiplied in turn, the next one's fragments on
     // their way; meanwhile step ks + 1's codes become the other stage's numbers.  The barrier before the last quarter
     // has the other stage complete (all but step ks + 2's codes have arrived) and frees stage S,
     // for step ks + 2's dy, and the registers of codes, for step ks + 3's.
-    constexpr int T1 = (Q_LD + 2) / 3, T2 = (2 * Q_LD + 2) / 3;
+    constexpr int I1 = (QC + 2) / 3, I2 = (2 * QC + 2) / 3;
     auto step = [&](auto s_c, int ks, Codes& codes) {
       constexpr int S = decltype(s_c)::value;
-      frags(stages[S], 1, a1, b1);
+      frags(S, 1, a1, b1);
 #pragma unroll
-      for (int t = 0; t < T1; ++t) put_q(codes, stages[S ^ 1], t);
+      for (int i = 0; i < I1; ++i) put_q(codes, stages[2 * (S ^ 1) + 1], i);
       mfmas(a0, b0);
-      frags(stages[S], 2, a0, b0);
+      mix<NM, ND, I1 * QR * 5 / 2, I1>();
+      frags(S, 2, a0, b0);
 #pragma unroll
-      for (int t = T1; t < T2; ++t) put_q(codes, stages[S ^ 1], t);
+      for (int i = I1; i < I2; ++i) put_q(codes, stages[2 * (S ^ 1) + 1], i);
       mfmas(a1, b1);
-      frags(stages[S], 3, a1, b1);
+      mix<NM, ND, (I2 - I1) * QR * 5 / 2, I2 - I1>();
+      frags(S, 3, a1, b1);
 #pragma unroll
-      for (int t = T2; t < Q_LD; ++t) put_q(codes, stages[S ^ 1], t);
+      for (int i = I2; i < QC; ++i) put_q(codes, stages[2 * (S ^ 1) + 1], i);
       mfmas(a0, b0);
-      wait_barrier<Q_LD + 1>();
-      load_p(stages[S], ks + 2);
+      mix<NM, ND, (QC - I2) * QR * 5 / 2, QC - I2>();
+      wait_barrier<Q_LD>();
+      load_p(stages[2 * S], ks + 2);
       in_order();
       load_q(codes, ks + 3);
-      frags(stages[S ^ 1], 0, a0, b0);
+      frags(S ^ 1, 0, a0, b0);
       mfmas(a1, b1);
+      interleave<NM, ND, P_LD + Q_LD>();
+      __builtin_amdgcn_sched_barrier(0);
     };
     for (int ks = 0; ks < nk; ks += 2) {
       step(std::integral_constant<int, 0>{}, ks, qb);
@@ -209,7 +253,9 @@ template <class Tile, int ODT, bool SILU>
 __global__ __launch_bounds__(256) void gemm_i8_dx_kernel(GradI8Args a, int ntiles) {
   __shared__ __attribute__((aligned(1024))) char smem0[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem1[Tile::SMEM_BYTES];
-  char* const stages[4] = {smem0, smem1, smem0, smem1};
+  __shared__ __attribute__((aligned(1024))) char smem2[Tile::SMEM_BYTES];
+  __shared__ __attribute__((aligned(1024))) char smem3[Tile::SMEM_BYTES];
+  char* const stages[4] = {smem0, smem1, smem2, smem3};
   const RowTile t = row_tile<Tile::TM>(a.offsets, a.E, a.T, ntiles, a.sync);
   if (t.e < 0) return;
   const int rows = (int)min((int64_t)Tile::TM, t.end - t.row), col0 = t.nt * Tile::TN, cols = min(Tile::TN, a.K - col0);
@@ -234,17 +280,40 @@ __global__ __launch_bounds__(256) void gemm_i8_dx_kernel(GradI8Args a, int ntile
       });
 }
 
+// The expert of rank r when experts stand by falling rows (up to 64; by number where there are more, and among equals).
+__device__ __forceinline__ int expert_of_rank(const GradI8Args& a, int r) {
+  if (a.E > 64 || !a.offsets) return r;
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, hi = -1;
+  if (lane < a.E) group_bounds(a.offsets, lane, a.T, &lo, &hi);
+  const int n = (int)(hi - lo);  // (-1 past the last expert)
+  int before = 0;
+  for (int i = 0; i < a.E; ++i) {
+    const int o = __shfl(n, i, 64);
+    before += o > n || (o == n && i < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < a.E && before == r));
+}
+
+// A tile of an expert's matrix, or of one of `splits` parts of the sum over its rows (then in
+// fp32 to the workspace, which holds the parts one after another).  Every XCD takes an eighth of
+// each expert's tiles, the experts with most rows first: groups differ in length, and what is
+// long is not to be left for the end (three groups of 8192 rows in all, 112 tiles each: on average
+// 73 steps of 64 rows a CU, 119 with the experts' tiles dealt to the XCDs as they stand, 57 at best).
 template <class Tile, int ODT>
-__global__ __launch_bounds__(256) void gemm_i8_dw_kernel(GradI8Args a, int ktiles, int ntiles) {
+__global__ __launch_bounds__(256) void gemm_i8_dw_kernel(GradI8Args a, int ktiles, int ntiles, int splits) {
   __shared__ __attribute__((aligned(1024))) char smem0[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem1[Tile::SMEM_BYTES];
-  char* const stages[4] = {smem0, smem1, smem0, smem1};
-  // each XCD takes one run of all tiles, expert by expert, row tile by row tile
-  const int64_t total = (int64_t)a.E * ktiles * ntiles, b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-  const int q = (int)(b % kNumQueues);
-  const int64_t at = total * q / kNumQueues + b / kNumQueues;
-  if (at >= total * (q + 1) / kNumQueues) return;
-  const int e = (int)(at / ((int64_t)ktiles * ntiles)), in = (int)(at - (int64_t)e * ktiles * ntiles);
+  __shared__ __attribute__((aligned(1024))) char smem2[Tile::SMEM_BYTES];
+  __shared__ __attribute__((aligned(1024))) char smem3[Tile::SMEM_BYTES];
+  char* const stages[4] = {smem0, smem1, smem2, smem3};
+  const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, i = b / kNumQueues;
+  const int q = (int)(b % kNumQueues), units = ktiles * ntiles * splits;
+  const int most = (units + kNumQueues - 1) / kNumQueues;  // of one expert on one XCD
+  const int rank = (int)(i / most);
+  const int unit = (int)((int64_t)units * q / kNumQueues + i % most);
+  if (rank >= a.E || unit >= (int)((int64_t)units * (q + 1) / kNumQueues)) return;
+  const int e = uniform(expert_of_rank(a, rank)), part = unit / (ktiles * ntiles), in = unit - part * (ktiles * ntiles);
   const int k0 = in / ntiles * Tile::TM, n0 = in % ntiles * Tile::TN;
   int64_t lo = 0, hi = a.T;
   if (a.offsets) {
@@ -253,9 +322,14 @@ __global__ __launch_bounds__(256) void gemm_i8_dw_kernel(GradI8Args a, int ktile
     lo = uniform64(lo);
     hi = uniform64(hi);
   }
+  if (splits > 1) {
+    const int64_t steps = (hi - lo + Tile::BK - 1) / Tile::BK, first = lo;
+    lo = min(first + steps * part / splits * Tile::BK, hi);
+    hi = min(first + steps * (part + 1) / splits * Tile::BK, hi);
+  }
   floatx16 acc[Tile::FM][Tile::FN];
   Tile::run({a.dy + lo * a.N, a.q + lo * a.K, a.s + lo, hi - lo, a.N, a.K, 0, n0, k0}, stages, acc);
-  char* dst = reinterpret_cast<char*>(a.out) + (((int64_t)e * a.K + k0) * a.N + n0) * (ODT == kBF16 ? 2 : 4);
+  char* dst = reinterpret_cast<char*>(a.out) + ((((int64_t)part * a.E + e) * a.K + k0) * a.N + n0) * (ODT == kBF16 ? 2 : 4);
   store_rows<Tile, ODT, false>(
       dst, a.N, min(Tile::TM, a.K - k0), min(Tile::TN, a.N - n0), stages,
       [&](int i, int j, int g) {
@@ -263,6 +337,16 @@ __global__ __launch_bounds__(256) void gemm_i8_dw_kernel(GradI8Args a, int ktile
         return floatx4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
       },
       [](int, int, floatx4 v) { return v; });
+}
+
+// The parts of the sums, added in order.
+template <int ODT>
+__global__ __launch_bounds__(256) void dw_sum_kernel(const float* part, void* out, int64_t n, int splits) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+    floatx4 v = *reinterpret_cast<const floatx4*>(part + i);
+    for (int c = 1; c < splits; ++c) v = v + *reinterpret_cast<const floatx4*>(part + c * n + i);
+    st4<ODT>(out, i, v);
+  }
 }
 
 template <class Tile, int ODT>
@@ -285,19 +369,32 @@ int launch_gemm_i8_dx(const GradI8Args& a, hipStream_t s) {
 }
 
 template <class Tile, int ODT>
-static int launch_dw_tile(const GradI8Args& a, hipStream_t s) {
+static hipError_t launch_dw_tile(const GradI8Args& a, int splits, hipStream_t s) {
   const int kt = (a.K + Tile::TM - 1) / Tile::TM, nt = (a.N + Tile::TN - 1) / Tile::TN;
-  const int64_t n = ((int64_t)a.E * kt * nt + kNumQueues - 1) / kNumQueues * kNumQueues, x = std::min<int64_t>(n, 1 << 20);
-  hipLaunchKernelGGL((gemm_i8_dw_kernel<Tile, ODT>), dim3((uint32_t)x, (uint32_t)((n + x - 1) / x)), dim3(256), 0, s, a, kt, nt);
+  const int most = (kt * nt * splits + kNumQueues - 1) / kNumQueues;
+  const int64_t n = (int64_t)most * a.E * kNumQueues, x = std::min<int64_t>(n, 1 << 20);
+  hipLaunchKernelGGL((gemm_i8_dw_kernel<Tile, ODT>), dim3((uint32_t)x, (uint32_t)((n + x - 1) / x)), dim3(256), 0, s, a, kt, nt,
+                     splits);
   return hipGetLastError();
 }
 template <int ODT>
 static int launch_dw(const GradI8Args& a, hipStream_t s) {
+  const int splits = dw_splits(a.E, a.T, a.N, a.K);
+  if (splits > 1) {
+    GradI8Args b = a;
+    b.out = a.part;
+    const hipError_t e = launch_dw_tile<TileGrad<true, 256, 256>, kF32>(b, splits, s);
+    if (e != hipSuccess) return e;
+    const int64_t n = (int64_t)a.E * a.K * a.N;
+    hipLaunchKernelGGL(dw_sum_kernel<ODT>, dim3((uint32_t)std::min<int64_t>((n + 1023) / 1024, 8192)), dim3(256), 0, s, a.part,
+                       a.out, n, splits);
+    return hipGetLastError();
+  }
   const int64_t big = (int64_t)a.E * ((a.K + 255) / 256) * ((a.N + 255) / 256);
   const int64_t mid = (int64_t)a.E * ((a.K + 127) / 128) * ((a.N + 127) / 128);
-  if (big >= 128) return launch_dw_tile<TileGrad<true, 256, 256>, ODT>(a, s);
-  if (mid >= 128) return launch_dw_tile<TileGrad<true, 128, 128>, ODT>(a, s);
-  return launch_dw_tile<TileGrad<true, 64, 64>, ODT>(a, s);
+  if (big >= 128) return launch_dw_tile<TileGrad<true, 256, 256>, ODT>(a, 1, s);
+  if (mid >= 128) return launch_dw_tile<TileGrad<true, 128, 128>, ODT>(a, 1, s);
+  return launch_dw_tile<TileGrad<true, 64, 64>, ODT>(a, 1, s);
 }
 int launch_gemm_i8_dw(const GradI8Args& a, hipStream_t s) {
   return a.out_dt == kBF16 ? launch_dw<kBF16>(a, s) : launch_dw<kF32>(a, s);

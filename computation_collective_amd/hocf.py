@@ -43,7 +43,7 @@ EXPORTED = [
     "hocf_moe_slots", "hocf_moe_slots_workspace_bytes", "hocf_moe_combine", "hocf_moe_combine_bwd",
     "hocf_gemv_w4", "hocf_w4_pack",
     "hocf_quant_i8", "hocf_dequant_i8", "hocf_weights_i8", "hocf_weights_i8_workspace_bytes",
-    "hocf_gemm_i8", "hocf_gemv_i8", "hocf_gemm_i8_dx", "hocf_gemm_i8_dw",
+    "hocf_gemm_i8", "hocf_gemv_i8", "hocf_gemm_i8_dx", "hocf_gemm_i8_dw", "hocf_gemm_i8_dw_workspace_bytes",
     "hocf_status_string", "hocf_last_error", "hocf_abi_version",
 ]
 
@@ -140,6 +140,8 @@ def lib():
         L.hocf_gemv_i8.argtypes = [i] * 7 + [vp] * 6 + [S, vp]
         L.hocf_gemm_i8_dx.argtypes = [i, i64, i, i, i] + [vp] * 7 + [S, vp]
         L.hocf_gemm_i8_dw.argtypes = [i, i64, i, i, i] + [vp] * 5 + [S, vp]
+        L.hocf_gemm_i8_dw_workspace_bytes.argtypes = [i, i64, i, i]
+        L.hocf_gemm_i8_dw_workspace_bytes.restype = sz
         for f in ("hocf_moe_route", "hocf_moe_route_bwd", "hocf_moe_slots", "hocf_moe_combine", "hocf_moe_combine_bwd",
                   "hocf_gemv_w4", "hocf_w4_pack", "hocf_quant_i8", "hocf_dequant_i8", "hocf_weights_i8", "hocf_gemm_i8",
                   "hocf_gemv_i8", "hocf_gemm_i8_dx", "hocf_gemm_i8_dw"):
@@ -423,6 +425,10 @@ def hocf_gemm_i8_dx(E, T, N, K, out_dt, dy, wq, ws, offsets, pre_codes, pre_scal
     """The gradient of the product's rows (with pre_codes: of what SiLU was given)."""
     return lib().hocf_gemm_i8_dx(E, T, N, K, out_dt, ptr(dy), ptr(wq), ptr(ws), ptr(offsets), ptr(pre_codes),
                                  ptr(pre_scales), ptr(dx), ctypes.byref(sync_), _stream(stream))
+
+
+def hocf_gemm_i8_dw_workspace_bytes(E, T, N, K) -> int:
+    return lib().hocf_gemm_i8_dw_workspace_bytes(E, T, N, K)
 
 
 def hocf_gemm_i8_dw(E, T, N, K, out_dt, xq, xs, dy, offsets, dw, sync_, stream=None) -> int:

@@ -114,14 +114,14 @@
  * workgroup take many items; every operator completes with any grid of one
  * or more workgroups.  hocf_moe_slots (one or two kernels), hocf_moe_combine
  * and its backward pass, hocf_gemv_w4, hocf_w4_pack and the 8-bit operators
- * (hocf_weights_i8: two kernels, the others: one) launch ordinary grids, which
+ * (hocf_weights_i8 two kernels, hocf_gemm_i8_dw one or two, the others one) launch ordinary grids, which
  * the variable does not cap.
  *
  * Workspace.  Scheduler counters.  The caller allocates at least the size
  * the matching *_workspace_bytes() query returns, zeroes it ONCE, and may
  * then reuse it for any number of calls: every call leaves it zeroed again,
- * except those of hocf_a2a_gemm*, hocf_moe_slots and hocf_weights_i8, which need
- * no zeroing and do not leave it zeroed (zero it before another operator takes it).
+ * except those of hocf_a2a_gemm*, hocf_moe_slots, hocf_weights_i8 and hocf_gemm_i8_dw,
+ * which need no zeroing and do not leave it zeroed (zero it before another operator takes it).
  * Calls that may run concurrently need separate workspaces.
  */
 #ifndef HOCF_H
@@ -826,10 +826,14 @@ hocf_status hocf_gemm_i8_dx(int E, int64_t T, int N, int K, hocf_dtype out_dt, c
  *
  *   xq [T][K] int8   xs [T] fp32   dy [T][N] bf16   offsets  as for hocf_gemm_i8
  *   dw [E][K][N] out_dt
+ * Where the matrices have few tiles and many rows, the sums are taken in parts
+ * that go through the workspace (which needs no zeroing, and is not left zeroed)
+ * and are added in order by a second kernel.
  * Other arguments, offsets and support as for hocf_gemm_i8.
  * ---------------------------------------------------------------------- */
 hocf_status hocf_gemm_i8_dw(int E, int64_t T, int N, int K, hocf_dtype out_dt, const int8_t* xq, const float* xs,
                             const void* dy, const int64_t* offsets, void* dw, const hocf_sync* sync, void* stream);
+size_t hocf_gemm_i8_dw_workspace_bytes(int E, int64_t T, int N, int K);
 
 /* ---------------------------------------------------------------------- */
 const char* hocf_status_string(hocf_status s); /* static string, never NULL */
