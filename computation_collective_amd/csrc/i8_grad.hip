@@ -20,23 +20,6 @@ __device__ __forceinline__ float silu_slope(float h) {
   return p * fmaf(h, 1.0f - p, 1.0f);
 }
 
-// Order within a quarter of a step: NM matrix instructions, ND LDS reads soon behind the
-// first of them, NV vector instructions and NW LDS writes spread over all.
-template <int NM, int ND, int NV, int NW, int X = 0>
-__device__ __forceinline__ void mix() {
-  if constexpr (X < NM) {
-    constexpr int dpm = (ND + NM - 1) / NM, d = ND - X * dpm < dpm ? (ND - X * dpm > 0 ? ND - X * dpm : 0) : dpm;
-    constexpr int v = NV * (X + 1) / NM - NV * X / NM, w = NW * (X + 1) / NM - NW * X / NM;
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
-    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
-    if constexpr (w > 0) __builtin_amdgcn_sched_group_barrier(0x200, w, 0);
-    mix<NM, ND, NV, NW, X + 1>();
-  } else {
-    __builtin_amdgcn_sched_barrier(0);  // (conversions stay in their quarter)
-  }
-}
-
 // A TR x TC tile (rows x columns of the result) of four waves, summed over steps of 64.
 // DW: rows are codes, columns dy.  Else: rows are dy, columns codes.
 //
@@ -51,8 +34,8 @@ template <bool DW, int TR, int TC>
 struct TileGrad {
   static constexpr int TM = TR, TN = TC, WM = 2, WN = 2, NW = 4, NT = 256;
   static constexpr int WTM = TM / WM, WTN = TN / WN, FM = WTM / 32, FN = WTN / 32;
-  // Two stages of two arrays, 2 S for dy and 2 S + 1 for codes: with one array for both, the
-  // compiler would wait for dy's loads before it lets the codes' writes go (dx 177 us, not 130).
+  // Two stages of dy and of codes (which wait in registers before), each an array of its own:
+  // the compiler then knows that what is on its way into one is not read or written in another.
   static constexpr int BK = 64, NST = 4;
   static constexpr int QW = DW ? TR : TC, PW = DW ? TC : TR;     // codes and dy of a step
   static constexpr int SMEM_BYTES = TM * BK * 2;
@@ -71,7 +54,8 @@ struct TileGrad {
     int p0, q0;          // dw: first column of dy; first column of q
   };
 
-  __device__ static __forceinline__ void run(const Operands& o, char* const (&stages)[4], floatx16 (&acc)[FM][FN]) {
+  __device__ static __forceinline__ void run(const Operands& o, char* const (&ps)[2], char* const (&qs)[2],
+                                             floatx16 (&acc)[FM][FN]) {
 #if defined(__HIP_DEVICE_COMPILE__)
     const int lane = opaque_lane(), wave = uniform(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -97,18 +81,18 @@ struct TileGrad {
       poff = (uint32_t)row * (uint32_t)o.N * 2u + ppiece;
     }
     const __amdgpu_buffer_rsrc_t rp0 = ranged_rsrc(o.dy, DW ? 0 : (uint32_t)o.rows * (uint32_t)o.N * 2u);
-    auto load_p = [&](char* st, int ks) {
+    auto load_p = [&](char* st, int ks, int t0, int t1) {
       if constexpr (DW) {
         const int64_t c0 = min((int64_t)ks * BK, o.C);
         const uint32_t left = (uint32_t)min((int64_t)BK, o.C - c0);
         const __amdgpu_buffer_rsrc_t r = ranged_rsrc(o.dy + c0 * o.N, left * (uint32_t)o.N * 2u);
 #pragma unroll
-        for (int t = 0; t < P_LD; ++t)
+        for (int t = t0; t < t1; ++t)
           load_lds16(r, st + (t * NW + wave) * 1024, poff, (uint32_t)(t * NW * RP) * (uint32_t)o.N * 2u);
       } else {
         const uint32_t voff = (int64_t)ks * BK * 2 + ppiece < (int64_t)o.N * 2 ? poff : kNowhere;
 #pragma unroll
-        for (int t = 0; t < P_LD; ++t)
+        for (int t = t0; t < t1; ++t)
           load_lds16(rp0, st + (t * NW + wave) * 1024, voff,
                      (uint32_t)ks * (BK * 2) + (uint32_t)(t * 32) * (uint32_t)o.N * 2u);
       }
@@ -120,16 +104,17 @@ struct TileGrad {
       uint32_t w[QR][QC / 4];
       floatx4 s[QR / 4];
     };
-    auto load_q = [&](Codes& r, int ks) {
+    auto load_q = [&](Codes& r, int ks, int l0, int l1) {
       const int64_t c0 = min((int64_t)ks * BK, o.C);
       const uint32_t left = (uint32_t)min((int64_t)BK, o.C - c0);
       const __amdgpu_buffer_rsrc_t rq = ranged_rsrc(o.q + c0 * o.K, left * (uint32_t)o.K), rs = ranged_rsrc(o.s + c0, left * 4u);
 #pragma unroll
-      for (int t = 0; t < QR / 4; ++t)
-        r.s[t] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, qrow * 4 + t * 16, 0, 0));
-#pragma unroll
-      for (int t = 0; t < QR; ++t) {
-        const int soff = uniform((int)(t * (uint32_t)o.K));
+      for (int l = l0; l < l1; ++l) {
+        if (l < QR / 4) {
+          r.s[l] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, qrow * 4 + l * 16, 0, 0));
+          continue;
+        }
+        const int t = l - QR / 4, soff = uniform((int)(t * (uint32_t)o.K));
         if constexpr (QC == 8) {
           const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rq, (int)qoff, soff, 0);
           r.w[t][0] = v[0];
@@ -178,8 +163,7 @@ struct TileGrad {
             (HOCF_LDS short4v*)(st + (t_at ^ (j << 6)) + (kk * 16 + 4 * hh) * (PW * 2)));
       return __builtin_bit_cast(bf16x8, short8v{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]});
     };
-    auto frags = [&](int S, int kk, bf16x8 (&a)[FM], bf16x8 (&b)[FN]) {
-      const char *p = stages[2 * S], *q = stages[2 * S + 1];
+    auto frags = [&](const char* p, const char* q, int kk, bf16x8 (&a)[FM], bf16x8 (&b)[FN]) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) a[i] = DW ? frag_q(q, kk, i) : frag_p(p, kk, i);
 #pragma unroll
@@ -195,55 +179,59 @@ struct TileGrad {
     constexpr int NM = FM * FN, ND = FM + (DW ? 2 : 1) * FN;
     bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
     Codes qa, qb;
-
     // whole pairs of steps: what is past the sum's end loads as zeros
     const int nk = (int)((o.C + 2 * BK - 1) / (2 * BK) * 2);
     if (nk == 0) return;
-    load_q(qa, 0);
-    load_q(qb, 1);
+    // a step's loads: dy's in two runs, the codes' in three (the last quarter's before the first two of the next step)
+    constexpr int P0 = P_LD / 2, Q0 = Q_LD / 3, Q1 = 2 * Q_LD / 3;
+    load_q(qa, 0, 0, Q_LD);
+    load_p(ps[0], 0, 0, P_LD);
     in_order();
-    load_p(stages[0], 0);
+    load_q(qb, 1, 0, Q_LD);
 #pragma unroll
-    for (int i = 0; i < QC; ++i) put_q(qa, stages[1], i);
-    wait_barrier<0>();
-    load_p(stages[2], 1);
+    for (int i = 0; i < QC; ++i) put_q(qa, qs[0], i);
+    wait_barrier<Q_LD>();
+    load_p(ps[1], 1, 0, P0);
+    load_q(qa, 2, 0, Q0);
+    frags(ps[0], qs[0], 0, a0, b0);
     in_order();
-    load_q(qa, 2);
-    frags(0, 0, a0, b0);
-    // Stage S holds step ks, whose quarters are multiplied in turn, the next one's fragments on
-    // their way; meanwhile step ks + 1's codes become the other stage's numbers.  The barrier before the last quarter
-    // has the other stage complete (all but step ks + 2's codes have arrived) and frees stage S,
-    // for step ks + 2's dy, and the registers of codes, for step ks + 3's.
-    constexpr int I1 = (QC + 2) / 3, I2 = (2 * QC + 2) / 3;
-    auto step = [&](auto s_c, int ks, Codes& codes) {
+    // Step ks multiplies its quarters in turn, the next one's fragments on their way; meanwhile the codes of
+    // step ks + 1 become numbers in the other stage.  At the barrier before the last quarter that stage is complete
+    // (of the loads, only those behind its dy may still be on their way), and what step ks read is free: for step ks + 2's dy,
+    // and the registers of codes for step ks + 3's.  Their loads are spread over three quarters:
+    // in a bunch they hold up the waves that issue them.
+    constexpr int C1 = (QC + 2) / 3, C2 = (2 * QC + 2) / 3, VC = QR * 5 / 2;  // (vector instructions of a column)
+    auto step = [&](auto s_c, int ks, Codes& next, Codes& after) {
       constexpr int S = decltype(s_c)::value;
-      frags(S, 1, a1, b1);
-#pragma unroll
-      for (int i = 0; i < I1; ++i) put_q(codes, stages[2 * (S ^ 1) + 1], i);
-      mfmas(a0, b0);
-      mix<NM, ND, I1 * QR * 5 / 2, I1>();
-      frags(S, 2, a0, b0);
-#pragma unroll
-      for (int i = I1; i < I2; ++i) put_q(codes, stages[2 * (S ^ 1) + 1], i);
-      mfmas(a1, b1);
-      mix<NM, ND, (I2 - I1) * QR * 5 / 2, I2 - I1>();
-      frags(S, 3, a1, b1);
-#pragma unroll
-      for (int i = I2; i < QC; ++i) put_q(codes, stages[2 * (S ^ 1) + 1], i);
-      mfmas(a0, b0);
-      mix<NM, ND, (QC - I2) * QR * 5 / 2, QC - I2>();
-      wait_barrier<Q_LD>();
-      load_p(stages[2 * S], ks + 2);
+      load_p(ps[S ^ 1], ks + 1, P0, P_LD);
       in_order();
-      load_q(codes, ks + 3);
-      frags(S ^ 1, 0, a0, b0);
+      load_q(after, ks + 2, Q0, Q1);
+      frags(ps[S], qs[S], 1, a1, b1);
+#pragma unroll
+      for (int i = 0; i < C1; ++i) put_q(next, qs[S ^ 1], i);
+      mfmas(a0, b0);
+      mix<NM, ND, P_LD - P0 + Q1 - Q0, C1 * VC, C1>();
+      load_q(after, ks + 2, Q1, Q_LD);
+      frags(ps[S], qs[S], 2, a0, b0);
+#pragma unroll
+      for (int i = C1; i < C2; ++i) put_q(next, qs[S ^ 1], i);
       mfmas(a1, b1);
-      interleave<NM, ND, P_LD + Q_LD>();
-      __builtin_amdgcn_sched_barrier(0);
+      mix<NM, ND, Q_LD - Q1, (C2 - C1) * VC, C2 - C1>();
+      frags(ps[S], qs[S], 3, a1, b1);
+#pragma unroll
+      for (int i = C2; i < QC; ++i) put_q(next, qs[S ^ 1], i);
+      mfmas(a0, b0);
+      mix<NM, ND, 0, (QC - C2) * VC, QC - C2>();
+      wait_barrier<Q_LD - Q0>();
+      load_p(ps[S], ks + 2, 0, P0);
+      load_q(next, ks + 3, 0, Q0);
+      frags(ps[S ^ 1], qs[S ^ 1], 0, a0, b0);
+      mfmas(a1, b1);
+      mix<NM, ND, P0 + Q0, 0, 0>();
     };
     for (int ks = 0; ks < nk; ks += 2) {
-      step(std::integral_constant<int, 0>{}, ks, qb);
-      step(std::integral_constant<int, 1>{}, ks + 1, qa);
+      step(std::integral_constant<int, 0>{}, ks, qb, qa);
+      step(std::integral_constant<int, 1>{}, ks + 1, qa, qb);
     }
 #endif
   }
@@ -256,12 +244,13 @@ __global__ __launch_bounds__(256) void gemm_i8_dx_kernel(GradI8Args a, int ntile
   __shared__ __attribute__((aligned(1024))) char smem2[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem3[Tile::SMEM_BYTES];
   char* const stages[4] = {smem0, smem1, smem2, smem3};
+  char *const ps[2] = {smem0, smem1}, *const qs[2] = {smem2, smem3};
   const RowTile t = row_tile<Tile::TM>(a.offsets, a.E, a.T, ntiles, a.sync);
   if (t.e < 0) return;
   const int rows = (int)min((int64_t)Tile::TM, t.end - t.row), col0 = t.nt * Tile::TN, cols = min(Tile::TN, a.K - col0);
   floatx16 acc[Tile::FM][Tile::FN];
   Tile::run({a.dy + t.row * a.N, a.q + (int64_t)t.e * a.N * a.K, a.s + (int64_t)t.e * a.N, a.N, a.N, a.K, rows, 0, col0},
-            stages, acc);
+            ps, qs, acc);
   char* dst = reinterpret_cast<char*>(a.out) + (t.row * a.K + col0) * (ODT == kBF16 ? 2 : 4);
   const int8_t* pre = SILU ? a.pre + t.row * a.K + col0 : nullptr;
   const float* pre_s = SILU ? a.pre_s + t.row : nullptr;
@@ -307,6 +296,7 @@ __global__ __launch_bounds__(256) void gemm_i8_dw_kernel(GradI8Args a, int ktile
   __shared__ __attribute__((aligned(1024))) char smem2[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem3[Tile::SMEM_BYTES];
   char* const stages[4] = {smem0, smem1, smem2, smem3};
+  char *const ps[2] = {smem0, smem1}, *const qs[2] = {smem2, smem3};
   const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, i = b / kNumQueues;
   const int q = (int)(b % kNumQueues), units = ktiles * ntiles * splits;
   const int most = (units + kNumQueues - 1) / kNumQueues;  // of one expert on one XCD
@@ -328,7 +318,7 @@ __global__ __launch_bounds__(256) void gemm_i8_dw_kernel(GradI8Args a, int ktile
     hi = min(first + steps * (part + 1) / splits * Tile::BK, hi);
   }
   floatx16 acc[Tile::FM][Tile::FN];
-  Tile::run({a.dy + lo * a.N, a.q + lo * a.K, a.s + lo, hi - lo, a.N, a.K, 0, n0, k0}, stages, acc);
+  Tile::run({a.dy + lo * a.N, a.q + lo * a.K, a.s + lo, hi - lo, a.N, a.K, 0, n0, k0}, ps, qs, acc);
   char* dst = reinterpret_cast<char*>(a.out) + ((((int64_t)part * a.E + e) * a.K + k0) * a.N + n0) * (ODT == kBF16 ? 2 : 4);
   store_rows<Tile, ODT, false>(
       dst, a.N, min(Tile::TM, a.K - k0), min(Tile::TN, a.N - n0), stages,

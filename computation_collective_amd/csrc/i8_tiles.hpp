@@ -41,9 +41,29 @@ __device__ __forceinline__ void wait_barrier() {
   static_assert(N <= 63, "vmcnt range");
   in_order();
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
-  __asm__ volatile("" ::: "memory");
+  in_order();
   __builtin_amdgcn_s_barrier();
-  __asm__ volatile("" ::: "memory");
+  in_order();
+}
+
+// Order within a quarter of a step: NM matrix instructions, ND LDS reads soon behind the
+// first of them, NL loads, NV vector instructions and NW LDS writes spread over all.  Nothing moves
+// out of the quarter: counts of loads on their way go by it.
+template <int NM, int ND, int NL, int NV, int NW, int X = 0>
+__device__ __forceinline__ void mix() {
+  if constexpr (X < NM) {
+    constexpr int dpm = (ND + NM - 1) / NM, d = ND - X * dpm < dpm ? (ND - X * dpm > 0 ? ND - X * dpm : 0) : dpm;
+    constexpr int l = NL * (X + 1) / NM - NL * X / NM, v = NV * (X + 1) / NM - NV * X / NM, w = NW * (X + 1) / NM - NW * X / NM;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
+    if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(0x020, l, 0);
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
+    if constexpr (w > 0) __builtin_amdgcn_sched_group_barrier(0x200, w, 0);
+    mix<NM, ND, NL, NV, NW, X + 1>();
+  } else {
+    in_order();
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 // The bounds of group e within [0, T], whatever the offsets hold.
@@ -160,7 +180,7 @@ __device__ __forceinline__ void store_rows(char* dst, int64_t ld, int rows, int 
   const int wm = wave / Tile::WN, wn = wave % Tile::WN;
   const int lr = lane & 31, half = lane >> 5, sr = lane / L::NCH, sc = lane % L::NCH;
   const int tcol = wn * Tile::WTN + sc * CE;
-  __syncthreads();
+  wait_barrier<0>();  // (loads past the sum's end may still be on their way into the stages)
   char* area = L::area(stages, wave);
 #pragma unroll
   for (int i = 0; i < Tile::FM; ++i) {
