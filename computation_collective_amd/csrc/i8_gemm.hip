@@ -155,20 +155,22 @@ int launch_gemm_i8(const GemmI8Args& a, hipStream_t s) {
 }
 
 // A few rows, each with an expert of its own choice.  Bound by the weights' bytes.  A
-// workgroup takes 16 columns of an expert for up to 16 of its rows: its four waves take
-// pieces of 128 k in turn (two loads of a lane: 16 columns x 128 bytes, whole lines), up to U of
-// them at once, and add up in LDS.  Sums of integers: their order does not matter.
+// workgroup takes C blocks of 16 columns of an expert for up to 16 of its rows: its four waves
+// take pieces of 128 k in turn (two loads of a lane: 16 columns x 128 bytes, whole lines), U pieces
+// at once, and add up in LDS.  Where all of K is at once (C > 1) the rows stay in
+// registers and the next block's weights are on their way while one's sums are put together.
+// Sums of integers: their order does not matter.
 __device__ __forceinline__ int local_expert(const GemvI8Args& a, int r) {
   const uint32_t e = (uint32_t)a.experts[r] - (uint32_t)a.e0;
   return e < (uint32_t)a.E ? (int)e : -1;
 }
 
-template <int ODT, int U>
+template <int ODT, int U, int C>
 __global__ __launch_bounds__(256) void gemv_i8_kernel(GemvI8Args a, bool by_row) {
-  __shared__ int s_part[4][16][17];
+  __shared__ int s_part[2][4][16][17];
   __shared__ uint16_t s_rows[kI8MaxRows];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int y = blockIdx.y, n0 = blockIdx.x * 16;
+  const int y = blockIdx.y, n0 = blockIdx.x * 16 * C;
   // this workgroup's expert: the y-th local one, or row y's (and then only for the
   // first of the rows that chose it)
   const int want = !a.experts ? 0 : by_row ? uniform(local_expert(a, y)) : y;
@@ -186,60 +188,110 @@ __global__ __launch_bounds__(256) void gemv_i8_kernel(GemvI8Args a, bool by_row)
     n_rows += __popcll(m);
     // rows of other ranks' experts: zeros, by the row's own workgroup or the first expert's
     if (wave == 0 && a.experts && e < 0 && r < a.R && (by_row ? r == y : y == 0))
-      for (int c = n0; c < min(a.N, n0 + 16); ++c) st1<ODT>(a.out, (int64_t)r * a.N + c, 0.0f);
+      for (int c = n0; c < min(a.N, n0 + 16 * C); ++c) st1<ODT>(a.out, (int64_t)r * a.N + c, 0.0f);
   }
   if (!first || n_rows == 0) return;  // (the same in every wave)
   __builtin_amdgcn_wave_barrier();
 
   const int q = lane >> 4, c = lane & 15;
-  const int8_t* w = a.wq + ((int64_t)want * a.N + min(n0 + c, a.N - 1)) * a.K;  // (columns past the last repeat it, unused)
+  const int8_t* w0 = a.wq + (int64_t)want * a.N * a.K;
+  // (columns past the last repeat it, unused; k past K too, as zeros of the rows)
+  auto load_w = [&](i32x4 (&w)[U][2], int n, int k0) {
+    const int8_t* p = w0 + (int64_t)min(n + c, a.N - 1) * a.K;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[u][h] = *reinterpret_cast<const i32x4*>(p + min(k0 + u * 512 + h * 64 + q * 16, a.K - 16));
+  };
+  auto load_x = [&](i32x4 (&x)[U][2], int row, int k0) {
+    const int8_t* p = a.xq + (int64_t)row * a.K;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x[u][h] = *reinterpret_cast<const i32x4*>(p + min(k0 + u * 512 + h * 64 + q * 16, a.K - 16));
+  };
+  auto zero_x = [&](i32x4 (&x)[U][2], int k0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (k0 + u * 512 + h * 64 + q * 16 >= a.K) x[u][h] = i32x4{0, 0, 0, 0};
+  };
+  auto products = [&](const i32x4 (&x)[U][2], const i32x4 (&w)[U][2], i32x4 acc) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[u][h], w[u][h], acc, 0, 0, 0);
+    return acc;
+  };
   for (int r0 = blockIdx.z * 16; r0 < n_rows; r0 += gridDim.z * 16) {
     const int rows = min(16, n_rows - r0);
-    const int8_t* x = a.xq + (int64_t)(s_rows[r0 + min(c, rows - 1)] / a.rows_per_x) * a.K;
-    i32x4 acc = {0, 0, 0, 0};
-    for (int k0 = wave * 128; k0 < a.K; k0 += 512 * U) {
-      i32x4 xv[U][2], wv[U][2];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = min(k0 + u * 512 + h * 64 + q * 16, a.K - 16);
-          xv[u][h] = *reinterpret_cast<const i32x4*>(x + k);
-          wv[u][h] = *reinterpret_cast<const i32x4*>(w + k);
-        }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (k0 + u * 512 + h * 64 + q * 16 >= a.K) xv[u][h] = i32x4{0, 0, 0, 0};  // (past K: repeated)
-          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv[u][h], wv[u][h], acc, 0, 0, 0);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_part[wave][q * 4 + i][c] = acc[i];
-    lds_barrier();
+    const int xrow = s_rows[r0 + min(c, rows - 1)] / a.rows_per_x;
     const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;
-    if (tr < rows && n0 + tc < a.N) {
-      const int r = s_rows[r0 + tr];
-      const int v = s_part[0][tr][tc] + s_part[1][tr][tc] + s_part[2][tr][tc] + s_part[3][tr][tc];
-      st1<ODT>(a.out, (int64_t)r * a.N + n0 + tc,
-               (float)v * a.xs[r / a.rows_per_x] * a.ws[(int64_t)want * a.N + n0 + tc]);
+    const int r = s_rows[r0 + min(tr, rows - 1)];
+    const float xs = a.xs[r / a.rows_per_x];
+    // the waves' parts of block n, added up and scaled
+    auto fold = [&](const i32x4& acc, int n, int buf) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_part[buf][wave][q * 4 + i][c] = acc[i];
+      lds_barrier();
+      if (tr < rows && n + tc < a.N) {
+        const int v = s_part[buf][0][tr][tc] + s_part[buf][1][tr][tc] + s_part[buf][2][tr][tc] + s_part[buf][3][tr][tc];
+        st1<ODT>(a.out, (int64_t)r * a.N + n + tc, (float)v * xs * a.ws[(int64_t)want * a.N + n + tc]);
+      }
+    };
+    i32x4 xv[U][2], wa[U][2];
+    if constexpr (C == 1) {
+      i32x4 acc = {0, 0, 0, 0};
+      for (int k0 = wave * 128; k0 < a.K; k0 += 512 * U) {
+        load_x(xv, xrow, k0);
+        load_w(wa, n0, k0);
+        zero_x(xv, k0);
+        acc = products(xv, wa, acc);
+      }
+      fold(acc, n0, 0);
+      lds_barrier();
+    } else {
+      const int k0 = wave * 128, end = min(a.N, n0 + 16 * C);
+      load_x(xv, xrow, k0);
+      load_w(wa, n0, k0);
+      zero_x(xv, k0);
+      for (int n = n0, buf = 0; n < end; n += 16, buf ^= 1) {
+        const i32x4 acc = products(xv, wa, i32x4{0, 0, 0, 0});
+        if (n + 16 < end) load_w(wa, n + 16, k0);
+        fold(acc, n, buf);
+      }
+      lds_barrier();
     }
-    lds_barrier();
   }
 }
 
+template <int ODT, int U, int C>
+static int launch_gemv_c(const GemvI8Args& a, int tiles, hipStream_t s) {
+  const bool by_row = a.experts && a.R < a.E;
+  const dim3 grid((a.N + 16 * C - 1) / (16 * C), !a.experts ? 1 : std::min(a.R, a.E), tiles);
+  hipLaunchKernelGGL((gemv_i8_kernel<ODT, U, C>), grid, dim3(256), 0, s, a, by_row);
+  return hipGetLastError();
+}
+
+template <int ODT, int C>
+static int launch_gemv_k(const GemvI8Args& a, int tiles, hipStream_t s) {
+  if (a.K <= 512) return launch_gemv_c<ODT, 1, C>(a, tiles, s);
+  if (a.K <= 1024) return launch_gemv_c<ODT, 2, C>(a, tiles, s);
+  if (a.K <= 2048) return launch_gemv_c<ODT, 4, C>(a, tiles, s);
+  return launch_gemv_c<ODT, 8, C>(a, tiles, s);
+}
+
+// Blocks of columns a workgroup: as many as leave about 200 workgroups, while all of K is at
+// once.  TB/s of weights with 1, 2 and 4 of them: 1 token x 8 of 64 experts 4096 -> 1792 (896 blocks)
+// 3.9, 4.4, 4.5; 16 x 2 of 32, 1792 -> 4096 (8192) 4.1, 4.6, 4.8; 16 rows of 4096 x 32768 (2048) 3.6, 4.2,
+// 4.6; 8 rows of 1024 x 8192 (512) 2.05, 2.3, 1.6; 1 row of 4096 x 4096 (256) 2.8, 2.4, 1.6.
 template <int ODT>
 static int launch_gemv(const GemvI8Args& a, hipStream_t s) {
-  const bool by_row = a.experts && a.R < a.E;
-  const int y = !a.experts ? 1 : std::min(a.R, a.E);
   const int tiles = ((a.R + a.E - 1) / a.E + 15) / 16;
-  const dim3 grid((a.N + 15) / 16, y, tiles);
-  if (a.K <= 512) hipLaunchKernelGGL((gemv_i8_kernel<ODT, 1>), grid, dim3(256), 0, s, a, by_row);
-  else if (a.K <= 1024) hipLaunchKernelGGL((gemv_i8_kernel<ODT, 2>), grid, dim3(256), 0, s, a, by_row);
-  else if (a.K <= 2048) hipLaunchKernelGGL((gemv_i8_kernel<ODT, 4>), grid, dim3(256), 0, s, a, by_row);
-  else hipLaunchKernelGGL((gemv_i8_kernel<ODT, 8>), grid, dim3(256), 0, s, a, by_row);
-  return hipGetLastError();
+  const int64_t blocks = (int64_t)((a.N + 15) / 16) * (a.experts ? std::min(a.R, a.E) : 1) * tiles;
+  if (a.K > 4096 || blocks < 384) return launch_gemv_k<ODT, 1>(a, tiles, s);
+  return blocks < 768 ? launch_gemv_k<ODT, 2>(a, tiles, s) : launch_gemv_k<ODT, 4>(a, tiles, s);
 }
 
 int launch_gemv_i8(const GemvI8Args& a, hipStream_t s) {
