@@ -65,12 +65,26 @@ struct Eight<kF32> {
   }
 };
 
-// The larger of the running magnitude (its bits: NaN > infinity > numbers) and eight more.
-template <int DT>
-__device__ __forceinline__ uint32_t largest(const Eight<DT>& e, uint32_t m) {
+// The larger of the running magnitude and eight more: bits, in whose order NaN > infinity >
+// numbers.  bf16: of pairs, side by side.
+__device__ __forceinline__ uint32_t largest(const Eight<kF32>& e, uint32_t m) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(e[i]) & 0x7fffffffu);
   return m;
+}
+typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t largest(const Eight<kBF16>& e, uint32_t m) {
+  ushort2_t v = __builtin_bit_cast(ushort2_t, m);
+  v = __builtin_elementwise_max(v, __builtin_bit_cast(ushort2_t, e.u.x & 0x7fff7fffu));
+  v = __builtin_elementwise_max(v, __builtin_bit_cast(ushort2_t, e.u.y & 0x7fff7fffu));
+  v = __builtin_elementwise_max(v, __builtin_bit_cast(ushort2_t, e.u.z & 0x7fff7fffu));
+  v = __builtin_elementwise_max(v, __builtin_bit_cast(ushort2_t, e.u.w & 0x7fff7fffu));
+  return __builtin_bit_cast(uint32_t, v);
+}
+// The bits of the larger of the pair, as fp32's.
+template <int DT>
+__device__ __forceinline__ uint32_t of_pair(uint32_t m) {
+  return DT == kBF16 ? max(m & 0xffff0000u, m << 16) : m;
 }
 
 struct Scale {
@@ -111,27 +125,36 @@ __device__ __forceinline__ uint2 codes_of(const Eight<DT>& e, const Scale& sc) {
   return sc.bad ? make_uint2(0, 0) : make_uint2(four(0), four(4));
 }
 
-// x / (1 + exp(-x)).  In fp32 for a result that is rounded to bf16 (off by less than
-// 2^-20 of itself for |x| < 16), where exp(-|x|) would leave fp32's range through a scaled
-// exponent; in 64 bits for an fp32 result, whose last bit decides codes.
-template <int DT>
-__device__ __forceinline__ float silu(float x) {
-  if constexpr (DT == kBF16) {
-    const float t = fabsf(x) * -1.44269504f;
-    const bool far = t < -100.0f;
-    const float p = __builtin_amdgcn_exp2f(far ? t + 64.0f : t);  // exp(-|x|)
-    const float q = x < 0.0f ? x * p : x;
-    return far ? (x < 0.0f ? q * 0x1p-64f : q) : q * __builtin_amdgcn_rcpf(1.0f + p);
-  } else {
-    return (float)((double)x / (1.0 + exp(-(double)x)));
-  }
+// x / (1 + exp(-x)) of a number below -69, by a scaled exponent: its exp(x) may leave fp32's
+// normal range while the result does not.  (Minus infinity gives NaN, as the quotient does.)
+__device__ __forceinline__ float silu_far(float x) {
+  return x * __builtin_amdgcn_exp2f(fmaf(x, 1.44269504f, 64.0f)) * 0x1p-64f;
 }
-template <int DT>
-__device__ __forceinline__ Eight<DT> silu8(const Eight<DT>& e) {
+
+// x / (1 + exp(-x)).  In fp32 for a result that is rounded to bf16 (off by less than
+// 2^-20 of itself for |x| < 16); in 64 bits for an fp32 result, whose last bit decides codes.
+__device__ __forceinline__ Eight<kBF16> silu8(const Eight<kBF16>& e) {
+  float v[8], t[8], far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t[i] = e[i] * -1.44269504f;
+    far = fmaxf(far, t[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = e[i] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t[i]));
+  if (far > 100.0f)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t[i] > 100.0f) v[i] = silu_far(e[i]);
+  Eight<kBF16> r;
+  r.set(v);
+  return r;
+}
+__device__ __forceinline__ Eight<kF32> silu8(const Eight<kF32>& e) {
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = silu<DT>(e[i]);
-  Eight<DT> r;
+  for (int i = 0; i < 8; ++i) v[i] = (float)((double)e[i] / (1.0 + exp(-(double)e[i])));
+  Eight<kF32> r;
   r.set(v);
   return r;
 }
@@ -187,9 +210,9 @@ __global__ __launch_bounds__(kQThreads) void quant_kernel(QuantI8Args a) {
         m = largest(v[c], m);
       }
   }
-  const Scale s = scale_of(row_largest<W>(m, s_max[0], wave));
+  const Scale s = scale_of(row_largest<W>(of_pair<DT>(m), s_max[0], wave));
   Scale sp = s;
-  if constexpr (KEEP) sp = scale_of(row_largest<W>(mp, s_max[1], wave));
+  if constexpr (KEEP) sp = scale_of(row_largest<W>(of_pair<DT>(mp), s_max[1], wave));
   int8_t* q = a.codes + row * a.K;
   int8_t* qp = KEEP ? a.pre_codes + row * a.K : nullptr;
   auto put = [&](int k, const Eight<DT>& pre, const Eight<DT>& act) {
