@@ -110,11 +110,12 @@ __device__ __forceinline__ uint2 codes_of(const Eight<DT>& e, const Scale& sc) {
     y[i] = fmaf(e[i], sc.inv, kMagic);
     worst = fmaxf(worst, fabsf(fmaf(kMagic - y[i], sc.s, e[i])));
   }
-  if (worst + worst >= sc.s) {  // (a half, or a candidate on the wrong side of one)
+  if (worst + worst >= sc.s) {  // (a half, or a candidate on the wrong side of one; half the row's largest is one)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = fmaf(kMagic - y[i], sc.s, e[i]), d2 = fabsf(d) + fabsf(d);
-      if (d2 > sc.s || (d2 == sc.s && (__float_as_uint(y[i]) & 1u))) y[i] += copysignf(1.0f, d);
+      const int move = (int)(d2 > sc.s) | ((int)(d2 == sc.s) & (int)(__float_as_uint(y[i]) & 1u));
+      y[i] += copysignf((float)move, d);
     }
   }
   auto four = [&](int i) {
@@ -144,8 +145,10 @@ __device__ __forceinline__ Eight<kBF16> silu8(const Eight<kBF16>& e) {
   for (int i = 0; i < 8; ++i) v[i] = e[i] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t[i]));
   if (far > 100.0f)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (t[i] > 100.0f) v[i] = silu_far(e[i]);
+    for (int i = 0; i < 8; ++i) {
+      const float f = silu_far(e[i]);
+      v[i] = t[i] > 100.0f ? f : v[i];
+    }
   Eight<kBF16> r;
   r.set(v);
   return r;
