@@ -37,7 +37,8 @@ template <>
 struct Eight<kBF16> {
   uint4 u;
   __device__ __forceinline__ void load(const void* row, int k) {
-    u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(row) + k);
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    u = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(row) + k)));
   }
   __device__ __forceinline__ float operator[](int i) const {
     const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
@@ -281,8 +282,16 @@ __global__ __launch_bounds__(kQThreads) void dequant_kernel(DequantI8Args a, int
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * s;
-    st4<DT>(a.out, row * a.K + k, floatx4{v[0], v[1], v[2], v[3]});
-    st4<DT>(a.out, row * a.K + k + 4, floatx4{v[4], v[5], v[6], v[7]});
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    Eight<DT> r;
+    r.set(v);
+    u32x4_t* p = reinterpret_cast<u32x4_t*>(reinterpret_cast<char*>(a.out) + (row * a.K + k) * (DT == kBF16 ? 2 : 4));
+    if constexpr (DT == kBF16) {
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, r.u), p);
+    } else {
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, r.lo), p);
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, r.hi), p + 1);
+    }
   }
 }
 
