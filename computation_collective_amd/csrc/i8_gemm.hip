@@ -14,7 +14,10 @@ namespace hocf {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-// A TM x TN tile of four waves; a stage is 128 bytes of k of its rows and columns.
+// A TM x TN tile of four waves; a stage is 128 bytes of k of its rows and columns.  Large tiles
+// have two stages and read the next fragments while one's are multiplied.  Small ones, of
+// which many share a CU, have four, loaded three steps ahead: their steps are shorter than
+// a load takes.
 //
 // LDS: a row is 128 bytes, eight 16-byte pieces, piece c at c ^ (row / 2 mod 8): 16
 // lanes that read one piece of 16 rows touch 16 different groups of banks.
@@ -22,8 +25,8 @@ template <int TM_, int TN_>
 struct TileI8 {
   static constexpr int TM = TM_, TN = TN_, WM = 2, WN = 2, NW = 4, NT = 256;
   static constexpr int WTM = TM / WM, WTN = TN / WN, FM = WTM / 32, FN = WTN / 32;
-  static constexpr int BK = 128, NST = 2;
-  static constexpr int A_BYTES = TM * BK, B_BYTES = TN * BK;
+  static constexpr int A_BYTES = TM * 128, B_BYTES = TN * 128;
+  static constexpr int BK = 128, NST = TM == 64 ? 4 : 2;
   static constexpr int SMEM_BYTES = A_BYTES + B_BYTES;  // one stage
   static constexpr int A_LD = A_BYTES / 1024 / NW, B_LD = B_BYTES / 1024 / NW;
 
@@ -70,7 +73,31 @@ struct TileI8 {
     };
     constexpr int ND = FM + FN, NM = FM * FN;
     i32x4 a0[FM], b0[FN], a1[FM], b1[FN];
-    // whole pairs of steps: k past K loads as zeros, and costs no memory access
+    if constexpr (NST == 4) {
+      const int nk = (K + BK - 1) / BK;  // (steps past it load zeros, and cost no memory access)
+#pragma unroll
+      for (int s = 0; s < 3; ++s) {
+        load(stages[s], s * BK);
+        in_order();
+      }
+      auto step = [&](auto s_c, int ks) {
+        constexpr int S = decltype(s_c)::value;
+        wait_barrier<2 * (A_LD + B_LD)>();  // step ks has arrived, and step ks - 1 is read everywhere
+        load(stages[(S + 3) % 4], (ks + 3) * BK);
+        in_order();
+        frags(stages[S], 0, a0, b0);
+        frags(stages[S], 1, a1, b1);
+        mfmas(a0, b0);
+        frags(stages[S], 2, a0, b0);
+        mfmas(a1, b1);
+        frags(stages[S], 3, a1, b1);
+        mfmas(a0, b0);
+        mfmas(a1, b1);
+      };
+      four_steps(nk, step);
+      return;
+    }
+    // whole pairs of steps: k past K loads as zeros
     const int nk = (K + 2 * BK - 1) / (2 * BK) * 2;
     load(stages[0], 0);
     in_order();
@@ -108,7 +135,9 @@ template <class Tile, int ODT>
 __global__ __launch_bounds__(256) void gemm_i8_kernel(GemmI8Args a, int ntiles) {
   __shared__ __attribute__((aligned(1024))) char smem0[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem1[Tile::SMEM_BYTES];
-  char* const stages[4] = {smem0, smem1, smem0, smem1};
+  __shared__ __attribute__((aligned(1024))) char smem2[Tile::NST > 2 ? Tile::SMEM_BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char smem3[Tile::NST > 2 ? Tile::SMEM_BYTES : 16];
+  char* const stages[4] = {smem0, smem1, smem2, smem3};
   const RowTile t = row_tile<Tile::TM>(a.offsets, a.E, a.T, ntiles, a.sync);
   if (t.e < 0) return;
   const int rows = (int)min((int64_t)Tile::TM, t.end - t.row), col0 = t.nt * Tile::TN, cols = min(Tile::TN, a.N - col0);

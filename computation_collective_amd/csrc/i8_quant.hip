@@ -271,7 +271,7 @@ int launch_quant_i8(const QuantI8Args& a, hipStream_t s) {
   return a.dt == kBF16 ? launch_qdt<kBF16>(a, s) : launch_qdt<kF32>(a, s);
 }
 
-// Reading back: lanes of a wave take pieces of eight codes of 1 to 8 rows.
+// Reading back: 2^lg lanes take the pieces of eight codes of a row in turn.
 template <int DT>
 __global__ __launch_bounds__(kQThreads) void dequant_kernel(DequantI8Args a, int lg) {  // 2^lg lanes a row
   const int64_t i = flat_block() * kQThreads + threadIdx.x, row = i >> lg;
@@ -296,8 +296,10 @@ __global__ __launch_bounds__(kQThreads) void dequant_kernel(DequantI8Args a, int
 }
 
 int launch_dequant_i8(const DequantI8Args& a, hipStream_t s) {
+  // a lane for every piece where there are few, up to a wave a row else
+  const int most = a.T * a.K < (1 << 20) ? 13 : 6;
   int lg = 3;
-  while (lg < 6 && (8 << lg) < a.K) ++lg;
+  while (lg < most && (8 << lg) < a.K) ++lg;
   const int64_t grid = ((a.T << lg) + kQThreads - 1) / kQThreads;
   if (a.dt == kBF16) hipLaunchKernelGGL(dequant_kernel<kBF16>, flat_grid(grid), dim3(kQThreads), 0, s, a, lg);
   else hipLaunchKernelGGL(dequant_kernel<kF32>, flat_grid(grid), dim3(kQThreads), 0, s, a, lg);

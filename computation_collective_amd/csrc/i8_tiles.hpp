@@ -66,6 +66,18 @@ __device__ __forceinline__ void mix() {
   }
 }
 
+// Steps 0 .. n - 1 and on to whole turns of a ring of four stages, each step with its stage as a
+// constant.  (No way out in between: it would cost copies of the accumulators and of what is being loaded.)
+template <class S>
+__device__ __forceinline__ void four_steps(int n, S step) {
+  for (int ks = 0; ks < n; ks += 4) {
+    step(std::integral_constant<int, 0>{}, ks);
+    step(std::integral_constant<int, 1>{}, ks + 1);
+    step(std::integral_constant<int, 2>{}, ks + 2);
+    step(std::integral_constant<int, 3>{}, ks + 3);
+  }
+}
+
 // The bounds of group e within [0, T], whatever the offsets hold.
 __device__ __forceinline__ void group_bounds(const int64_t* offsets, int e, int64_t T, int64_t* lo, int64_t* hi) {
   const int64_t a = offsets[e], b = offsets[e + 1];
