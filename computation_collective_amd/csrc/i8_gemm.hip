@@ -46,14 +46,19 @@ struct TileI8 {
     // is 32 t rows on, which changes neither the piece's place nor the lane's offset
     const int row = wave * 8 + (lane >> 3), piece = ((lane & 7) ^ ((row >> 1) & 7)) << 4;
     const uint32_t off = (uint32_t)row * (uint32_t)K + piece, step32 = 32u * (uint32_t)K;
-    auto load = [&](char* st, int k0) {
+    auto load_a = [&](char* st, int k0) {
       const uint32_t voff = k0 + piece < K ? off : kNowhere;  // (the last stage may end inside)
 #pragma unroll
-      for (int t = 0; t < A_LD; ++t)
-        load_lds16(ra, st + (t * NW + wave) * 1024, voff, (uint32_t)k0 + t * step32);
+      for (int t = 0; t < A_LD; ++t) load_lds16(ra, st + (t * NW + wave) * 1024, voff, (uint32_t)k0 + t * step32);
+    };
+    auto load_b = [&](char* st, int k0) {
+      const uint32_t voff = k0 + piece < K ? off : kNowhere;
 #pragma unroll
-      for (int t = 0; t < B_LD; ++t)
-        load_lds16(rb, st + A_BYTES + (t * NW + wave) * 1024, voff, (uint32_t)k0 + t * step32);
+      for (int t = 0; t < B_LD; ++t) load_lds16(rb, st + A_BYTES + (t * NW + wave) * 1024, voff, (uint32_t)k0 + t * step32);
+    };
+    auto load = [&](char* st, int k0) {
+      load_a(st, k0);
+      load_b(st, k0);
     };
     // fragment kk of block row i: bytes 32 kk + 16 (lane / 32) of row 32 i + lane mod 32 (blocks: 4 KB apart; kk: two bits of the piece)
     const int m = lane & 31, first = m * BK + (((lane >> 5) ^ ((m >> 1) & 7)) << 4);
@@ -101,27 +106,30 @@ struct TileI8 {
     const int nk = (K + 2 * BK - 1) / (2 * BK) * 2;
     load(stages[0], 0);
     in_order();
-    load(stages[1], BK);
-    wait_barrier<A_LD + B_LD>();
+    load_a(stages[1], BK);
+    wait_barrier<A_LD>();
     frags(stages[0], 0, a0, b0);
-    // Stage s holds step ks.  Its last fragments are read while the third quarter multiplies; the
-    // barrier after that frees the stage for step ks + 2 and has step ks + 1 in the other.
+    // Stage S holds step ks.  Its last fragments are read while the third quarter multiplies; the
+    // barrier after that frees the stage for step ks + 2 and has step ks + 1 in the other.  Half of a step's
+    // loads follow the barrier and half go with the next quarter: in a bunch they hold up the
+    // waves that issue them.
     auto step = [&](auto s_c, int ks) {
       constexpr int S = decltype(s_c)::value;
+      load_b(stages[S ^ 1], (ks + 1) * BK);
       frags(stages[S], 1, a1, b1);
       mfmas(a0, b0);
-      interleave<NM, ND, 0>();
+      mix<NM, ND, B_LD, 0, 0>();
       frags(stages[S], 2, a0, b0);
       mfmas(a1, b1);
-      interleave<NM, ND, 0>();
+      mix<NM, ND, 0, 0, 0>();
       frags(stages[S], 3, a1, b1);
       mfmas(a0, b0);
-      interleave<NM, ND, 0>();
+      mix<NM, ND, 0, 0, 0>();
       wait_barrier<0>();
-      load(stages[S], (ks + 2) * BK);
+      load_a(stages[S], (ks + 2) * BK);
       frags(stages[S ^ 1], 0, a0, b0);
       mfmas(a1, b1);
-      interleave<NM, ND, A_LD + B_LD>();
+      mix<NM, ND, A_LD, 0, 0>();
     };
     for (int ks = 0; ks < nk; ks += 2) {
       step(std::integral_constant<int, 0>{}, ks);
@@ -147,18 +155,18 @@ __global__ __launch_bounds__(256) void gemm_i8_kernel(GemmI8Args a, int ntiles) 
   // lane l, element 4 g + v of block (i, j): row 32 i + l mod 32, column 32 j + 8 g + 4 (l / 32) + v of its wave's part
   const int lane = opaque_lane(), wave = uniform(threadIdx.x >> 6);
   const int r0 = wave / Tile::WN * Tile::WTM + (lane & 31), c0 = wave % Tile::WN * Tile::WTN + 4 * (lane >> 5);
-  const float* xs = a.xs + t.row;
-  const float* ws = a.ws + (int64_t)t.e * a.N + col0;
+  // (N is a multiple of 8: four columns are all there or none; rows and columns past the tile's end get zeros)
+  const __amdgpu_buffer_rsrc_t xs = ranged_rsrc(a.xs + t.row, (uint32_t)rows * 4u);
+  const __amdgpu_buffer_rsrc_t ws = ranged_rsrc(a.ws + (int64_t)t.e * a.N + col0, (uint32_t)cols * 4u);
   char* dst = reinterpret_cast<char*>(a.out) + (t.row * a.N + col0) * (ODT == kBF16 ? 2 : 4);
   store_rows<Tile, ODT, false>(
       dst, a.N, rows, cols, stages,
       [&](int i, int j, int g) {
-        // (N is a multiple of 8: four columns are all there or none; rows and columns past the tile's repeat)
-        const float x = xs[min(r0 + 32 * i, rows - 1)];
-        const float4 w = *reinterpret_cast<const float4*>(ws + min(c0 + 32 * j + 8 * g, cols - 4));
+        const float x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(xs, r0 * 4, 32 * 4 * i, 0));
+        const floatx4 w = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(ws, c0 * 4, (32 * j + 8 * g) * 4, 0));
         const i32x16& v = acc[i][j];
-        return floatx4{(float)v[4 * g] * x * w.x, (float)v[4 * g + 1] * x * w.y, (float)v[4 * g + 2] * x * w.z,
-                       (float)v[4 * g + 3] * x * w.w};
+        return floatx4{(float)v[4 * g] * x * w[0], (float)v[4 * g + 1] * x * w[1], (float)v[4 * g + 2] * x * w[2],
+                       (float)v[4 * g + 3] * x * w[3]};
       },
       [](int, int, floatx4 v) { return v; });
 }
