@@ -40,6 +40,7 @@ struct Eight<kBF16> {
     typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
     u = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(row) + k)));
   }
+  __device__ __forceinline__ void load_cached(const void* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ float operator[](int i) const {
     const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
     return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
@@ -56,6 +57,7 @@ struct Eight<kF32> {
     lo = p[0];
     hi = p[1];
   }
+  __device__ __forceinline__ void load_cached(const void* p) { load(p, 0); }
   __device__ __forceinline__ float operator[](int i) const {
     const float4& q = i < 4 ? lo : hi;
     return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
@@ -306,7 +308,7 @@ int launch_dequant_i8(const DequantI8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Weights, first step: the largest magnitude of every column of a slab of rows.
+// Weights in two kernels.  First step: the largest magnitude of every column of a slab of rows.
 // 64 columns x 256 rows a workgroup, eight lanes a row.
 template <int DT>
 __global__ __launch_bounds__(256) void w8_largest_kernel(WeightsI8Args a) {
@@ -378,8 +380,91 @@ __global__ __launch_bounds__(256) void w8_codes_kernel(WeightsI8Args a) {
   }
 }
 
+// Both steps at once, for matrices of up to 512 P rows: 32 columns a workgroup, whose numbers
+// stay in registers -- four rows x eight columns a thread and pass of 512 rows -- until their
+// scales are known, and whose codes are turned in LDS.
+template <int DT, int P>
+__global__ __launch_bounds__(512) void w8_once_kernel(WeightsI8Args a) {
+  constexpr int kRow = 512 * P + 16;  // bytes of a column's codes: columns start on different banks
+  __shared__ __attribute__((aligned(16))) char s_q[32 * kRow];
+  __shared__ uint32_t s_max[8][32];
+  __shared__ Scale s_scale[32];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  // (the columns of an expert that share cache lines go to one XCD)
+  const uint32_t b = xcd_contiguous(blockIdx.x, gridDim.x), nb = (a.N + 31) / 32;
+  const int e = b / nb, n0 = (b - e * nb) * 32, c8 = (lane & 3) * 8, n = n0 + c8;
+  const int r4 = (wave * 16 + (lane >> 2)) * 4;
+  const char* w = reinterpret_cast<const char*>(a.W) + ((int64_t)e * a.K * a.N + min(n, a.N - 8)) * (DT == kBF16 ? 2 : 4);
+  Eight<DT> v[P][4];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      // (K is a multiple of 16: four rows are all there or none; rows past the last repeat it)
+      const int k = min(p * 512 + r4 + r, a.K - 1);
+      v[p][r].load_cached(w + (int64_t)k * a.N * (DT == kBF16 ? 2 : 4));
+    }
+  uint32_t m[8] = {};
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i] = max(m[i], __float_as_uint(v[p][r][i]) & 0x7fffffffu);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int d = 4; d < 64; d <<= 1) m[i] = max(m[i], (uint32_t)__shfl_xor((int)m[i], d, 64));
+    if (lane < 4) s_max[wave][c8 + i] = m[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    uint32_t t = 0;
+    for (int i = 0; i < 8; ++i) t = max(t, s_max[i][threadIdx.x]);
+    s_scale[threadIdx.x] = scale_of(t);
+    if (n0 + (int)threadIdx.x < a.N) a.scales[(int64_t)e * a.N + n0 + threadIdx.x] = s_scale[threadIdx.x].s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const Scale sc = s_scale[c8 + i];
+#pragma unroll
+    for (int p = 0; p < P; p += 2) {  // (two passes' four rows: eight numbers of one scale)
+      const int q = p + 1 < P ? p + 1 : p;
+      const float f[8] = {v[p][0][i], v[p][1][i], v[p][2][i], v[p][3][i], v[q][0][i], v[q][1][i], v[q][2][i], v[q][3][i]};
+      Eight<kF32> col;
+      col.set(f);
+      const uint2 u = codes_of(col, sc);
+      *reinterpret_cast<uint32_t*>(s_q + (c8 + i) * kRow + p * 512 + r4) = u.x;
+      if (p + 1 < P) *reinterpret_cast<uint32_t*>(s_q + (c8 + i) * kRow + q * 512 + r4) = u.y;
+    }
+  }
+  __syncthreads();
+  const int pieces = a.K / 16;
+  for (int t = threadIdx.x; t < 32 * pieces; t += 512) {
+    const int c = t / pieces, k = (t - c * pieces) * 16;
+    if (n0 + c < a.N)
+      *reinterpret_cast<uint4*>(a.wq + ((int64_t)e * a.N + n0 + c) * a.K + k) = *reinterpret_cast<const uint4*>(s_q + c * kRow + k);
+  }
+}
+
+template <int DT, int P>
+static int launch_w8_once(const WeightsI8Args& a, hipStream_t s) {
+  hipLaunchKernelGGL((w8_once_kernel<DT, P>), dim3((a.N + 31) / 32 * a.E), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
 template <int DT>
 static int launch_w8(const WeightsI8Args& a, hipStream_t s) {
+  // One kernel where its workgroups are enough for most CUs (4 x 4096 x 1792 bf16, 224 of them: 27 us
+  // against 36; 3 x 1040 x 1000 fp32, 96: 12.3 against 10.6) and K fits: a thread's share of more rows does
+  // not fit its registers, nor the codes of 32 columns LDS.
+  if ((a.N + 31) / 32 * a.E >= 160) {
+    if (a.K <= 1024) return launch_w8_once<DT, 2>(a, s);
+    if (a.K <= 2048) return launch_w8_once<DT, 4>(a, s);
+    if constexpr (DT == kBF16)
+      if (a.K <= 4096) return launch_w8_once<DT, 8>(a, s);
+  }
   const int nb = (a.N + 63) / 64;
   hipLaunchKernelGGL(w8_largest_kernel<DT>, dim3(nb, a.slabs, a.E), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();

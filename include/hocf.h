@@ -114,7 +114,7 @@
  * workgroup take many items; every operator completes with any grid of one
  * or more workgroups.  hocf_moe_slots (one or two kernels), hocf_moe_combine
  * and its backward pass, hocf_gemv_w4, hocf_w4_pack and the 8-bit operators
- * (hocf_weights_i8 two kernels, hocf_gemm_i8_dw one or two, the others one) launch ordinary grids, which
+ * (hocf_weights_i8 and hocf_gemm_i8_dw one or two kernels, the others one) launch ordinary grids, which
  * the variable does not cap.
  *
  * Workspace.  Scheduler counters.  The caller allocates at least the size

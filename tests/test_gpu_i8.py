@@ -193,7 +193,8 @@ def test_dequant(T, K, dt):
 
 
 @pytest.mark.parametrize("E,K,N", [(1, 16, 8), (2, 48, 64), (3, 1040, 1000), (1, 256, 72), (2, 272, 136), (1, 65536, 8),
-                                   (1, 16, 65536), (5, 400, 200)])
+                                   (1, 16, 65536), (5, 400, 200), (5, 400, 1032), (161, 1040, 24), (40, 1552, 136),
+                                   (170, 2064, 8), (5, 4096, 1032), (4, 4112, 1288)])
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_weights(E, K, N, dt):
     say(f"weights E={E} K={K} N={N} dt={dt}")
@@ -440,6 +441,17 @@ def check_dw(E, T, N, K, out_dt, offsets=None):
 def test_dw_groups(E, T, offsets, out_dt):
     say(f"dw groups E={E} T={T} out={out_dt}")
     check_dw(E, T, 72, 80, out_dt, offsets)
+
+
+def test_dw_sums_in_parts():
+    """Few tiles and many rows: the sums go through the workspace in parts, groups of very different lengths too."""
+    say("dw, sums in parts")
+    assert hocf.hocf_gemm_i8_dw_workspace_bytes(1, 5000, 72, 80) == 4 * 72 * 80 * 4
+    assert hocf.hocf_gemm_i8_dw_workspace_bytes(1, 2000, 72, 80) == 0
+    check_dw(1, 5000, 72, 80, F32)
+    check_dw(1, 4097, 264, 272, BF16)
+    check_dw(2, 9000, 136, 80, F32, [10, 20, 8990])       # one group shorter than a step of each part
+    check_dw(3, 7000, 72, 144, BF16, [0, 0, 6999, 7000])
 
 
 def test_dw_groups_large_tiles():
