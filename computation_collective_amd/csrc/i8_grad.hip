@@ -30,9 +30,12 @@ __device__ __forceinline__ float silu_slope(float h) {
 // of eight columns apart and the reads of neighbours both touch every bank once).  dw's dy
 // has c outermost too and goes straight to LDS as it is, rows of c, pieces at p ^ 4 (c mod 4)
 // (64 columns: ^ 4 (c / 2 mod 2)); the transposing read turns it, four rows x 64 bytes at a time.
+//
+// Small tiles have few steps' work between barriers: two groups of four waves each sum half of the
+// steps, and the first adds the second's.
 template <bool DW, int TR, int TC>
 struct TileGrad {
-  static constexpr int TM = TR, TN = TC, WM = 2, WN = 2, NW = 4, NT = 256;
+  static constexpr int TM = TR, TN = TC, WM = 2, WN = 2, NW = 4, NT = 256, GROUPS = TR == 64 ? 2 : 1;
   static constexpr int WTM = TM / WM, WTN = TN / WN, FM = WTM / 32, FN = WTN / 32;
   // Two stages of dy and of codes (which wait in registers before), each an array of its own:
   // the compiler then knows that what is on its way into one is not read or written in another.
@@ -52,12 +55,48 @@ struct TileGrad {
     int64_t C;           // length of the sum
     int N, K, rows;      // rows: dy's of a dx tile
     int p0, q0;          // dw: first column of dy; first column of q
+    // its half of the steps, `n` each
+    __device__ __forceinline__ Operands half(int group, int n) const {
+      const int64_t first = min((int64_t)n * BK, C), from = group ? first : 0;
+      return {dy + from * (DW ? N : 1), q + from * K, s + from, group ? C - first : first, N, K, rows, p0, q0};
+    }
   };
+  // Steps of a sum, in whole pairs, of one group.
+  __device__ static __forceinline__ int steps(int64_t C) {
+    return (int)((C + 2 * GROUPS * BK - 1) / (2 * GROUPS * BK) * 2);
+  }
 
-  __device__ static __forceinline__ void run(const Operands& o, char* const (&ps)[2], char* const (&qs)[2],
-                                             floatx16 (&acc)[FM][FN]) {
+  // All of a workgroup's sum, in the first group's accumulators.
+  __device__ static __forceinline__ void sum(const Operands& o, char* const (&st)[8], floatx16 (&acc)[FM][FN]) {
+    const int n = steps(o.C);
+    if constexpr (GROUPS == 1) {
+      run(o, n, {st[0], st[1]}, {st[2], st[3]}, acc);
+    } else {
+      const int group = uniform(threadIdx.x >> 8);
+      if (group == 0) run(o.half(0, n), n, {st[0], st[1]}, {st[2], st[3]}, acc);
+      else run(o.half(1, n), n, {st[4], st[5]}, {st[6], st[7]}, acc);
+      wait_barrier<0>();
+      static_assert(FM == 1 && FN == 1 && SMEM_BYTES == 8 * NT * 4, "the second group's accumulators in two of its arrays");
+      if (group) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) reinterpret_cast<float*>(st[4 + v / 8])[v % 8 * NT + threadIdx.x % NT] = acc[0][0][v];
+      }
+      wait_barrier<0>();
+      if (!group) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[0][0][v] += reinterpret_cast<const float*>(st[4 + v / 8])[v % 8 * NT + threadIdx.x];
+      }
+    }
+  }
+
+  struct Two {
+    char* at[2];
+    __device__ __forceinline__ char* operator[](int i) const { return at[i]; }
+  };
+  // nk steps (even; the same in both groups, whose barriers they share)
+  __device__ static __forceinline__ void run(const Operands& o, int nk, const Two& ps, const Two& qs, floatx16 (&acc)[FM][FN]) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    const int lane = opaque_lane(), wave = uniform(threadIdx.x >> 6);
+    const int lane = opaque_lane(), wave = uniform((threadIdx.x >> 6) % NW);
     const int wm = wave / WN, wn = wave % WN;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -80,7 +119,9 @@ struct TileGrad {
       ppiece = ((lane & 7) ^ ((row >> 1) & 7)) << 4;
       poff = (uint32_t)row * (uint32_t)o.N * 2u + ppiece;
     }
-    const __amdgpu_buffer_rsrc_t rp0 = ranged_rsrc(o.dy, DW ? 0 : (uint32_t)o.rows * (uint32_t)o.N * 2u);
+    // (dx: o.C columns of dy's rows from here; the last row ends o.N - o.C columns early, or more)
+    const __amdgpu_buffer_rsrc_t rp0 =
+        ranged_rsrc(o.dy, DW ? 0 : ((uint32_t)(o.rows - 1) * (uint32_t)o.N + (uint32_t)o.C) * 2u);
     auto load_p = [&](char* st, int ks, int t0, int t1) {
       if constexpr (DW) {
         const int64_t c0 = min((int64_t)ks * BK, o.C);
@@ -90,7 +131,7 @@ struct TileGrad {
         for (int t = t0; t < t1; ++t)
           load_lds16(r, st + (t * NW + wave) * 1024, poff, (uint32_t)(t * NW * RP) * (uint32_t)o.N * 2u);
       } else {
-        const uint32_t voff = (int64_t)ks * BK * 2 + ppiece < (int64_t)o.N * 2 ? poff : kNowhere;
+        const uint32_t voff = (int64_t)ks * BK * 2 + ppiece < o.C * 2 ? poff : kNowhere;
 #pragma unroll
         for (int t = t0; t < t1; ++t)
           load_lds16(rp0, st + (t * NW + wave) * 1024, voff,
@@ -179,8 +220,7 @@ struct TileGrad {
     constexpr int NM = FM * FN, ND = FM + (DW ? 2 : 1) * FN;
     bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
     Codes qa, qb;
-    // whole pairs of steps: what is past the sum's end loads as zeros
-    const int nk = (int)((o.C + 2 * BK - 1) / (2 * BK) * 2);
+    // (what is past the sum's end loads as zeros)
     if (nk == 0) return;
     // a step's loads: dy's in two runs, the codes' in three (the last quarter's before the first two of the next step)
     constexpr int P0 = P_LD / 2, Q0 = Q_LD / 3, Q1 = 2 * Q_LD / 3;
@@ -238,19 +278,28 @@ struct TileGrad {
 };
 
 template <class Tile, int ODT, bool SILU>
-__global__ __launch_bounds__(256) void gemm_i8_dx_kernel(GradI8Args a, int ntiles) {
+__global__ __launch_bounds__(256 * Tile::GROUPS) void gemm_i8_dx_kernel(GradI8Args a, int ntiles) {
   __shared__ __attribute__((aligned(1024))) char smem0[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem1[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem2[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem3[Tile::SMEM_BYTES];
+  constexpr int kSecond = Tile::GROUPS == 2 ? Tile::SMEM_BYTES : 16;
+  __shared__ __attribute__((aligned(1024))) char smem4[kSecond];
+  __shared__ __attribute__((aligned(1024))) char smem5[kSecond];
+  __shared__ __attribute__((aligned(1024))) char smem6[kSecond];
+  __shared__ __attribute__((aligned(1024))) char smem7[kSecond];
   char* const stages[4] = {smem0, smem1, smem2, smem3};
-  char *const ps[2] = {smem0, smem1}, *const qs[2] = {smem2, smem3};
+  char* const all[8] = {smem0, smem1, smem2, smem3, smem4, smem5, smem6, smem7};
   const RowTile t = row_tile<Tile::TM>(a.offsets, a.E, a.T, ntiles, a.sync);
   if (t.e < 0) return;
   const int rows = (int)min((int64_t)Tile::TM, t.end - t.row), col0 = t.nt * Tile::TN, cols = min(Tile::TN, a.K - col0);
   floatx16 acc[Tile::FM][Tile::FN];
-  Tile::run({a.dy + t.row * a.N, a.q + (int64_t)t.e * a.N * a.K, a.s + (int64_t)t.e * a.N, a.N, a.N, a.K, rows, 0, col0},
-            ps, qs, acc);
+  Tile::sum({a.dy + t.row * a.N, a.q + (int64_t)t.e * a.N * a.K, a.s + (int64_t)t.e * a.N, a.N, a.N, a.K, rows, 0, col0},
+            all, acc);
+  if (Tile::GROUPS > 1 && threadIdx.x >= 256) {
+    wait_barrier<0>();  // (store_rows')
+    return;
+  }
   char* dst = reinterpret_cast<char*>(a.out) + (t.row * a.K + col0) * (ODT == kBF16 ? 2 : 4);
   const int8_t* pre = SILU ? a.pre + t.row * a.K + col0 : nullptr;
   const float* pre_s = SILU ? a.pre_s + t.row : nullptr;
@@ -290,13 +339,18 @@ __device__ __forceinline__ int expert_of_rank(const GradI8Args& a, int r) {
 // long is not to be left for the end (three groups of 8192 rows in all, 112 tiles each: on average
 // 73 steps of 64 rows a CU, 119 with the experts' tiles dealt to the XCDs as they stand, 57 at best).
 template <class Tile, int ODT>
-__global__ __launch_bounds__(256) void gemm_i8_dw_kernel(GradI8Args a, int ktiles, int ntiles, int splits) {
+__global__ __launch_bounds__(256 * Tile::GROUPS) void gemm_i8_dw_kernel(GradI8Args a, int ktiles, int ntiles, int splits) {
   __shared__ __attribute__((aligned(1024))) char smem0[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem1[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem2[Tile::SMEM_BYTES];
   __shared__ __attribute__((aligned(1024))) char smem3[Tile::SMEM_BYTES];
+  constexpr int kSecond = Tile::GROUPS == 2 ? Tile::SMEM_BYTES : 16;
+  __shared__ __attribute__((aligned(1024))) char smem4[kSecond];
+  __shared__ __attribute__((aligned(1024))) char smem5[kSecond];
+  __shared__ __attribute__((aligned(1024))) char smem6[kSecond];
+  __shared__ __attribute__((aligned(1024))) char smem7[kSecond];
   char* const stages[4] = {smem0, smem1, smem2, smem3};
-  char *const ps[2] = {smem0, smem1}, *const qs[2] = {smem2, smem3};
+  char* const all[8] = {smem0, smem1, smem2, smem3, smem4, smem5, smem6, smem7};
   const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, i = b / kNumQueues;
   const int q = (int)(b % kNumQueues), units = ktiles * ntiles * splits;
   const int most = (units + kNumQueues - 1) / kNumQueues;  // of one expert on one XCD
@@ -318,7 +372,11 @@ __global__ __launch_bounds__(256) void gemm_i8_dw_kernel(GradI8Args a, int ktile
     hi = min(first + steps * (part + 1) / splits * Tile::BK, hi);
   }
   floatx16 acc[Tile::FM][Tile::FN];
-  Tile::run({a.dy + lo * a.N, a.q + lo * a.K, a.s + lo, hi - lo, a.N, a.K, 0, n0, k0}, ps, qs, acc);
+  Tile::sum({a.dy + lo * a.N, a.q + lo * a.K, a.s + lo, hi - lo, a.N, a.K, 0, n0, k0}, all, acc);
+  if (Tile::GROUPS > 1 && threadIdx.x >= 256) {
+    wait_barrier<0>();  // (store_rows')
+    return;
+  }
   char* dst = reinterpret_cast<char*>(a.out) + ((((int64_t)part * a.E + e) * a.K + k0) * a.N + n0) * (ODT == kBF16 ? 2 : 4);
   store_rows<Tile, ODT, false>(
       dst, a.N, min(Tile::TM, a.K - k0), min(Tile::TN, a.N - n0), stages,
@@ -343,8 +401,8 @@ template <class Tile, int ODT>
 static int launch_dx_tile(const GradI8Args& a, hipStream_t s) {
   const int ntiles = (a.K + Tile::TN - 1) / Tile::TN;
   const dim3 grid = row_tile_grid(a.T, a.E, a.offsets, Tile::TM, ntiles);
-  if (a.pre) hipLaunchKernelGGL((gemm_i8_dx_kernel<Tile, ODT, true>), grid, dim3(256), 0, s, a, ntiles);
-  else hipLaunchKernelGGL((gemm_i8_dx_kernel<Tile, ODT, false>), grid, dim3(256), 0, s, a, ntiles);
+  if (a.pre) hipLaunchKernelGGL((gemm_i8_dx_kernel<Tile, ODT, true>), grid, dim3(256 * Tile::GROUPS), 0, s, a, ntiles);
+  else hipLaunchKernelGGL((gemm_i8_dx_kernel<Tile, ODT, false>), grid, dim3(256 * Tile::GROUPS), 0, s, a, ntiles);
   return hipGetLastError();
 }
 template <int ODT>
@@ -363,7 +421,7 @@ static hipError_t launch_dw_tile(const GradI8Args& a, int splits, hipStream_t s)
   const int kt = (a.K + Tile::TM - 1) / Tile::TM, nt = (a.N + Tile::TN - 1) / Tile::TN;
   const int most = (kt * nt * splits + kNumQueues - 1) / kNumQueues;
   const int64_t n = (int64_t)most * a.E * kNumQueues, x = std::min<int64_t>(n, 1 << 20);
-  hipLaunchKernelGGL((gemm_i8_dw_kernel<Tile, ODT>), dim3((uint32_t)x, (uint32_t)((n + x - 1) / x)), dim3(256), 0, s, a, kt, nt,
+  hipLaunchKernelGGL((gemm_i8_dw_kernel<Tile, ODT>), dim3((uint32_t)x, (uint32_t)((n + x - 1) / x)), dim3(256 * Tile::GROUPS), 0, s, a, kt, nt,
                      splits);
   return hipGetLastError();
 }
