@@ -181,9 +181,9 @@ static int launch_tile(const GemmI8Args& a, hipStream_t s) {
 
 template <int ODT>
 static int launch_odt(const GemmI8Args& a, hipStream_t s) {
-  const int64_t big = ((a.T + 255) / 256) * ((a.N + 255) / 256), mid = ((a.T + 127) / 128) * ((a.N + 127) / 128);
-  if (big >= 128) return launch_tile<TileI8<256, 256>, ODT>(a, s);
-  if (mid >= 128) return launch_tile<TileI8<128, 128>, ODT>(a, s);
+  const int side = tile_side(1, a.T, a.N);
+  if (side == 256) return launch_tile<TileI8<256, 256>, ODT>(a, s);
+  if (side == 128) return launch_tile<TileI8<128, 128>, ODT>(a, s);
   return launch_tile<TileI8<64, 64>, ODT>(a, s);
 }
 

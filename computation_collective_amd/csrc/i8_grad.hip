@@ -407,9 +407,9 @@ static int launch_dx_tile(const GradI8Args& a, hipStream_t s) {
 }
 template <int ODT>
 static int launch_dx(const GradI8Args& a, hipStream_t s) {
-  const int64_t big = ((a.T + 255) / 256) * ((a.K + 255) / 256), mid = ((a.T + 127) / 128) * ((a.K + 127) / 128);
-  if (big >= 128) return launch_dx_tile<TileGrad<false, 256, 256>, ODT>(a, s);
-  if (mid >= 128) return launch_dx_tile<TileGrad<false, 128, 128>, ODT>(a, s);
+  const int side = tile_side(1, a.T, a.K);
+  if (side == 256) return launch_dx_tile<TileGrad<false, 256, 256>, ODT>(a, s);
+  if (side == 128) return launch_dx_tile<TileGrad<false, 128, 128>, ODT>(a, s);
   return launch_dx_tile<TileGrad<false, 64, 64>, ODT>(a, s);
 }
 int launch_gemm_i8_dx(const GradI8Args& a, hipStream_t s) {
@@ -438,10 +438,9 @@ static int launch_dw(const GradI8Args& a, hipStream_t s) {
                        a.out, n, splits);
     return hipGetLastError();
   }
-  const int64_t big = (int64_t)a.E * ((a.K + 255) / 256) * ((a.N + 255) / 256);
-  const int64_t mid = (int64_t)a.E * ((a.K + 127) / 128) * ((a.N + 127) / 128);
-  if (big >= 128) return launch_dw_tile<TileGrad<true, 256, 256>, ODT>(a, 1, s);
-  if (mid >= 128) return launch_dw_tile<TileGrad<true, 128, 128>, ODT>(a, 1, s);
+  const int side = tile_side(a.E, a.K, a.N);
+  if (side == 256) return launch_dw_tile<TileGrad<true, 256, 256>, ODT>(a, 1, s);
+  if (side == 128) return launch_dw_tile<TileGrad<true, 128, 128>, ODT>(a, 1, s);
   return launch_dw_tile<TileGrad<true, 64, 64>, ODT>(a, 1, s);
 }
 int launch_gemm_i8_dw(const GradI8Args& a, hipStream_t s) {

@@ -154,7 +154,8 @@ class ExpertsI8:
     forward(x [rows][K] bf16, offsets [E + 1] int64 on the GPU) -> y [rows][K] bf16; group e is
     rows [offsets[e], offsets[e + 1]), as the dispatch leaves them.  backward(dy) -> (dx
     [rows][K] bf16, dw_up [E][K][H] fp32, dw_down [E][H][K] fp32), from the codes of the last
-    forward().  Rows of no group hold nothing in y and dx.  requantise() takes the weights'
+    forward().  Rows of no group are not written: y and dx hold there what an earlier step left,
+    zeros at first.  requantise() takes the weights'
     codes anew, after an optimiser's step on w_up and w_down.  The results are the layer's own
     buffers: the next step writes them again.  check() raises what an operator has reported
     (offsets that fall or leave the rows); it waits for the stream."""
@@ -179,7 +180,7 @@ class ExpertsI8:
         dh = self.dh.out.view(torch.bfloat16)
         self.dw_up = bf.GemmI8Dw(E, rows, H, K, *x, dh, offsets=self.offsets)
         self.dx = bf.GemmI8Dx(E, rows, H, K, dh, *up, offsets=self.offsets)
-        # rows of no group are not written: they hold zeros, never what the memory held before
+        # (rows of no group: never what the memory held before)
         for handle in (self.up, self.down, self.dh, self.dx):
             handle.out.zero_()
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)

@@ -762,8 +762,8 @@ size_t hocf_weights_i8_workspace_bytes(int E, int N, int K);
  *
  *   out[r][n] = xs[r] * ws[e][n] * sum_k xq[r][k] * wq[e][n][k]
  * for the rows r of expert e's group, [offsets[e], offsets[e + 1]).  The sum is
- * exact (32-bit integers); it and the two factors are rounded to fp32, the
- * result to out_dt.  Groups may have any number of rows, also none; rows
+ * exact (32-bit integers) and converted to fp32, times xs, times ws, and the
+ * result rounded to out_dt.  Groups may have any number of rows, also none; rows
  * before the first group and behind the last are not read, and their rows of
  * out are left as they were.
  *

@@ -398,7 +398,8 @@ def test_dx_groups(E, T, offsets):
 
 
 @pytest.mark.parametrize("E,T,N,K,offsets", [(1, 5, 16, 16, None), (1, 333, 136, 1040, None), (1, 4200, 72, 2064, None),
-                                             (3, 700, 64, 208, [5, 300, 300, 690])])
+                                             (1, 8200, 72, 1040, None), (3, 700, 64, 208, [5, 300, 300, 690]),
+                                             (4, 5000, 72, 1808, [3, 1300, 1300, 1301, 4990])])
 @pytest.mark.parametrize("out_dt", [F32, BF16])
 def test_dx_through_silu(E, T, N, K, offsets, out_dt):
     say(f"dx through silu E={E} T={T} N={N} K={K} out={out_dt}")
