@@ -10,6 +10,11 @@
 // codes, taken to bf16 on their way through registers to LDS, next to 64 rows
 // (dw) or 64 columns (dx) of dy, which go straight to LDS.  Operands whose
 // summed index is not adjacent in LDS are turned by the transposing LDS read.
+//
+// Bound by the matrix instructions and by what issues beside them: of a step's 3340 cycles (256 x
+// 256, dx) 2048 multiply, some 300 go to LDS reads, conversions and barriers, and about 50 to each of the
+// 18 loads, for which a wave holds its matrix pipe.  8192 rows, 4096 -> 1792: dx 127 us, through SiLU 150, dw
+// (fp32) 144 as one matrix in two parts.
 #include "i8_tiles.hpp"
 
 namespace hocf {
