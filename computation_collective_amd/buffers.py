@@ -662,6 +662,8 @@ class QuantI8(_Moe):
     def __init__(self, T, K, x, act=hocf.HOCF_ACT_NONE, keep=False):
         ld, dev = _rows_apart(x, T, K), x.device
         _on(dev)
+        if keep and act == hocf.HOCF_ACT_NONE:
+            raise ValueError("without an activation the codes are those of x already")
         self.x = x
         self.codes = torch.empty((T, K), dtype=torch.int8, device=dev)
         self.scales = torch.empty(T, dtype=torch.float32, device=dev)

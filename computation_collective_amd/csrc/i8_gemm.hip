@@ -64,7 +64,8 @@ struct TileI8 {
       load_a(st, k0);
       load_b(st, k0);
     };
-    // fragment kk of block row i: bytes 32 kk + 16 (lane / 32) of row 32 i + lane mod 32 (blocks: 4 KB apart; kk: two bits of the piece)
+    // fragment kk of block row i: bytes 32 kk + 16 (lane / 32) of row 32 i + lane mod 32 (blocks are 4 KB
+    // apart, kk is two bits of the piece)
     const int m = lane & 31, first = m * BK + (((lane >> 5) ^ ((m >> 1) & 7)) << 4);
     const int afirst = wm * WTM * BK + first, bfirst = A_BYTES + wn * WTN * BK + first;
     auto frags = [&](const char* st, int kk, i32x4 (&a)[FM], i32x4 (&b)[FN]) {

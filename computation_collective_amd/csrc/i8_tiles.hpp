@@ -168,11 +168,12 @@ __device__ __forceinline__ RowTile row_tile(const int64_t* offsets, int E, int64
 
 // The side of the tiles for `groups` results of rows x columns each: 256 where its tiles fill five
 // eighths of the turns of 256 CUs that they take, else 128 where there are enough of them, else 64.
-// Measured with 256 and 128 (tiles of 256): 8-bit product 4096 x 1024 -> 2048 (128) 21.8 and 14.3 us, 6144 x 4096 ->
-// 1792 (168) 58.6 and 60.6, 8192 x 8192 -> 8192 (1024) 439 and 496; dx 4096 x 1024 -> 2048 34 and 26, 6144 x 4096 ->
-// 1792 117 and 131; two turns: product 9216 x 2048 -> 2048 (288) 63 and 52.  With 128 and 64 (tiles of 128): product 2000 x 1024 -> 1024 (128) 7.4 and 6.5, 3000 x 2048 -> 1024
-// (192) 11.2 and 13.0; dx 1500 x 1000 -> 1040 (108) 14.7 and 13.1, 3000 x 2048 -> 1024 (192) 26.8 and 34; dw
-// 512 x 1536 x 1536 (144) 11.2 and 13.5.
+// Measured with 256 and 128 (in brackets the tiles of 256): 8-bit product 4096 x 1024 -> 2048
+// (128) 21.8 and 14.3 us, 6144 x 4096 -> 1792 (168) 58.6 and 60.6, 9216 x 2048 -> 2048 (288) 63 and 52,
+// 8192 x 8192 -> 8192 (1024) 439 and 496; dx 4096 x 1024 -> 2048 34 and 26, 6144 x 4096 -> 1792 117
+// and 131.  With 128 and 64 (the tiles of 128): product 2000 x 1024 -> 1024 (128) 7.4 and 6.5, 3000 x
+// 2048 -> 1024 (192) 11.2 and 13.0; dx 1500 x 1000 -> 1040 (108) 14.7 and 13.1, 3000 x 2048 -> 1024
+// (192) 26.8 and 34; dw 512 x 1536 x 1536 (144) 11.2 and 13.5.
 inline int tile_side(int64_t groups, int64_t rows, int64_t columns) {
   const int64_t big = groups * ((rows + 255) / 256) * ((columns + 255) / 256);
   if (big * 8 >= (big + 255) / 256 * 256 * 5) return 256;

@@ -742,3 +742,32 @@ def test_far_experts():
     a = run(bf.GemvI8(4, 1, E, 0, N, K, xq[:4], xs[:4], e, wq, ws))
     b = run(bf.GemvI8(4, 1, 1, 0, N, K, xq[:4], xs[:4], None, wq[-1:], ws[-1:]))
     assert torch.equal(a.out, b.out)
+
+
+def test_many_rows():
+    """More workgroups than one dimension of a grid takes here (2^20): rows to codes, back, and their products."""
+    say("many rows")
+    T, K, N = 280_000_000, 16, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    few = torch.randn((1000, K), generator=g, device="cuda").bfloat16()
+    x = torch.zeros((T // 40, K), dtype=torch.bfloat16, device="cuda")      # 7 million rows, four a workgroup
+    at = torch.randint(0, len(x), (1000,), generator=g, device="cuda").unique()
+    at[-1] = len(x) - 1
+    x[at] = few[:len(at)]
+    h, want = run(bf.QuantI8(len(x), K, x)), run(bf.QuantI8(len(at), K, few[:len(at)]))
+    assert torch.equal(h.codes[at], want.codes) and torch.equal(h.scales[at], want.scales)
+    assert int((h.codes != 0).any(1).sum()) <= len(at) and not h.scales.isnan().any()
+    q = torch.zeros((T, K), dtype=torch.int8, device="cuda")
+    s = torch.ones(T, dtype=torch.float32, device="cuda")
+    at = torch.randint(0, T, (1000,), generator=g, device="cuda").unique()
+    at[-1] = T - 1
+    q[at] = dev(codes((len(at), K), 2))
+    d = run(bf.DequantI8(T, K, q, s))
+    assert torch.equal(d.out[at], run(bf.DequantI8(len(at), K, q[at], s[at])).out)
+    assert int((d.out != 0).any(1).sum()) <= len(at)
+    del d
+    torch.cuda.empty_cache()
+    wq, ws = dev(codes((1, N, K), 3)), dev(scales((1, N), 4))
+    h = run(bf.GemmI8(1, T, N, K, q, s, wq, ws))
+    assert torch.equal(h.out[at], run(bf.GemmI8(1, len(at), N, K, q[at], s[at], wq, ws)).out)
+    assert int((h.out != 0).any(1).sum()) <= len(at)

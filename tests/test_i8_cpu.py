@@ -163,6 +163,8 @@ def test_handles_refuse():
         bf.QuantI8(4, 32, x[:, ::2])
     with pytest.raises(ValueError, match="GPU"):
         bf.DequantI8(4, 64, q, s)
+    with pytest.raises(ValueError, match="GPU"):
+        bf.QuantI8(4, 64, x, keep=True)
     with pytest.raises(TypeError):
         bf.DequantI8(4, 64, q.float(), s)
     with pytest.raises(ValueError, match="contiguous"):
