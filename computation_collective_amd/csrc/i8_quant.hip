@@ -13,7 +13,7 @@
 // A row stays in registers between its largest number and its codes: read once.
 // Bound by memory (8192 x 4096 bf16 20 us, 5.0 TB/s; reading 32768 x 1792 back 27 us,
 // 6.4 TB/s with codes from the Infinity Cache), but for SiLU with both sides kept, whose
-// vector instructions take as long (32768 x 1792: 59 us where memory would take 49).
+// vector instructions take as long (32768 x 1792: 56 us where memory would take 49).
 #include <algorithm>
 
 #include "i8.hpp"
@@ -167,8 +167,13 @@ __device__ __forceinline__ Eight<kF32> silu8(const Eight<kF32>& e) {
   return r;
 }
 
-template <int W>
+template <int W, bool HALF>
 __device__ __forceinline__ uint32_t row_largest(uint32_t m, uint32_t* s_max, int wave) {
+  if constexpr (HALF) {
+    uint32_t a, b;
+    across<16>((uint32_t)row_max<16>((int)m), a, b);
+    return max(a, b);
+  }
   m = (uint32_t)row_max<64>((int)m);  // (magnitudes: the sign bit is clear)
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) s_max[wave] = m;
@@ -179,19 +184,22 @@ __device__ __forceinline__ uint32_t row_largest(uint32_t m, uint32_t* s_max, int
   return m;
 }
 
-// W waves a row (1 or 4), up to C pieces of eight numbers a lane; LOOP: rows of any
-// length, read twice.
+// W waves a row (1 or 4), or HALF of one, up to C pieces of eight numbers a lane; LOOP: rows
+// of any length, read twice.
 // KEEP only with an activation: the codes of x and of act(x).
-template <int DT, int ACT, bool KEEP, int W, int C, bool LOOP>
+template <int DT, int ACT, bool KEEP, int W, int C, bool LOOP, bool HALF>
 __global__ __launch_bounds__(kQThreads) void quant_kernel(QuantI8Args a) {
   __shared__ uint32_t s_max[2][4];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int64_t row = W == 1 ? flat_block() * 4 + wave : flat_block();
+  const int64_t row = HALF     ? flat_block() * 8 + wave * 2 + (lane >> 5)
+                      : W == 1 ? flat_block() * 4 + wave
+                               : flat_block();
   if (row >= a.T) return;  // (W = 4: the workgroup's row)
   const char* x = reinterpret_cast<const char*>(a.x) + row * a.ld * (DT == kBF16 ? 2 : 4);
-  const int k0 = (W == 1 ? lane : (int)threadIdx.x) * 8;
-  constexpr int kStep = W * 512;
+  const int k0 = (HALF ? lane & 31 : W == 1 ? lane : (int)threadIdx.x) * 8;
+  constexpr int kStep = HALF ? 256 : W * 512;
   static_assert(ACT == kSilu || !KEEP, "one side only");
+  static_assert(!HALF || (W == 1 && !LOOP), "half of one wave");
   Eight<DT> v[LOOP ? 1 : C], p[KEEP && !LOOP ? C : 1];
   uint32_t m = 0, mp = 0;
   if constexpr (LOOP) {
@@ -218,9 +226,9 @@ __global__ __launch_bounds__(kQThreads) void quant_kernel(QuantI8Args a) {
         m = largest(v[c], m);
       }
   }
-  const Scale s = scale_of(row_largest<W>(of_pair<DT>(m), s_max[0], wave));
+  const Scale s = scale_of(row_largest<W, HALF>(of_pair<DT>(m), s_max[0], wave));
   Scale sp = s;
-  if constexpr (KEEP) sp = scale_of(row_largest<W>(of_pair<DT>(mp), s_max[1], wave));
+  if constexpr (KEEP) sp = scale_of(row_largest<W, HALF>(of_pair<DT>(mp), s_max[1], wave));
   int8_t* q = a.codes + row * a.K;
   int8_t* qp = KEEP ? a.pre_codes + row * a.K : nullptr;
   auto put = [&](int k, const Eight<DT>& pre, const Eight<DT>& act) {
@@ -238,16 +246,16 @@ __global__ __launch_bounds__(kQThreads) void quant_kernel(QuantI8Args a) {
     for (int c = 0; c < C; ++c)
       if (k0 + c * kStep < a.K) put(k0 + c * kStep, p[KEEP ? c : 0], v[c]);
   }
-  if (lane == 0 && (W == 1 || wave == 0)) {
+  if ((HALF ? (lane & 31) == 0 : lane == 0) && (W == 1 || wave == 0)) {
     a.scales[row] = s.s;
     if constexpr (KEEP) a.pre_scales[row] = sp.s;
   }
 }
 
-template <int DT, int ACT, bool KEEP, int W, int C, bool LOOP>
+template <int DT, int ACT, bool KEEP, int W, int C, bool LOOP, bool HALF = false>
 static int launch_q(const QuantI8Args& a, hipStream_t s) {
-  const int64_t grid = W == 1 ? (a.T + 3) / 4 : a.T;
-  hipLaunchKernelGGL((quant_kernel<DT, ACT, KEEP, W, C, LOOP>), flat_grid(grid), dim3(kQThreads), 0, s, a);
+  const int64_t grid = HALF ? (a.T + 7) / 8 : W == 1 ? (a.T + 3) / 4 : a.T;
+  hipLaunchKernelGGL((quant_kernel<DT, ACT, KEEP, W, C, LOOP, HALF>), flat_grid(grid), dim3(kQThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -256,6 +264,14 @@ static int launch_q(const QuantI8Args& a, hipStream_t s) {
 template <int DT, int ACT, bool KEEP>
 static int launch_act(const QuantI8Args& a, hipStream_t s) {
   if (a.T >= 2048 && a.K <= 4096) {
+    // Half a wave a row where a whole one's last pass would be half empty, and what bounds the kernel is
+    // vector instructions (bf16, SiLU with both sides, whole -> half a wave: 65536 x 768 53 -> 42 us,
+    // 32768 x 1792 51 -> 47; 65536 x 256 without SiLU 18 -> 13).  Longer rows without SiLU are bound by
+    // memory (32768 x 1792 32 -> 34), and of few a lane's time counts (2048 x 1792 6.8 -> 7.7).
+    const bool half = a.K % 512 && a.K % 512 <= 256;
+    if (half && a.K <= 1024) return launch_q<DT, ACT, KEEP, 1, 4, false, true>(a, s);
+    if constexpr (ACT == kSilu)
+      if (half && a.K <= 2048 && a.T >= 16384) return launch_q<DT, ACT, KEEP, 1, 8, false, true>(a, s);
     if (a.K <= 1024) return launch_q<DT, ACT, KEEP, 1, 2, false>(a, s);
     if (a.K <= 2048) return launch_q<DT, ACT, KEEP, 1, 4, false>(a, s);
     return launch_q<DT, ACT, KEEP, 1, 8, false>(a, s);

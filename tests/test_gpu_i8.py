@@ -154,6 +154,25 @@ def test_quant_silu(T, K, dt, keep):
         same(h.pre_scales, s)
 
 
+@pytest.mark.parametrize("T,K", [(2049, 16), (2051, 256), (2055, 592), (2049, 768), (2053, 1040), (16385, 1040),
+                                 (16389, 1792)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_quant_halves_of_waves(T, K, dt):
+    """Odd numbers of rows at lengths where two rows share a wave, each row of its own scale, some not finite."""
+    say(f"quant halves of waves T={T} K={K} dt={dt}")
+    g = rng(T + K)
+    x = g.standard_normal((T, K)).astype(np.float32) * np.exp2(g.integers(-20, 20, (T, 1))).astype(np.float32)
+    x[5, 3], x[8, K - 1], x[T - 1, 0], x[10] = np.nan, np.inf, -np.inf, 0
+    x = dev(x, TORCH[dt])
+    h = run(bf.QuantI8(T, K, x))
+    q, s = ref.quant(host(x))
+    same(h.codes, q)
+    same(h.scales, s)
+    h = run(bf.QuantI8(T, K, x, act=SILU, keep=True))
+    same(h.pre_codes, q)
+    same(h.pre_scales, s)
+
+
 def test_silu_far():
     """SiLU far from zero: rows that fp32's exponential alone would lose or overflow."""
     say("silu far")
