@@ -726,9 +726,8 @@ hocf_status hocf_w4_pack(int E, int N, int K, int group, const uint8_t* codes, c
  * pre_codes, the activation function's part of hocf_gemm_i8_dx).
  *
  *   x        [T][ld] dt, the first K of each row (K <= ld <= 2^24; rows start on 16 bytes)
- *   act      HOCF_ACT_NONE, or HOCF_ACT_SILU: a = x / (1 + exp(-x)) rounded to dt
- *            (dt F32: computed in 64 bits; BF16: in 32, its rounding may go the other
- *            way within 2^-20 of a border)
+ *   act      HOCF_ACT_NONE, or HOCF_ACT_SILU: a = x / (1 + exp(-x)), computed in 64 bits
+ *            and rounded to dt (BF16: in 32 bits, with the same result for every number)
  *   codes    [T][K] int8          scales  [T] fp32
  *   pre_codes, pre_scales   NULL, or (with an activation) the same for x itself
  * Supported: dt F32 or BF16; K a multiple of 16 up to 65536; 0 <= T < 2^31.
