@@ -327,9 +327,9 @@ __global__ __launch_bounds__(256 * Tile::GROUPS) void gemm_i8_dx_kernel(GradI8Ar
 __device__ __forceinline__ int expert_of_rank(const GradI8Args& a, int r) {
   if (a.E > 64 || !a.offsets) return r;
   const int lane = threadIdx.x & 63;
-  int64_t lo = 0, hi = -1;
-  if (lane < a.E) group_bounds(a.offsets, lane, a.T, &lo, &hi);
-  const int n = (int)(hi - lo);  // (-1 past the last expert)
+  int lo, hi, upto = 0;
+  lane_bounds(a.offsets, a.E, a.T, 0, false, &upto, &lo, &hi);  // (where they fall: any order, the same for all)
+  const int n = lane < a.E ? hi - lo : -1;
   int before = 0;
   for (int i = 0; i < a.E; ++i) {
     const int o = __shfl(n, i, 64);
@@ -368,8 +368,6 @@ __global__ __launch_bounds__(256 * Tile::GROUPS) void gemm_i8_dw_kernel(GradI8Ar
   if (a.offsets) {
     group_bounds(a.offsets, e, a.T, &lo, &hi);
     if (in == 0 && threadIdx.x == 0 && (lo != a.offsets[e] || hi != a.offsets[e + 1])) report_status(a.sync, kErrBadIndex);
-    lo = uniform64(lo);
-    hi = uniform64(hi);
   }
   if (splits > 1) {
     const int64_t steps = (hi - lo + Tile::BK - 1) / Tile::BK, first = lo;

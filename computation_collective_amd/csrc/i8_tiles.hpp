@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "i8.hpp"
+#include "lanes.hpp"
 #include "mfma_tile.hpp"
 #include "publish.hpp"
 #include "sync.hpp"
@@ -78,11 +79,46 @@ __device__ __forceinline__ void four_steps(int n, S step) {
   }
 }
 
-// The bounds of group e within [0, T], whatever the offsets hold.
+// An offset within [0, T] (T < 2^31).
+__device__ __forceinline__ int within(int64_t o, int64_t T) { return (int)(o < 0 ? 0 : o > T ? T : o); }
+
+// Group bounds, whatever the offsets hold: each counts as the largest of itself and those before it, within
+// [0, T].  So groups follow one another and share no row, also where the offsets fall.
+
+// Of one group e (uniform).  Every lane takes part.
 __device__ __forceinline__ void group_bounds(const int64_t* offsets, int e, int64_t T, int64_t* lo, int64_t* hi) {
-  const int64_t a = offsets[e], b = offsets[e + 1];
-  *lo = a < 0 ? 0 : a > T ? T : a;
-  *hi = b < *lo ? *lo : b > T ? T : b;
+  int m = 0;
+  for (int i = threadIdx.x & 63; i - (int)(threadIdx.x & 63) <= e; i += 256) {
+#pragma unroll
+    for (int u = 0; u < 256; u += 64) m = max(m, within(offsets[min(i + u, e)], T));
+  }
+  m = uniform(row_max<64>(m));
+  *lo = m;
+  *hi = max(m, within(offsets[e + 1], T));
+}
+
+// Of groups e0 + lane, 64 at a time (past the last: no rows).  Only where some offset of the list falls or leaves
+// [0, T] (`fall`, uniform) do those before e0 matter: `upto` is their largest, 0 at first.  Whether this
+// group's own do.
+__device__ __forceinline__ bool lane_bounds(const int64_t* offsets, int E, int64_t T, int e0, bool fall, int* upto, int* lo,
+                                            int* hi) {
+  const int lane = threadIdx.x & 63, e = min(e0 + lane, E);
+  const int64_t a = offsets[e], b = offsets[min(e + 1, E)];
+  *lo = within(a, T);
+  *hi = max(*lo, within(b, T));
+  const bool own = *lo != a || *hi != b;
+  if (fall) {
+    int m = max(*hi, *upto);
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(m, d, 64);
+      if (lane >= d) m = max(m, o);
+    }
+    const int before = __shfl_up(m, 1, 64);
+    *lo = lane ? before : max(*lo, *upto);
+    *hi = m;
+    *upto = uniform(__shfl(m, 63, 64));
+  }
+  return own;
 }
 
 struct RowTile {
@@ -99,23 +135,28 @@ __device__ __forceinline__ RowTile row_tile(const int64_t* offsets, int E, int64
   const int lane = threadIdx.x & 63;
   RowTile t{0, T, 0, 0};
   int64_t total, skip = 0;
+  bool fall = false;
+  auto tiles = [](int lo, int hi) { return (int)(((uint32_t)(hi - lo) + TM - 1) / TM); };
   if (!offsets) {
     total = (T + TM - 1) / TM;
   } else {
-    total = 0;
-    bool bad = false;
+    int n = 0, upto = 0, lo, hi;
+    bool own = false;
     for (int e0 = 0; e0 < E; e0 += 64) {
-      int n = 0;
-      if (e0 + lane < E) {
-        int64_t lo, hi;
-        group_bounds(offsets, e0 + lane, T, &lo, &hi);
-        bad |= lo != offsets[e0 + lane] || hi != offsets[e0 + lane + 1];
-        n = (int)((hi - lo + TM - 1) / TM);
-      }
-      for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d, 64);
-      total += n;
+      own |= lane_bounds(offsets, E, T, e0, false, &upto, &lo, &hi);
+      n += tiles(lo, hi);
     }
-    if (blockIdx.x == 0 && blockIdx.y == 0 && bad) report_status(sync, kErrBadIndex);
+    fall = __ballot(own) != 0;
+    if (fall) {
+      if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_status(sync, kErrBadIndex);
+      n = 0;
+      for (int e0 = 0; e0 < E; e0 += 64) {
+        lane_bounds(offsets, E, T, e0, true, &upto, &lo, &hi);
+        n += tiles(lo, hi);
+      }
+    }
+    for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d, 64);
+    total = n;
   }
   total = uniform64(total) * ntiles;
   const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;  // (a row of the grid is whole turns of the XCDs)
@@ -129,10 +170,11 @@ __device__ __forceinline__ RowTile row_tile(const int64_t* offsets, int E, int64
   if (offsets) {
     // the group that holds tile `at`: tiles before it are skip * ntiles
     bool found = false;
+    int last = 0;
     for (int e0 = 0; e0 < E && !found; e0 += 64) {
-      int64_t lo = 0, hi = 0;
-      if (e0 + lane < E) group_bounds(offsets, e0 + lane, T, &lo, &hi);
-      const int n = (int)((hi - lo + TM - 1) / TM);
+      int lo, hi;
+      lane_bounds(offsets, E, T, e0, fall, &last, &lo, &hi);
+      const int n = tiles(lo, hi);
       int upto = n;
       for (int d = 1; d < 64; d <<= 1) {
         const int o = __shfl_up(upto, d, 64);
@@ -144,8 +186,8 @@ __device__ __forceinline__ RowTile row_tile(const int64_t* offsets, int E, int64
         t.e = uniform(e0 + l);
         skip = uniform64(skip + __shfl(upto, l, 64) - __shfl(n, l, 64));
         mtiles = uniform(__shfl(n, l, 64));
-        t.row = uniform64(__shfl(lo, l, 64));
-        t.end = uniform64(__shfl(hi, l, 64));
+        t.row = uniform(__shfl(lo, l, 64));
+        t.end = uniform(__shfl(hi, l, 64));
         found = true;
       } else {
         skip = uniform64(skip + __shfl(upto, 63, 64));
@@ -162,7 +204,6 @@ __device__ __forceinline__ RowTile row_tile(const int64_t* offsets, int E, int64
   t.e = uniform(t.e);
   t.nt = uniform(t.nt);
   t.row = uniform64(t.row);
-  if (t.row >= t.end) t.e = -1;  // (offsets that overlap)
   return t;
 }
 

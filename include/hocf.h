@@ -770,8 +770,9 @@ size_t hocf_weights_i8_workspace_bytes(int E, int N, int K);
  *   offsets  [E + 1] int64 (device), rising from 0 or more to T or less; or NULL
  *            (E = 1): every row.  As hocf_a2a_gemm writes them.
  *   out [T][N] out_dt
- * Offsets that fall, or leave [0, T], are taken as the nearest that do not, and
- * HOCF_ERR_BAD_INDEX goes to the status word.
+ * Where offsets fall, or leave [0, T], each counts as the largest of itself and those
+ * before it, within [0, T] (so no row is in two groups), and HOCF_ERR_BAD_INDEX goes
+ * to the status word.
  * Supported: out_dt F32 or BF16; 1 <= E <= 1024; N a multiple of 8 and K of 16,
  * up to 65536; 0 <= T < 2^31.
  * ---------------------------------------------------------------------- */

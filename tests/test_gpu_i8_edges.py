@@ -1,5 +1,6 @@
 """The 8-bit integer operators on the GPU where test_gpu_i8.py does not reach:
-every bf16 number through SiLU, and SiLU in every form of the kernel."""
+every bf16 number through SiLU, SiLU in every form of the kernel, and offsets
+that fall over three groups and more."""
 
 import numpy as np
 import pytest
@@ -7,8 +8,9 @@ import torch
 
 import i8_ref as ref
 from computation_collective_amd import buffers as bf
-from test_gpu_i8 import BF16, F32, SILU, TORCH, dev, rng, same
-from test_gpu_moe import host, run, say
+from computation_collective_amd import hocf
+from test_gpu_i8 import BAD_INDEX, BF16, F32, GEMM_STEPS, SILU, TORCH, check_rows, codes, dev, rng, same, scales
+from test_gpu_moe import host, near, run, say
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +73,73 @@ def test_silu_codes_are_the_definitions(T, K, dt, keep):
         q, s = ref.quant(x)
         same(h.pre_codes, q)
         same(h.pre_scales, s)
+
+
+# ------------------------------------------------------------------------------ offsets that fall
+
+def counted(offsets, T):
+    """The offsets that the header has in their place: each the largest of itself and those before it, within [0, T]."""
+    return np.maximum.accumulate(np.clip(np.array(offsets, object), 0, T)).astype(np.int64).tolist()
+
+
+class Guarded:
+    """A tensor of `shape` inside a larger one, all NaN: what is written beside it shows."""
+
+    def __init__(self, shape, out_dt):
+        n, self.guard = int(np.prod(shape)), 8192
+        self.all = torch.full((n + 2 * self.guard,), float("nan"), dtype=TORCH[out_dt], device="cuda")
+        self.out = self.all[self.guard:self.guard + n].view(shape)
+
+    def intact(self):
+        return bool(self.all[:self.guard].isnan().all() and self.all[-self.guard:].isnan().all())
+
+
+FALLING = [
+    (3, 90, 72, 64, [0, 70, 50, 90]), (4, 90, 72, 64, [-5, 40, 200, 30, 90]), (4, 90, 72, 64, [80, 20, 60, 85, 10]),
+    (5, 700, 136, 144, [0, 700, 0, 700, 0, 700]), (5, 700, 136, 144, [0, 300, 100, 400, 350, 1 << 40]),
+    (130, 400, 72, 80, [min(400, 4 * i) if i % 50 else -i for i in range(131)]),     # falls at the 64-group borders' sides too
+    (200, 900, 72, 80, [900 - 5 * i if 64 <= i < 70 else 5 * (i - 1) for i in range(201)]),
+    (4, 5000, 1800, 208, [3, 2600, 2500, 4000, 3990]), (3, 2400, 1032, 272, [0, 1100, 1037, 2400]),
+    (3, 9000, 136, 80, [10, 6000, 20, 8990]),                                        # (dw's sums in parts)
+    (3, 0, 72, 64, [0, 5, -1, 0]), (2, 90, 72, 64, [-(1 << 63), (1 << 63) - 1, -(1 << 63)])]
+
+
+@pytest.mark.parametrize("E,T,N,K,offsets", FALLING)
+@pytest.mark.parametrize("out_dt", [F32, BF16])
+def test_offsets_that_fall(E, T, N, K, offsets, out_dt):
+    """The products and both gradients as the header has them, each row in one group, nothing beside the outputs
+    written, and the same bits again."""
+    say(f"offsets that fall E={E} T={T} out={out_dt} {offsets[:6]}")
+    c = counted(offsets, T)
+    xq, wq, xs, ws = codes((T, K), 1), codes((E, N, K), 2), scales(T, 3), scales((E, N), 4)
+    dy = dev(rng(5).standard_normal((T, N)).astype(np.float32), torch.bfloat16)
+    off, word = dev(np.array(offsets, np.int64)), torch.zeros(1, dtype=torch.int32, device="cuda")
+    d = [dev(a) for a in (xq, xs, wq, ws)]
+    size = hocf.hocf_gemm_i8_dw_workspace_bytes(E, T, N, K)
+    space = torch.empty(max(16, size), dtype=torch.uint8, device="cuda")
+    st = torch.cuda.current_stream()
+
+    def call(entry, shape, *args):
+        got = []
+        for again in range(2):
+            word.zero_()
+            g = Guarded(shape, out_dt)
+            hocf.check(entry(E, T, N, K, out_dt, *args, off, *(() if entry is not hocf.hocf_gemm_i8_dx else (None, None)), g.out,
+                             hocf.sync(1, space, size, status=word), st))
+            torch.cuda.synchronize()
+            assert g.intact() and (word.item() == BAD_INDEX or (T == 0 and entry is not hocf.hocf_gemm_i8_dw))
+            got.append(g.out)
+        assert torch.equal(got[0].isnan(), got[1].isnan()) and torch.equal(got[0].nan_to_num(), got[1].nan_to_num())
+        return got[0]
+
+    out = call(hocf.hocf_gemm_i8, (T, N), *d)
+    if T:
+        want = ref.gemm(xq, xs, wq, ws, c)
+        check_rows(out, want, np.abs(want), TORCH[out_dt], GEMM_STEPS)
+    dx = call(hocf.hocf_gemm_i8_dx, (T, K), dy, d[2], d[3])
+    if T:
+        want, room = ref.dx(host(dy), wq, ws, c)
+        check_rows(dx, want, room, TORCH[out_dt], N)
+    dw = call(hocf.hocf_gemm_i8_dw, (E, K, N), d[0], d[1], dy)
+    want, room = ref.dw(xq, xs, host(dy), E, c)
+    near(dw, want, room, TORCH[out_dt], max(1, T))
