@@ -19,10 +19,16 @@
 
 namespace hocf {
 
-// x / (1 + exp(-x)), its derivative.
+// The derivative of x / (1 + exp(-x)) at a bf16 number h: p (1 + h (1 - p)), p = 1 / (1 + exp(-h)).  With z =
+// exp(-|h|), p and 1 - p are 1 / (1 + z) and z / (1 + z), or the other way round: neither is a difference.  h
+// times the first 16 bits of log2(e) is exact, so the exponential's error does not grow with h; the rest of
+// log2(e) is the factor exp(-|h| rest) = 1 - |h| rest, off by 2^-23 at most where z is not zero (below |h| = 88).
 __device__ __forceinline__ float silu_slope(float h) {
-  const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(h * -1.44269504f));
-  return p * fmaf(h, 1.0f - p, 1.0f);
+  constexpr double kHead = 47274.0 / 32768, kRest = (1.4426950408889634 - kHead) * 0.6931471805599453;
+  float z = __builtin_amdgcn_exp2f(fabsf(h) * (float)-kHead);
+  z = fmaf(z, fabsf(h) * (float)-kRest, z);
+  const float i = __builtin_amdgcn_rcpf(1.0f + z), zi = z * i;
+  return (h < 0.0f ? zi : i) * fmaf(h, h < 0.0f ? i : zi, 1.0f);
 }
 
 // A TR x TC tile (rows x columns of the result) of four waves, summed over steps of 64.

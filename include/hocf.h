@@ -806,6 +806,7 @@ hocf_status hocf_gemv_i8(int R, int rows_per_x, int E, int e0, int N, int K, hoc
  * identity).  With pre_codes, the rows came through SiLU from h, which
  * was kept in codes, and the result is h's gradient:
  *   dx[r][k] *= p (1 + h (1 - p)),  p = 1 / (1 + exp(-h)),  h = bf16(pre_codes[r][k] * pre_scales[r])
+ * (exp(-|h|) below 2^-126 counts as zero: |h| beyond 87)
  *
  *   dy  [T][N] bf16    wq, ws, offsets  as hocf_gemm_i8 takes them
  *   pre_codes, pre_scales  NULL, or [T][K] int8 and [T] fp32 as hocf_quant_i8 keeps them

@@ -1,6 +1,6 @@
 """The 8-bit integer operators on the GPU where test_gpu_i8.py does not reach:
-every bf16 number through SiLU, SiLU in every form of the kernel, and offsets
-that fall over three groups and more."""
+every bf16 number through SiLU, SiLU in every form of the kernel, offsets that
+fall over three groups and more, and SiLU's derivative far from zero."""
 
 import numpy as np
 import pytest
@@ -143,3 +143,36 @@ def test_offsets_that_fall(E, T, N, K, offsets, out_dt):
     dw = call(hocf.hocf_gemm_i8_dw, (E, K, N), d[0], d[1], dy)
     want, room = ref.dw(xq, xs, host(dy), E, c)
     near(dw, want, room, TORCH[out_dt], max(1, T))
+
+
+# ------------------------------------------------------------------------------ SiLU's derivative
+
+@pytest.mark.parametrize("T,N,K", [(2, 8, 65536), (300, 16, 1024)])
+def test_slope_of_every_code(T, N, K):
+    """dx through SiLU at h from -300 to 300, beside its roots and signs: within a fixed number of roundings of the
+    formula.  With z = exp(-|h|), i = 1 / (1 + z), p is i or z i and 1 - p the other.  Errors in half steps (2^-24):
+    z 5 (the instruction 2, its argument's constant 2, a product 1), 1 + z 1, i 2, z i 1: p and 1 - p 9 at most each; 1 + h (1 - p)
+    1 more, the slope 1, its product with the sum 1.  In all 21 of |sum| p (1 + |h| (1 - p)).  A z below 2^-126 is zero."""
+    say(f"slope T={T} N={N} K={K}")
+    g = rng(T)
+    dy = dev(g.standard_normal((T, N)).astype(np.float32), torch.bfloat16)
+    wq, ws = codes((1, N, K), 2), scales((1, N), 3)
+    pre = g.integers(-127, 128, (T, K)).astype(np.int8)
+    pre_s = (10.0 ** g.uniform(-4, np.log10(300 / 127), T)).astype(np.float32)
+    pre_s[0] = np.float32(1.0)
+    h = run(bf.GemmI8Dx(1, T, N, K, dy, dev(wq), dev(ws), pre_codes=dev(pre), pre_scales=dev(pre_s), out_dt=F32))
+    want, _ = ref.dx(host(dy), wq, ws, None, (pre, pre_s))
+    plain, size = ref.dx(host(dy), wq, ws)
+    at = ref.held(pre, pre_s)
+    z = np.exp(-np.abs(at))
+    p, rest = np.where(at < 0, z, 1) / (1 + z), np.where(at < 0, 1, z) / (1 + z)
+    # the sum's own roundings (N of its terms' sizes) meet the slope, whose roots they do not know
+    slope = np.abs(ref.silu_slope(at))
+    sums = N * size * 2.0 ** -24
+    room = sums * slope + 21 * 2.0 ** -24 * (np.abs(plain) + sums) * p * (1 + np.abs(at) * rest)
+    room = room * (1 + 2.0 ** -10) + 2.0 ** -126 * (1 + (1 + np.abs(at)) * size)
+    got = host(h.out)
+    off = np.abs(got - want) - room
+    worst = np.unravel_index(np.argmax(off), off.shape)
+    assert off[worst] <= 0, (at[worst], got[worst], want[worst], room[worst])
+    assert np.isfinite(got).all()
