@@ -1,6 +1,7 @@
 """The 8-bit integer operators on the GPU where test_gpu_i8.py does not reach:
 every bf16 number through SiLU, SiLU in every form of the kernel, offsets that
-fall over three groups and more, and SiLU's derivative far from zero."""
+fall over three groups and more, SiLU's derivative far from zero, and the
+decode products' forms of several blocks of columns."""
 
 import numpy as np
 import pytest
@@ -176,3 +177,40 @@ def test_slope_of_every_code(T, N, K):
     worst = np.unravel_index(np.argmax(off), off.shape)
     assert off[worst] <= 0, (at[worst], got[worst], want[worst], room[worst])
     assert np.isfinite(got).all()
+
+
+# ------------------------------------------------------------------------------ a few rows, many column blocks
+
+@pytest.mark.parametrize("R,rows_per_x,E,N,K", [
+    # two blocks of columns a workgroup (384 to 767 blocks): the last workgroup has one of them, or eight columns
+    (1, 1, 1, 6152, 528), (5, 1, 1, 6168, 1040), (8, 8, 64, 888, 2064), (9, 1, 1, 8200, 4080),
+    # four blocks (768 and more): one to four of them in the last
+    (1, 1, 1, 12296, 48), (20, 1, 1, 16408, 528), (32, 2, 32, 408, 1040), (17, 1, 1, 12312, 2064), (48, 4, 16, 792, 4080),
+    (7, 1, 1, 12328, 4096),
+    # K beyond what is at once: one block a workgroup, in turns
+    (3, 1, 1, 12296, 4112), (40, 2, 8, 1544, 4112)])
+@pytest.mark.parametrize("out_dt", [F32, BF16])
+def test_gemv_blocks(R, rows_per_x, E, N, K, out_dt):
+    """More than 16 rows on one expert too, rows of other ranks' experts, and nothing behind the rows written."""
+    say(f"gemv blocks R={R} E={E} N={N} K={K} out={out_dt}")
+    rows, e0 = R // rows_per_x, 3 if E > 1 else 0
+    xq, wq, xs, ws = codes((rows, K), 1), codes((E, N, K), 2), scales(rows, 3), scales((E, N), 4)
+    e = None
+    if E > 1:
+        e = rng(5).integers(e0, e0 + E, R).astype(np.int32)
+        e[:min(R - 2, 21)] = e0 + E // 2                   # (21 rows on one expert: more than one turn of 16)
+        e[R // 2], e[R - 1] = e0 + E, e0 - 1
+    guard = 64
+    out = torch.full((guard + R * N + guard,), float("nan"), dtype=TORCH[out_dt], device="cuda")
+    args = (dev(xq), dev(xs), None if e is None else dev(e), dev(wq), dev(ws))
+    hocf.check(hocf.hocf_gemv_i8(R, rows_per_x, E, e0, N, K, out_dt, *args, out[guard:guard + R * N], hocf.sync(1, None, 0),
+                                 torch.cuda.current_stream()))
+    torch.cuda.synchronize()
+    assert out[:guard].isnan().all() and out[-guard:].isnan().all()
+    want = np.zeros((R, N))
+    for r in range(R):
+        at = 0 if e is None else int(e[r]) - e0
+        if 0 <= at < E:
+            i = r // rows_per_x
+            want[r] = ref.gemm(xq[i:i + 1], xs[i:i + 1], wq[at:at + 1], ws[at:at + 1])[0]
+    near(out[guard:guard + R * N].view(R, N), want, np.abs(want), TORCH[out_dt], GEMM_STEPS)
