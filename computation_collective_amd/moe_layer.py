@@ -152,7 +152,8 @@ class ExpertsI8:
     y = silu(x w_up) w_down for the rows of each group, in 8-bit integers.
 
     forward(x [rows][K] bf16, offsets [E + 1] int64 on the GPU) -> y [rows][K] bf16; group e is
-    rows [offsets[e], offsets[e + 1]), as the dispatch leaves them.  backward(dy) -> (dx
+    rows [offsets[e], offsets[e + 1]), as the dispatch leaves them (hocf_a2a_gemm's recv and offsets;
+    its padding rows are zeros, and take any dy that is finite).  backward(dy) -> (dx
     [rows][K] bf16, dw_up [E][K][H] fp32, dw_down [E][H][K] fp32), from the codes of the last
     forward().  Rows of no group are not written: y and dx hold there what an earlier step left,
     zeros at first.  requantise() takes the weights'
@@ -192,9 +193,20 @@ class ExpertsI8:
         self.w_up.run()
         self.w_down.run()
 
+    @staticmethod
+    def _take(into, name, t):
+        """`t` into the layer's own tensor: bf16 bit patterns, as the dispatch's rows are, count as bf16."""
+        if tuple(t.shape) != tuple(into.shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(into.shape)}")
+        if into.dtype == torch.bfloat16 and t.dtype == torch.int16:
+            t = t.view(torch.bfloat16)
+        if t.is_floating_point() != into.is_floating_point():
+            raise TypeError(f"{name} is {t.dtype}, not {into.dtype}")
+        into.copy_(t)
+
     def forward(self, x, offsets):
-        self.x.copy_(x)
-        self.offsets.copy_(offsets)
+        self._take(self.x, "x", x)
+        self._take(self.offsets, "offsets", offsets)
         return self.experts()
 
     def experts(self):
@@ -206,7 +218,7 @@ class ExpertsI8:
         return self.down.out.view(torch.bfloat16)
 
     def backward(self, dy):
-        self.dy.copy_(dy)
+        self._take(self.dy, "dy", dy)
         self.dw_down.run()
         self.dh.run()
         self.dw_up.run()

@@ -1,7 +1,7 @@
 """The 8-bit integer operators on the GPU where test_gpu_i8.py does not reach:
 every bf16 number through SiLU, SiLU in every form of the kernel, offsets that
-fall over three groups and more, SiLU's derivative far from zero, and the
-decode products' forms of several blocks of columns."""
+fall over three groups and more, SiLU's derivative far from zero, the decode
+products' forms of several blocks of columns, and the layer behind a dispatch."""
 
 import numpy as np
 import pytest
@@ -10,7 +10,8 @@ import torch
 import i8_ref as ref
 from computation_collective_amd import buffers as bf
 from computation_collective_amd import hocf
-from test_gpu_i8 import BAD_INDEX, BF16, F32, GEMM_STEPS, SILU, TORCH, check_rows, codes, dev, rng, same, scales
+from computation_collective_amd import moe_layer
+from test_gpu_i8 import BAD_INDEX, BF16, F32, GEMM_STEPS, SILU, TORCH, check_rows, codes, dev, normal, plain_experts, rng, same, scales
 from test_gpu_moe import host, near, run, say
 
 pytestmark = pytest.mark.gpu
@@ -214,3 +215,52 @@ def test_gemv_blocks(R, rows_per_x, E, N, K, out_dt):
             i = r // rows_per_x
             want[r] = ref.gemm(xq[i:i + 1], xs[i:i + 1], wq[at:at + 1], ws[at:at + 1])[0]
     near(out[guard:guard + R * N].view(R, N), want, np.abs(want), TORCH[out_dt], GEMM_STEPS)
+
+
+# ------------------------------------------------------------------------------ the layer behind a dispatch
+
+def test_experts_take_what_the_dispatch_leaves():
+    """hocf_a2a_gemm's received rows (bit patterns, padded with zero rows to 256 a group, NaN behind the last) and offsets go
+    into the layer as they are; near the layer without codes, and the same as from the rows as bfloat16."""
+    say("experts behind a dispatch")
+    P, E, B, topk, K, H, cap = 2, 3, 60, 2, 128, 256, 1100
+    n = P * E
+    w_up, w_down = normal((E, K, H), 1, K ** -0.5), normal((E, H, K), 2, H ** -0.5)
+    X = normal((P, B, K), 3)
+    chosen = np.stack([rng(4 + p).permuted(np.tile(np.arange(n), (B, 1)), axis=1)[:, :topk] for p in range(P)]).astype(np.int32)
+    d = bf.A2aGemm(P, E, E, B, topk, H, K, BF16, X, dev(chosen), w_up, cap)
+    d.poison()
+    d.run()
+    layer = moe_layer.ExpertsI8(E, cap, w_up, w_down)
+    dy = normal((cap, K), 5)
+    got = [layer.forward(d.recv, d.offsets).clone()] + [t.clone() for t in layer.backward(dy.view(torch.int16))]
+    layer.check()
+    off = d.offsets.tolist()
+    assert off[0] == 0 and 512 <= off[-1] <= 768 and off[-1] % 256 == 0
+    x = d.recv.view(torch.bfloat16).clone()
+    again = [layer.forward(x, d.offsets), *layer.backward(dy)]
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    x[off[-1]:] = 0
+    # (8 %: the bound of the layer's own test)
+    for a, b in zip(got, plain_experts(x, w_up, w_down, dy, off)):
+        a, b = host(a), b.numpy()
+        assert np.linalg.norm(a - b) < 0.08 * np.linalg.norm(b)
+
+
+def test_experts_refuse_other_shapes():
+    say("experts' refusals")
+    layer = moe_layer.ExpertsI8(2, 64, normal((2, 32, 48), 1), normal((2, 48, 32), 2))
+    x, off = normal((64, 32), 3), torch.tensor([0, 30, 64], device="cuda")
+    want = layer.forward(x, off).clone()
+    for bad in (x[:1], x[0], x[:63], x[:, :16]):
+        with pytest.raises(ValueError, match="x has shape"):
+            layer.forward(bad, off)
+        with pytest.raises(ValueError, match="dy has shape"):
+            layer.backward(bad)
+    for bad in (off[:2], off[:1], off[0]):
+        with pytest.raises(ValueError, match="offsets"):
+            layer.forward(x, bad)
+    for a, o in ((x.int(), off), (x, off.float())):
+        with pytest.raises(TypeError):
+            layer.forward(a, o)
+    assert torch.equal(layer.forward(x, off.int()), want) and torch.equal(layer.forward(x.float(), off), want)
