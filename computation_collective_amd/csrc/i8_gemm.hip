@@ -6,9 +6,9 @@
 // matrix instruction takes them (16 bytes a lane), so a tile's stages go
 // straight from memory to LDS and from there to the instruction.
 //
-// Bound by the matrix instructions and by what issues beside them: 8192^3 427 us (2.57 POP/s,
-// where the instruction alone on such numbers reaches 3.95), 8192 x 4096 -> 1792 67-69 us (224 of 256 CUs have a
-// tile; the first loads and the stores are about 12 us of it).
+// Bound by the matrix instructions and by what issues beside them: 8192^3 427-439 us (2.5 POP/s,
+// where the instruction alone on such numbers reaches 3.95), 8192 x 4096 -> 1792 57-69 us, by the card (224 of 256 CUs
+// have a tile; the first loads and the stores are about 12 us of it).
 #include "i8_tiles.hpp"
 #include "mfma_tile.hpp"
 #include "publish.hpp"

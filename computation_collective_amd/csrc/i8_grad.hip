@@ -13,8 +13,8 @@
 //
 // Bound by the matrix instructions and by what issues beside them: of a step's 3340 cycles (256 x
 // 256, dx) 2048 multiply, some 300 go to LDS reads, conversions and barriers, and about 50 to each of the
-// 18 loads, for which a wave holds its matrix pipe.  8192 rows, 4096 -> 1792: dx 127 us, through SiLU 150, dw
-// (fp32) 144 as one matrix in two parts.
+// 18 loads, for which a wave holds its matrix pipe.  8192 rows, 4096 -> 1792: dx 114-127 us, through SiLU 25 more, dw (fp32)
+// 130-144 as one matrix in two parts (one card and another).
 #include "i8_tiles.hpp"
 
 namespace hocf {

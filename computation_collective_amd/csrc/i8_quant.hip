@@ -13,7 +13,7 @@
 // A row stays in registers between its largest number and its codes: read once.
 // Bound by memory (8192 x 4096 bf16 20 us, 5.0 TB/s; reading 32768 x 1792 back 27 us,
 // 6.4 TB/s with codes from the Infinity Cache), but for SiLU with both sides kept, whose
-// vector instructions take as long (32768 x 1792: 56 us where memory would take 49).
+// vector instructions take as long (32768 x 1792: 49-58 us where memory would take 49).
 #include <algorithm>
 
 #include "i8.hpp"
@@ -272,8 +272,8 @@ template <int DT, int ACT, bool KEEP>
 static int launch_act(const QuantI8Args& a, hipStream_t s) {
   if (a.T >= 2048 && a.K <= 4096) {
     // Half a wave a row where a whole one's last pass would be half empty, and what bounds the kernel is
-    // vector instructions (bf16, SiLU with both sides, whole -> half a wave: 65536 x 768 53 -> 42 us,
-    // 32768 x 1792 51 -> 47; 65536 x 256 without SiLU 18 -> 13).  Longer rows without SiLU are bound by
+    // vector instructions (bf16, SiLU with both sides, whole -> half a wave: 65536 x 768 55 -> 44 us,
+    // 32768 x 1792 53 -> 49; 65536 x 256 without SiLU 18 -> 12).  Longer rows without SiLU are bound by
     // memory (32768 x 1792 32 -> 34), and of few a lane's time counts (2048 x 1792 6.8 -> 7.7).
     const bool half = a.K % 512 && a.K % 512 <= 256;
     if (half && a.K <= 1024) return launch_q<DT, ACT, KEEP, 1, 4, false, true>(a, s);

@@ -330,7 +330,7 @@ def main(argv=None):
     x, dy = normal(rows, K), normal(rows, K)
     experts.backward(experts.forward(x, off))
     experts.check()
-    print(f"one rank's {E} experts in 8-bit integers, {pairs * P} rows {K} -> {H} -> {K}: "
+    print(f"one rank's {E} experts in 8-bit integers, {pairs * P} rows (of {rows} in its buffers) {K} -> {H} -> {K}: "
           f"forward {_timed(lambda: experts.forward(x, off), a.steps):.3f} ms, "
           f"backward {_timed(lambda: experts.backward(dy), a.steps):.3f} ms, "
           f"weights to codes {_timed(experts.requantise, a.steps):.3f} ms")

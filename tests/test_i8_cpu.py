@@ -180,3 +180,13 @@ def test_handles_refuse():
     with pytest.raises(ValueError, match="4 or 8"):
         from computation_collective_amd import moe_layer
         moe_layer.MoeDecode(1, 4, 2, x, None, None, 64, 64, bits=2)
+
+
+def test_sums_in_parts_need_their_workspace():
+    """dw of few tiles and many rows takes its sums in parts through the workspace: none, or one byte too few, is refused."""
+    T, N, K = 9000, 64, 128
+    need = hocf.hocf_gemm_i8_dw_workspace_bytes(2, T, N, K)
+    assert need == 4 * 2 * N * K * 4
+    for s in (sync(ws=0, nbytes=0), sync(ws=0, nbytes=need), sync(nbytes=need - 1)):
+        assert call("gemm_i8_dw", T=T, s=s) == INVALID
+    valid(call("gemm_i8_dw", T=T, s=sync(nbytes=need)))
